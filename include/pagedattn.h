@@ -561,6 +561,172 @@ int pa_chunked_prefill_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_
                             size_t workspace_bytes, pa_dtype dtype, void* stream);
 
 /*
+ * Draft trees (speculative decoding). A step offers every sequence a tree of
+ * drafted tokens instead of one new token ("Speculative decoding": Medusa,
+ * EAGLE and n-gram drafts, in the vLLM architecture page's section on V1
+ * features); the target scores the whole tree at once, the drafts that agree
+ * with it are kept, and their K/V rows stay in the cache. The three calls
+ * below are one step's: write the nodes' K/V with pa_reshape_and_cache (or
+ * its 8-bit forms) at positions ctx .. ctx + nodes - 1, attend with
+ * pa_decode_tree in every layer, choose with pa_verify_tree, and move the
+ * kept rows together with pa_compact_tree.
+ *
+ * Trees are given as parents, ragged over the batch:
+ *   cu_q_lens : int32 [num_seqs+1]; sequence i owns the nodes (rows of q, of
+ *               the probabilities, ...) cu_q_lens[i] .. cu_q_lens[i+1]-1; none
+ *               is allowed (a sequence that sits the step out)
+ *   parents   : int32 [total_q]; the parent of each node as a node number
+ *               within its sequence, lower than the node's own; -1 for a
+ *               root. Node 0 is the newest committed token.
+ * A sequence has at most max_q_len nodes, and max_q_len at most 1024
+ * (PA_ERR_UNSUPPORTED).
+ */
+
+/*
+ * pa_decode_tree - attention of tree nodes over the paged context. Node j of
+ * sequence i sits in the cache at position ctx_lens[i] + j and attends to
+ * keys 0 .. ctx_lens[i]-1, to itself and to its ancestors, and to nothing
+ * else: whatever the K/V rows of other branches or of the positions behind
+ * the tree hold (infinities and NaN included) does not reach it.
+ *   q          : [total_q][num_q_heads][head_dim]
+ *   ctx_lens   : int32 [num_seqs]; committed tokens before the tree (>= 0)
+ *   max_q_len, max_kv_len : host upper bounds of the nodes and of ctx + nodes
+ *                of a sequence; a sequence above them, or with a cu_q_lens
+ *                that falls or leaves [0, total_q], records PA_ERR_SEQLEN and
+ *                its rows are not written
+ *   out        : [total_q][num_q_heads][head_dim]
+ *   workspace  : pa_decode_tree_workspace_size() bytes, 16-byte aligned, no
+ *                initialisation needed; not shared by calls that overlap. Its
+ *                size depends on the device's SM count, not on the lengths.
+ * A parent that is not below its node records PA_ERR_ARG (the node then
+ * counts as a root). fp16/bf16: head_dim 64 or 128, a GQA group of at most
+ * 128 and scale > 0 (PA_ERR_UNSUPPORTED, PA_ERR_ARG otherwise); the softmax
+ * weights are rounded to the 16-bit type for the second product, as in
+ * pa_decode. fp32: head_dim a multiple of 32 up to 256, exact fp32
+ * arithmetic, any finite scale. Rows are computed from their own sequence
+ * alone; results do not depend on the order in which the device runs.
+ */
+size_t pa_decode_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t block_size, int32_t total_q, int32_t max_q_len, int32_t max_kv_len,
+                                     pa_dtype dtype);
+int pa_decode_tree(const void* q, int32_t total_q, const int32_t* cu_q_lens, const int32_t* parents,
+                   const void* k_cache, const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                   const int32_t* ctx_lens, int32_t num_seqs, int32_t max_q_len, int32_t max_kv_len,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                   int32_t num_blocks, float scale, void* out, void* workspace, size_t workspace_bytes,
+                   pa_dtype dtype, void* stream);
+
+/* pa_decode_tree_fp8, pa_decode_tree_e5m2 - pa_decode_tree over the 8-bit
+ * pools (kv_scales as for pa_decode_fp8, 16-byte aligned). q/out fp16 or bf16
+ * (else PA_ERR_DTYPE), head_dim 128 (else PA_ERR_UNSUPPORTED). */
+int pa_decode_tree_fp8(const void* q, int32_t total_q, const int32_t* cu_q_lens, const int32_t* parents,
+                       const void* k_cache, const void* v_cache, const float* kv_scales, const int32_t* block_tables,
+                       int32_t max_blocks_per_seq, const int32_t* ctx_lens, int32_t num_seqs, int32_t max_q_len,
+                       int32_t max_kv_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, int32_t num_blocks, float scale, void* out, void* workspace,
+                       size_t workspace_bytes, pa_dtype dtype, void* stream);
+int pa_decode_tree_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_lens, const int32_t* parents,
+                        const void* k_cache, const void* v_cache, const float* kv_scales,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* ctx_lens,
+                        int32_t num_seqs, int32_t max_q_len, int32_t max_kv_len, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                        void* out, void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream);
+
+/*
+ * pa_verify_tree - which drafted tokens are kept, and the token after them,
+ * so that the kept tokens and the next one are distributed as the target
+ * alone would draw them (speculative sampling).
+ *   target_probs : [total_q][vocab_size] of dtype, rows target_stride elements
+ *                  apart; row r: the target's distribution of the token after
+ *                  node r
+ *   draft_probs  : the same for the draft (draft_stride): row r is the
+ *                  distribution that the children of node r were drawn from,
+ *                  independently; or NULL: the children were chosen, not
+ *                  drawn (a lookup, the likeliest few)
+ *   draft_tokens : int32 [total_q]; the token of each node (a root's is not
+ *                  read). A node whose token lies outside [0, vocab_size) is
+ *                  padding: never kept.
+ *   uniform_accept : float [total_q], uniform_sample : float [num_seqs];
+ *                  random numbers in [0, 1), one for each node and sequence
+ *   path         : int32 [num_seqs][max_path_len] (output): the kept nodes
+ *                  from node 0 down, then -1
+ *   path_lens    : int32 [num_seqs] (output): kept nodes; at least 1 (node 0)
+ *                  unless the sequence has no nodes
+ *   next_tokens  : int32 [num_seqs] (output): the token drawn at the last kept
+ *                  node; -1 for a sequence without nodes
+ * From node 0 on, the children of the last kept node are tried in node order.
+ * With its target row p, draft row q, w = p and S = 1, child c with token x
+ * is kept if uniform_accept[c] * q(x) * S < w(x); otherwise w becomes
+ * max(0, w - S q) and S the sum of w, and the next child is tried. Without
+ * draft_probs child c is kept if uniform_accept[c] * S < w(x); otherwise S
+ * drops by w(x) and w(x) becomes 0. Where no child is kept (or the path is
+ * full: then none is tried) the next token is the smallest y with
+ * w(0) + .. + w(y) > uniform_sample * sum(w); if every w is 0, w = p is used.
+ * Probabilities outside [0, 1] are held to it and NaN counts as 0; a row
+ * without any probability gives next token -1 and PA_ERR_ARG. Sums are taken
+ * over weights rounded to multiples of 2^-45, exactly, so results do not
+ * depend on the order in which the device runs. A sequence whose cu_q_lens
+ * falls, leaves [0, total_q] or has more than max_q_len nodes records
+ * PA_ERR_SEQLEN, one with a parent that is not below its node (or a node 0
+ * that is no root) PA_ERR_ARG; both get path_lens 0 and next token -1.
+ * vocab_size is at most 262144, max_path_len at least 1. Rows need no
+ * alignment beyond their element's.
+ */
+int pa_verify_tree(const void* target_probs, int64_t target_stride, const void* draft_probs, int64_t draft_stride,
+                   const int32_t* draft_tokens, const int32_t* cu_q_lens, const int32_t* parents,
+                   const float* uniform_accept, const float* uniform_sample, int32_t num_seqs, int32_t total_q,
+                   int32_t max_q_len, int32_t vocab_size, int32_t max_path_len, int32_t* path, int32_t* path_lens,
+                   int32_t* next_tokens, pa_dtype dtype, void* stream);
+
+/*
+ * pa_compact_tree - moves the kept nodes' K/V rows together: in every layer,
+ * for k < path_lens[i], the rows of position ctx_lens[i] + path[i][k] go to
+ * position ctx_lens[i] + k, as if all were read before any is written. The
+ * sequence then has ctx_lens[i] + path_lens[i] cached tokens.
+ *   k_caches, v_caches : HOST arrays of num_layers device pointers, the pools
+ *                  of each layer (same shape; one block table serves them
+ *                  all); read before the call returns
+ *   path, path_lens : int32 device, as pa_verify_tree writes them; any
+ *                  strictly rising path of nodes >= 0 will do, and length 0.
+ *                  max_path_len at most 1024.
+ * Bit-exact; every other row stays as it is. The blocks written must be the
+ * sequence's own (copy shared ones first). head_dim * sizeof(dtype) must be a
+ * multiple of 16. A sequence with a negative context, a length outside
+ * [0, max_path_len] or a position past its block table records
+ * PA_ERR_SEQLEN, a path that does not rise PA_ERR_ARG, a block outside the
+ * pool PA_ERR_BLOCK_OOB; nothing of it is moved.
+ */
+int pa_compact_tree(void* const* k_caches, void* const* v_caches, int32_t num_layers, const int32_t* block_tables,
+                    int32_t max_blocks_per_seq, const int32_t* ctx_lens, const int32_t* path,
+                    const int32_t* path_lens, int32_t num_seqs, int32_t max_path_len, int32_t num_blocks,
+                    int32_t block_size, int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype, void* stream);
+
+/*
+ * pa_compact_tree_fp8, pa_compact_tree_e5m2 - the same over 8-bit pools.
+ *   kv_scales : HOST array of num_layers device pointers, float32
+ *               [num_blocks][num_kv_heads][2] each
+ * Scale rule, per (block, KV head, pool) that rows land in: with o the offset
+ * of the first of them, s_new = the largest of the landing rows' scales (their
+ * source blocks', before the call) and, if o > 0, the block's own; codes at
+ * offsets below o are re-encoded by fl32(s_old / s_new) if s_new > s_old > 0,
+ * as a cache write does; a landing row whose scale is s_new keeps its codes,
+ * another is encoded as code(fl32(value * fl32(s_source / s_new))). Codes at
+ * offsets above the landing rows are untouched (their scale may not be: the
+ * rows of dropped nodes hold no meaning any more). head_dim 64 or 128
+ * (PA_ERR_UNSUPPORTED).
+ */
+int pa_compact_tree_fp8(void* const* k_caches, void* const* v_caches, float* const* kv_scales, int32_t num_layers,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* ctx_lens,
+                        const int32_t* path, const int32_t* path_lens, int32_t num_seqs, int32_t max_path_len,
+                        int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                        void* stream);
+int pa_compact_tree_e5m2(void* const* k_caches, void* const* v_caches, float* const* kv_scales, int32_t num_layers,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* ctx_lens,
+                         const int32_t* path, const int32_t* path_lens, int32_t num_seqs, int32_t max_path_len,
+                         int32_t num_blocks, int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                         void* stream);
+
+/*
  * pa_selftest_bounded_wait — exercises the failure path every kernel relies
  * on: one warp waits on an mbarrier that nothing completes; the wait gives up
  * after limit_ns nanoseconds of device time (1 us .. 1 s, else PA_ERR_ARG),

@@ -30,7 +30,8 @@ EXPORTS = (
     "pa_reshape_and_cache_fp8", "pa_copy_blocks_fp8", "pa_decode_fp8", "pa_swap_blocks",
     "pa_decode_step_shared_prefix", "pa_decode_step", "pa_selftest_bounded_wait", "pa_decode_shared_prefix_fp8",
     "pa_chunked_prefill_fp8", "pa_reshape_and_cache_e5m2", "pa_decode_e5m2", "pa_decode_shared_prefix_e5m2",
-    "pa_chunked_prefill_e5m2",
+    "pa_chunked_prefill_e5m2", "pa_decode_tree_workspace_size", "pa_decode_tree", "pa_decode_tree_fp8",
+    "pa_decode_tree_e5m2", "pa_verify_tree", "pa_compact_tree", "pa_compact_tree_fp8", "pa_compact_tree_e5m2",
 )
 
 _i32, _i64, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
@@ -95,7 +96,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                   _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _sz, ctypes.c_int,
                                                   _vp]),
     }
-    for name in ("reshape_and_cache", "decode", "decode_shared_prefix", "chunked_prefill"):
+    sig.update({
+        "pa_decode_tree_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_int]),
+        "pa_decode_tree": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                          _i32, _i32, _i32, _i32, _f32, _vp, _vp, _sz, ctypes.c_int, _vp]),
+        "pa_decode_tree_fp8": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                                              _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _sz, ctypes.c_int, _vp]),
+        "pa_verify_tree": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                          _i32, _vp, _vp, _vp, ctypes.c_int, _vp]),
+        "pa_compact_tree": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                           _i32, ctypes.c_int, _vp]),
+        "pa_compact_tree_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32,
+                                               _i32, _i32, _i32, _vp]),
+    })
+    for name in ("reshape_and_cache", "decode", "decode_shared_prefix", "chunked_prefill", "decode_tree",
+                 "compact_tree"):
         sig[f"pa_{name}_e5m2"] = sig[f"pa_{name}_fp8"]  # same arguments, e5m2 codes
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -567,3 +582,211 @@ def pa_swap_blocks(src_k: torch.Tensor, src_v: torch.Tensor | None, dst_k: torch
         pairs.ctypes.data_as(ctypes.c_void_p), pairs.shape[0], src_k.shape[0], dst_k.shape[0], block_bytes,
         _stream(stream))
     _check(rc, "pa_swap_blocks")
+
+
+# ---------------------------------------------------------------------------
+# Draft trees: attention, verification, compaction of the kept path.
+# ---------------------------------------------------------------------------
+
+def _cuda_here(t, name: str, dtype=None) -> int:
+    """_cuda() of a tensor on the current device: the calls launch there."""
+    p = _cuda(t, name, dtype)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return p
+
+
+def _scratch(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that a call on `stream` may use: its memory is not handed out
+    again before that stream is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    h = _stream(stream)
+    if h != torch.cuda.current_stream().cuda_stream:
+        t.record_stream(torch.cuda.ExternalStream(h))
+    return t
+
+
+def _shape(t, name: str, *dims) -> None:
+    """Check t's dimensions (None: any)."""
+    if t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims}")
+
+
+def _dtype_code(t, name: str) -> int:
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return _DT[t.dtype]
+
+
+def pa_decode_tree_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                                  total_q: int, max_q_len: int, max_kv_len: int,
+                                  dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(load().pa_decode_tree_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, total_q,
+                                                    max_q_len, max_kv_len, _DT[dtype]))
+
+
+def pa_decode_tree(q: torch.Tensor, cu_q_lens: torch.Tensor, parents: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, block_tables: torch.Tensor, ctx_lens: torch.Tensor, max_q_len: int,
+                   max_kv_len: int, scale: float, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of every sequence's tree nodes (rows of q) over its paged context."""
+    return _decode_tree("pa_decode_tree", q, cu_q_lens, parents, k_cache, v_cache, None, block_tables, ctx_lens,
+                        max_q_len, max_kv_len, scale, out, workspace, stream)
+
+
+def pa_decode_tree_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor, parents: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, kv_scales: torch.Tensor, block_tables: torch.Tensor,
+                       ctx_lens: torch.Tensor, max_q_len: int, max_kv_len: int, scale: float,
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    return _decode_tree("pa_decode_tree_fp8", q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_tables,
+                        ctx_lens, max_q_len, max_kv_len, scale, out, workspace, stream)
+
+
+def pa_decode_tree_e5m2(q: torch.Tensor, cu_q_lens: torch.Tensor, parents: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, kv_scales: torch.Tensor, block_tables: torch.Tensor,
+                        ctx_lens: torch.Tensor, max_q_len: int, max_kv_len: int, scale: float,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    return _decode_tree("pa_decode_tree_e5m2", q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_tables,
+                        ctx_lens, max_q_len, max_kv_len, scale, out, workspace, stream)
+
+
+def _decode_tree(sym, q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_tables, ctx_lens, max_q_len,
+                 max_kv_len, scale, out, workspace, stream) -> torch.Tensor:
+    T, hq, D = q.shape
+    P, hkv, B, _ = k_cache.shape
+    n = ctx_lens.shape[0]
+    dt = q.dtype
+    code = _dtype_code(q, "q")
+    kv = dt if kv_scales is None else torch.uint8
+    _shape(k_cache, "k_cache", P, hkv, B, D)
+    _shape(v_cache, "v_cache", P, hkv, B, D)
+    _shape(cu_q_lens, "cu_q_lens", n + 1)
+    _shape(parents, "parents", T)
+    _shape(block_tables, "block_tables", n, None)
+    if out is None:
+        out = _scratch((T, hq, D), dt, q.device, stream)
+    _shape(out, "out", T, hq, D)
+    if workspace is None:
+        need = pa_decode_tree_workspace_size(n, hq, hkv, D, B, T, max_q_len, max_kv_len, dt)
+        workspace = _scratch(max(need, 16), torch.uint8, q.device, stream)
+    scales = ()
+    if kv_scales is not None:
+        _shape(kv_scales, "kv_scales", P, hkv, 2)
+        scales = (_cuda_here(kv_scales, "kv_scales", torch.float32),)
+    rc = getattr(load(), sym)(
+        _cuda_here(q, "q"), T, _cuda_here(cu_q_lens, "cu_q_lens", torch.int32),
+        _cuda_here(parents, "parents", torch.int32), _cuda_here(k_cache, "k_cache", kv),
+        _cuda_here(v_cache, "v_cache", kv), *scales, _cuda_here(block_tables, "block_tables", torch.int32),
+        block_tables.shape[1], _cuda_here(ctx_lens, "ctx_lens", torch.int32), n, int(max_q_len), int(max_kv_len), hq,
+        hkv, D, B, P, float(scale), _cuda_here(out, "out", dt), _cuda_here(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), code, _stream(stream))
+    _check(rc, sym)
+    return out
+
+
+def _rows(t, name: str, dtype, rows: int, cols: int) -> tuple[int, int]:
+    """Pointer and row stride (elements) of a [rows, cols] CUDA tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    _shape(t, name, rows, cols)
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows must be contiguous and not overlap")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr(), max(t.stride(0), cols)
+
+
+def pa_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
+                   cu_q_lens: torch.Tensor, parents: torch.Tensor, uniform_accept: torch.Tensor,
+                   uniform_sample: torch.Tensor, max_q_len: int, max_path_len: int, path: torch.Tensor | None = None,
+                   path_lens: torch.Tensor | None = None, next_tokens: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Keep drafted tokens and draw the next one: (path, path_lens, next_tokens).
+    target_probs, draft_probs: [total_q, vocab]; rows may be padded apart."""
+    T, V = target_probs.shape
+    n = uniform_sample.shape[0]
+    dev = target_probs.device
+    code = _dtype_code(target_probs, "target_probs")
+    tp, ts = _rows(target_probs, "target_probs", target_probs.dtype, T, V)
+    dp, ds = (None, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", target_probs.dtype, T, V)
+    _shape(cu_q_lens, "cu_q_lens", n + 1)
+    for t, name in ((parents, "parents"), (draft_tokens, "draft_tokens"), (uniform_accept, "uniform_accept")):
+        _shape(t, name, T)
+    if path is None:
+        path = _scratch((n, max_path_len), torch.int32, dev, stream)
+    if path_lens is None:
+        path_lens = _scratch(n, torch.int32, dev, stream)
+    if next_tokens is None:
+        next_tokens = _scratch(n, torch.int32, dev, stream)
+    _shape(path, "path", n, max_path_len)
+    _shape(path_lens, "path_lens", n)
+    _shape(next_tokens, "next_tokens", n)
+    rc = load().pa_verify_tree(
+        tp, ts, dp, ds, _cuda_here(draft_tokens, "draft_tokens", torch.int32),
+        _cuda_here(cu_q_lens, "cu_q_lens", torch.int32), _cuda_here(parents, "parents", torch.int32),
+        _cuda_here(uniform_accept, "uniform_accept", torch.float32),
+        _cuda_here(uniform_sample, "uniform_sample", torch.float32), n, T, int(max_q_len), V, int(max_path_len),
+        _cuda_here(path, "path", torch.int32), _cuda_here(path_lens, "path_lens", torch.int32),
+        _cuda_here(next_tokens, "next_tokens", torch.int32), code, _stream(stream))
+    _check(rc, "pa_verify_tree")
+    return path, path_lens, next_tokens
+
+
+def pa_compact_tree(k_caches, v_caches, block_tables: torch.Tensor, ctx_lens: torch.Tensor, path: torch.Tensor,
+                    path_lens: torch.Tensor, stream=None) -> None:
+    """Move the kept nodes' K/V rows together in every layer. k_caches,
+    v_caches: one pool [blocks, Hkv, B, D] per layer."""
+    _compact_tree("pa_compact_tree", k_caches, v_caches, None, block_tables, ctx_lens, path, path_lens, stream)
+
+
+def pa_compact_tree_fp8(k_caches, v_caches, kv_scales, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
+                        path: torch.Tensor, path_lens: torch.Tensor, stream=None) -> None:
+    """pa_compact_tree over e4m3 pools; kv_scales: one [blocks, Hkv, 2] per layer."""
+    _compact_tree("pa_compact_tree_fp8", k_caches, v_caches, kv_scales, block_tables, ctx_lens, path, path_lens,
+                  stream)
+
+
+def pa_compact_tree_e5m2(k_caches, v_caches, kv_scales, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
+                         path: torch.Tensor, path_lens: torch.Tensor, stream=None) -> None:
+    """pa_compact_tree over e5m2 pools; kv_scales: one [blocks, Hkv, 2] per layer."""
+    _compact_tree("pa_compact_tree_e5m2", k_caches, v_caches, kv_scales, block_tables, ctx_lens, path, path_lens,
+                  stream)
+
+
+def _compact_tree(sym, k_caches, v_caches, kv_scales, block_tables, ctx_lens, path, path_lens, stream) -> None:
+    layers = len(k_caches)
+    if len(v_caches) != layers or (kv_scales is not None and len(kv_scales) != layers):
+        raise ValueError("k_caches, v_caches and kv_scales must list the same layers")
+    if layers == 0:
+        return
+    P, hkv, B, D = k_caches[0].shape
+    dt = torch.uint8 if kv_scales is not None else k_caches[0].dtype
+    code = () if kv_scales is not None else (_dtype_code(k_caches[0], "k_caches"),)
+    n = ctx_lens.shape[0]
+
+    def pointers(pools, name, dtype, *dims):
+        out = (ctypes.c_void_p * layers)()
+        here = torch.cuda.current_device()
+        for i, t in enumerate(pools):
+            if t.dtype != dtype or t.shape != dims or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {dtype} and shape {dims}")
+            if t.device.index != here:
+                raise ValueError(f"{name}[{i}] is on {t.device}, the current device is cuda:{here}")
+            out[i] = t.data_ptr()
+        return out
+
+    kp = pointers(k_caches, "k_caches", dt, P, hkv, B, D)
+    vp = pointers(v_caches, "v_caches", dt, P, hkv, B, D)
+    sp = () if kv_scales is None else (pointers(kv_scales, "kv_scales", torch.float32, P, hkv, 2),)
+    _shape(block_tables, "block_tables", n, None)
+    _shape(path, "path", n, None)
+    _shape(path_lens, "path_lens", n)
+    rc = getattr(load(), sym)(
+        kp, vp, *sp, layers, _cuda_here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
+        _cuda_here(ctx_lens, "ctx_lens", torch.int32), _cuda_here(path, "path", torch.int32),
+        _cuda_here(path_lens, "path_lens", torch.int32), n, path.shape[1], P, B, hkv, D, *code, _stream(stream))
+    _check(rc, sym)

@@ -1,0 +1,251 @@
+// Tree attention over the paged cache: parameters and the work split shared
+// by the tensor-core and the fp32 kernel.
+//
+// A unit is one (sequence, KV head, query tile): the tile's rows are (tree
+// node, query head of the group) pairs and its keys are the sequence's
+// ctx + nodes cached positions, cut into key tiles. The units of a batch,
+// sequence-major, form one line of key tiles, and CTA b of N takes the tiles
+// [W b / N, W (b + 1) / N) of it, so every CTA has the same work (to one
+// tile) whatever the lengths are. A CTA writes the units that lie wholly in
+// its range; of a unit that crosses a range border every CTA writes its
+// (m, l, o~) partial, and a second kernel joins them in CTA order. A CTA has
+// at most two such pieces: slot 2b holds the piece of a unit begun by an
+// earlier CTA, slot 2b + 1 that of a unit begun here. So the partials need
+// 2 N tiles whatever the batch is, and there is no plan kernel: every CTA
+// finds its place with a scan of the lengths.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+constexpr int kMaxTreeNodes = 1024;
+
+// Written by every CTA: the unit it began and did not finish.
+struct TreeMerge {
+  int32_t parts;   // pieces of the unit (0: nothing to join here)
+  int32_t q0;      // first row of the sequence in q / out
+  int32_t nodes;
+  int32_t kvh;
+  int32_t qt;
+  int32_t pad[3];
+};
+
+struct TreeParams {
+  const void* q;
+  void* out;
+  const void* k_cache;
+  const void* v_cache;
+  const float* kv_scales;  // 8-bit cache: (K, V) scale per (block, KV head); else nullptr
+  int32_t kv_fmt;
+  const int32_t* block_tables;
+  const int32_t* cu_q_lens;
+  const int32_t* parents;
+  const int32_t* ctx_lens;
+  int32_t max_blocks_per_seq;
+  int32_t num_seqs;
+  int32_t total_q;
+  int32_t max_q_len;
+  int32_t max_kv_len;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t group;
+  int32_t tile_rows;  // rows of a query tile in use: a multiple of the group, or any number (fp32)
+  int32_t tile_m;     // rows of a partial tile in the workspace
+  int32_t tile_keys;
+  int32_t min_tiles;  // a CTA takes at least this many key tiles, if there are any
+  float scale_log2;
+  TreeMerge* merge;   // [ctas]
+  float* part_o;      // [2 * ctas][tile_m][head_dim]
+  float* part_ml;     // [2 * ctas][tile_m][2]
+  int* status;
+};
+
+// Work of one sequence: key tiles and query tiles; 0 units for an empty or
+// illegal one.
+struct TreeSeq {
+  int q0, nodes, ctx, ktiles, qtiles;
+  __device__ __forceinline__ int64_t tiles(const TreeParams& p) const {
+    return (int64_t)ktiles * qtiles * p.num_kv_heads;
+  }
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int i, bool report) {
+  TreeSeq s;
+  s.q0 = p.cu_q_lens[i];
+  const int64_t n = (int64_t)p.cu_q_lens[i + 1] - s.q0;
+  s.ctx = p.ctx_lens[i];
+  s.nodes = 0;
+  s.ktiles = s.qtiles = 0;
+  const int64_t kv = s.ctx + n;
+  const int64_t cap = min((int64_t)p.max_kv_len, (int64_t)p.max_blocks_per_seq * p.block_size);
+  if (n == 0) return s;
+  if (n < 0 || s.q0 < 0 || s.q0 + n > p.total_q || n > p.max_q_len || s.ctx < 0 || kv > cap) {
+    if (report) record_error(p.status, PA_ERR_SEQLEN);
+    return s;
+  }
+  s.nodes = (int)n;
+  s.ktiles = (int)((kv + p.tile_keys - 1) / p.tile_keys);
+  s.qtiles = (int)((n * p.group + p.tile_rows - 1) / p.tile_rows);
+  return s;
+}
+
+// A CTA's place on the line of tiles.
+struct TreeRange {
+  int64_t begin;  // first tile of this CTA
+  int64_t left;   // tiles of this CTA
+  int64_t total;  // tiles of the batch
+  int ctas;       // CTAs that share it
+  int seq;        // sequence that holds the first tile, and the tile's place in it
+  int64_t off;
+};
+
+// The scan: threads 0 .. THREADS-1 of the CTA (all of them) sum the tiles of
+// a run of sequences each; the one whose run holds the CTA's first tile
+// walks it. `sm` is THREADS / 32 + 4 words of 8 bytes.
+template <int THREADS>
+__device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int per = (p.num_seqs + THREADS - 1) / THREADS;
+  const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) mine += tree_seq(p, s, blockIdx.x == 0).tiles(p);
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sm[w] = x;
+  __syncthreads();
+  int64_t base = x - mine, total = 0;
+  for (int i = 0; i < THREADS / 32; ++i) {
+    const int64_t t = sm[i];
+    if (i < w) base += t;
+    total += t;
+  }
+  TreeRange r;
+  r.total = total;
+  const int64_t most = (total + p.min_tiles - 1) / p.min_tiles;
+  r.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, most));
+  r.begin = 0;
+  r.left = 0;
+  r.seq = 0;
+  r.off = 0;
+  if ((int)blockIdx.x < r.ctas) {
+    r.begin = total * blockIdx.x / r.ctas;
+    r.left = total * (blockIdx.x + 1) / r.ctas - r.begin;
+  }
+  int64_t* found = sm + THREADS / 32;
+  if (r.left > 0 && r.begin >= base && r.begin < base + mine) {
+    int64_t at = base;
+    for (int s = s0; s < s1; ++s) {
+      const int64_t t = tree_seq(p, s, false).tiles(p);
+      if (r.begin < at + t) {
+        found[0] = s;
+        found[1] = r.begin - at;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  if (r.left > 0) {
+    r.seq = (int)found[0];
+    r.off = found[1];
+  }
+  return r;
+}
+
+// One piece of a unit: key tiles [t0, t1) of its ktiles.
+struct TreePiece {
+  TreeSeq s;
+  int seq, kvh, qt, t0, t1;
+  int64_t at;  // place of tile t0 on the line
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == s.ktiles; }
+  __device__ __forceinline__ int kv_len() const { return s.ctx + s.nodes; }
+};
+
+// Walks the pieces of a CTA's range. Every role of a CTA runs its own copy.
+struct TreeWalk {
+  TreeRange r;
+  int64_t at;
+  int seq;
+  int64_t off;  // place in the sequence
+  int64_t left;
+  __device__ __forceinline__ explicit TreeWalk(const TreeRange& range)
+      : r(range), at(range.begin), seq(range.seq), off(range.off), left(range.left) {}
+  __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& c) {
+    if (left <= 0) return false;
+    c.s = tree_seq(p, seq, false);
+    while (off >= c.s.tiles(p)) {  // also steps over sequences without work
+      off -= c.s.tiles(p);
+      c.s = tree_seq(p, ++seq, false);
+    }
+    c.seq = seq;
+    const int unit = (int)(off / c.s.ktiles);
+    c.t0 = (int)(off - (int64_t)unit * c.s.ktiles);
+    c.t1 = (int)min((int64_t)c.s.ktiles, c.t0 + left);
+    c.kvh = unit / c.s.qtiles;
+    c.qt = unit - c.kvh * c.s.qtiles;
+    c.at = at;
+    const int n = c.t1 - c.t0;
+    off += n;
+    at += n;
+    left -= n;
+    return true;
+  }
+};
+
+// Slot of a piece's partial, and what the join kernel needs of a unit begun here.
+__device__ __forceinline__ int tree_slot(const TreePiece& c) { return 2 * blockIdx.x + (c.t0 == 0 ? 1 : 0); }
+
+__device__ __forceinline__ void tree_note_merge(const TreeParams& p, const TreeRange& r, const TreePiece& c) {
+  // CTA of tile w: the b with floor(W b / N) <= w, the largest such b.
+  const int64_t last = c.at - c.t0 + c.s.ktiles - 1;
+  const int64_t e = ((last + 1) * r.ctas - 1) / r.total;
+  TreeMerge m;
+  m.parts = (int)(e - blockIdx.x + 1);
+  m.q0 = c.s.q0;
+  m.nodes = c.s.nodes;
+  m.kvh = c.kvh;
+  m.qt = c.qt;
+  m.pad[0] = m.pad[1] = m.pad[2] = 0;
+  p.merge[blockIdx.x] = m;
+}
+
+// Bits of the 32 nodes from `first` on that are `node` or its ancestors.
+// parents: the sequence's. A parent that is not below its node ends the walk
+// (reported by tree_check_parents).
+__device__ __forceinline__ uint32_t tree_ancestors(const int32_t* parents, int node, int first) {
+  uint32_t bits = 0;
+  while (node >= first && node >= 0) {
+    if (node < first + 32) bits |= 1u << (node - first);
+    const int up = __ldg(parents + node);
+    if (up >= node) break;
+    node = up;
+  }
+  return bits;
+}
+
+// Reports parents that are not below their node, once per sequence: by the
+// CTA with the last key tile of its first unit.
+template <int THREADS>
+__device__ __forceinline__ void tree_check_parents(const TreeParams& p, const TreePiece& c) {
+  if (c.kvh || c.qt || c.t1 != c.s.ktiles) return;
+  for (int j = threadIdx.x; j < c.s.nodes; j += THREADS) {
+    const int up = __ldg(p.parents + c.s.q0 + j);
+    if (up < -1 || up >= j) record_error(p.status, PA_ERR_ARG);
+  }
+}
+
+// The tensor-core kernel (fp16 / bf16 q; head_dim 64 or 128, 128 for 8-bit
+// caches), the fp32 kernel, and the join kernel behind either.
+int launch_tree_tc(const TreeParams& p, int ctas, pa_dtype dt, cudaStream_t stream);
+int launch_tree_simt(const TreeParams& p, int ctas, pa_dtype dt, cudaStream_t stream);
+
+}  // namespace pa

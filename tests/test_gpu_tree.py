@@ -1,0 +1,289 @@
+"""Tree attention over the paged cache against the fp64 oracle."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tree_helpers import assert_tree_close, tree_batch
+
+pytestmark = pytest.mark.gpu
+
+
+def run(lib, b, what="", **over):
+    got = b.call(lib, **over)
+    status = lib.pa_get_status()
+    assert status == 0, lib.pa_strerror(status)
+    assert_tree_close(b, got, what)
+    return got
+
+
+SHAPES = [
+    # dtype, kv, hq, hkv, d, block
+    ("f32", None, 2, 1, 64, 16),
+    ("f32", None, 12, 4, 96, 32),
+    ("f32", None, 4, 4, 256, 16),
+    ("f32", None, 80, 2, 32, 16),
+    ("bf16", None, 32, 8, 128, 16),
+    ("bf16", None, 64, 8, 128, 32),
+    ("f16", None, 8, 8, 64, 16),
+    ("f16", None, 28, 4, 128, 32),   # group 7: a tile's last rows are unused
+    ("bf16", None, 40, 2, 64, 32),   # group 20
+    ("bf16", None, 128, 1, 128, 16),  # group 128: one node a tile
+    ("bf16", "e4m3", 32, 8, 128, 16),
+    ("f16", "e4m3", 14, 2, 128, 32),
+    ("f16", "e5m2", 32, 4, 128, 16),
+    ("bf16", "e5m2", 8, 8, 128, 32),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+def test_ragged_batch(lib, shape):
+    dtype, kv, hq, hkv, d, block = shape
+    # Contexts and trees that end inside, at and behind tiles and blocks; no context; one node.
+    ctx = [0, 1, 15, 16, 63, 64, 100, 127, 128, 200, 500]
+    nodes = [1, 7, 1, 16, 1, 2, 33, 5, 64, 3, 17]
+    b = tree_batch(1, dtype, ctx, nodes, hq, hkv, d, block, kv)
+    run(lib, b, str(shape))
+
+
+@pytest.mark.parametrize("kind", ["chain", "star", "forest"])
+@pytest.mark.parametrize("dtype,kv,d", [("bf16", None, 128), ("f32", None, 64), ("f16", "e4m3", 128)])
+def test_tree_shapes(lib, kind, dtype, kv, d):
+    b = tree_batch(2, dtype, [70, 3, 129], [40, 31, 90], 8, 2, d, 16, kv, kind)
+    run(lib, b, kind)
+
+
+@pytest.mark.parametrize("nodes", [130, 257, 1024])
+def test_large_trees(lib, nodes):
+    run(lib, tree_batch(3, "bf16", [50], [nodes], 4, 2, 64, 16), "wide")
+
+
+def test_largest_chain(lib):
+    run(lib, tree_batch(4, "f16", [9], [1024], 2, 2, 64, 32, kind="chain"), "chain")
+
+
+@pytest.mark.parametrize("dtype,kv,d", [("bf16", None, 128), ("f16", None, 64), ("f32", None, 128),
+                                        ("bf16", "e4m3", 128), ("f16", "e5m2", 128)])
+def test_long_context_split_over_the_machine(lib, dtype, kv, d):
+    run(lib, tree_batch(5, dtype, [9000, 20], [6, 2], 8, 2, d, 16, kv), "long")
+
+
+@pytest.mark.parametrize("dtype,kv", [("bf16", None), ("f32", None), ("bf16", "e4m3")])
+def test_many_sequences(lib, dtype, kv):
+    rng = np.random.default_rng(6)
+    n = 700
+    run(lib, tree_batch(6, dtype, rng.integers(0, 90, n), rng.integers(0, 6, n), 4, 2, 128, 16, kv), "many")
+
+
+def test_sequences_without_nodes(lib):
+    b = tree_batch(7, "bf16", [40, 30, 20, 10, 5], [0, 5, 0, 0, 3], 8, 2, 128)
+    run(lib, b)
+    e = tree_batch(7, "bf16", [40, 30], [0, 0], 8, 2, 128)
+    assert e.call(lib).shape == (0, 8, 128)
+
+
+def test_chain_equals_causal_chunk(lib):
+    """A chain is a causal chunk: the chunked-prefill call is within both
+    kernels' roundings of the tree call."""
+    b = tree_batch(8, "bf16", [300, 17], [20, 9], 32, 8, 128, kind="chain")
+    got = run(lib, b)
+    a = b.device()
+    other = lib.pa_chunked_prefill(a["q"], a["cu_q_lens"], a["k_cache"], a["v_cache"], a["block_tables"],
+                                   a["ctx_lens"], a["max_q_len"], a["max_kv_len"], b.scale)
+    assert_tree_close(b, other, "chunk")
+    assert (got.float() - other.float()).abs().max() < 0.02
+
+
+def _masked_garbage(b, value, which="kv"):
+    """Fill every row that no node may read: the positions behind each
+    sequence's tree in its last block, and spare blocks."""
+    P, _, B, _ = b.k.shape
+    used = np.zeros((P, B), bool)
+    for i, (c, n) in enumerate(zip(b.ctx, b.counts)):
+        for pos in range(int(c) + int(n)):
+            used[b.table[i, pos // B], pos % B] = True
+    blk, off = np.nonzero(~used)
+    for x in (b.k, b.v):
+        x[blk, :, off] = value
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_behind_the_tree_do_not_matter(lib, dtype, value):
+    b = tree_batch(9, dtype, [0, 3, 60, 63, 100], [2, 5, 4, 9, 40], 8, 2, 64)
+    _masked_garbage(b, value)
+    run(lib, b)
+
+
+@pytest.mark.parametrize("kv,code", [("e4m3", 0x7F), ("e5m2", 0x7D), ("e5m2", 0x7C)])
+def test_codes_behind_the_tree_do_not_matter(lib, kv, code):
+    b = tree_batch(9, "bf16", [0, 3, 60, 63, 100], [2, 5, 4, 9, 40], 8, 2, 128, kv=kv)
+    _masked_garbage(b, code)
+    run(lib, b)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["k", "v", "one value"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("ctx", [50, 5000])
+def test_other_branches_do_not_matter(lib, dtype, where, value, ctx):
+    """A node whose K or V is not finite reaches its own subtree and no other
+    row: those are as if it held zeros, and rows below it are not finite where
+    the definition says so."""
+    nodes = 70
+    b = tree_batch(10, dtype, [ctx, 20], [nodes, 8], 8, 2, 128)
+    bad = [3, 40]
+    below = [j for j in range(nodes) if set(bad) & set(_up(b.parents[:nodes], j))]
+    at = [(b.table[0, (ctx + j) // 16], (ctx + j) % 16) for j in bad]
+    clean = b.call(lib).clone()
+    for blk, off in at:
+        if where == "k":
+            b.k[blk, :, off] = value
+        elif where == "v":
+            b.v[blk, :, off] = value
+        else:
+            b.v[blk, 1, off, 77] = value
+    got = b.call(lib)
+    assert lib.pa_get_status() == 0
+    others = [j for j in range(nodes) if j not in below] + list(range(nodes, nodes + 8))
+    assert torch.equal(got[others], clean[others])
+    if where != "k":
+        ref = b.oracle()[0][below]
+        fine = np.isfinite(ref)
+        g = got[below].double().cpu().numpy()
+        assert (np.isfinite(g) == fine).all()
+        assert np.array_equal(np.isnan(g), np.isnan(ref))
+        assert np.array_equal(g[~fine & ~np.isnan(g)], ref[~fine & ~np.isnan(ref)])
+
+
+def _up(parents, j):
+    out = []
+    while j >= 0:
+        out.append(j)
+        j = int(parents[j])
+    return out
+
+
+def test_scores_of_the_lowest_value(lib):
+    """Keys whose scores are all far below zero still weigh 1 together."""
+    b = tree_batch(11, "bf16", [0, 40], [3, 5], 4, 1, 64)
+    b.q[:] = 0
+    b.q[..., 0] = 200.0
+    b.k[..., 0] = -200.0
+    run(lib, b)
+
+
+def test_steep_scores(lib):
+    """Running maxima that rise from tile to tile."""
+    b = tree_batch(12, "f32", [700], [9], 4, 2, 64, q_scale=6.0)
+    run(lib, b)
+    b = tree_batch(12, "bf16", [700, 3000], [9, 4], 4, 2, 64, q_scale=6.0)
+    run(lib, b)
+
+
+def test_results_repeat_and_ignore_the_neighbours(lib):
+    b = tree_batch(13, "bf16", [800, 33, 470], [12, 8, 30], 32, 8, 128)
+    first = b.call(lib)
+    for _ in range(3):
+        assert torch.equal(b.call(lib), first)
+
+
+def test_captured_and_replayed(lib):
+    b = tree_batch(14, "bf16", [800, 33, 470], [12, 8, 30], 16, 4, 128)
+    a = b.device()
+    out = torch.empty_like(a["q"])
+    ws = torch.empty(lib.pa_decode_tree_workspace_size(3, 16, 4, 128, 16, 50, 64, 2000), dtype=torch.uint8,
+                     device="cuda")
+    a.update(max_q_len=64, max_kv_len=2000)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lib.pa_decode_tree(**a, out=out, workspace=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.pa_decode_tree(**a, out=out, workspace=ws)
+    # Other lengths and another tree within the same bounds.
+    b2 = tree_batch(15, "bf16", [310, 900, 64], [20, 12, 18], 16, 4, 128)
+    a2 = b2.device()
+    P = a["k_cache"].shape[0]
+    b2.table = b2.table % P
+    for name in ("q", "cu_q_lens", "parents", "ctx_lens"):
+        a[name].copy_(a2[name])
+    a["block_tables"].zero_()
+    w = min(a["block_tables"].shape[1], b2.table.shape[1])
+    a["block_tables"][:, :w] = torch.from_numpy(b2.table[:, :w]).cuda()
+    b2.table = a["block_tables"].cpu().numpy()
+    b2.ctx = np.minimum(b2.ctx, w * 16 - 20).astype(np.int32)
+    a["ctx_lens"].copy_(torch.from_numpy(b2.ctx))
+    b2.k, b2.v = b.k, b.v
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert lib.pa_get_status() == 0
+    assert_tree_close(b2, out)
+
+
+def test_two_streams(lib):
+    bs = [tree_batch(20 + i, "bf16", [500 * (i + 1), 44], [9, 30], 16, 4, 128) for i in range(2)]
+    args = [b.device() for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        outs.append([lib.pa_decode_tree(**a, stream=s) for a, s in zip(args, streams)])
+    torch.cuda.synchronize()
+    for pair in outs:
+        for b, o in zip(bs, pair):
+            assert_tree_close(b, o)
+
+
+def test_sequences_beyond_the_bounds(lib):
+    """A sequence beyond the given bounds is reported and left alone."""
+    b = tree_batch(16, "bf16", [100, 50, 20], [4, 9, 3], 8, 2, 128)
+    a = b.device()
+    out = torch.full_like(a["q"], 7.0)
+    a["max_q_len"] = 8
+    lib.pa_decode_tree(**a, out=out)
+    assert lib.pa_get_status() == -8
+    assert (out[4:13] == 7.0).all()
+    ref = b.call(lib)
+    assert torch.equal(out[:4], ref[:4]) and torch.equal(out[13:], ref[13:])
+    a["max_q_len"], a["max_kv_len"] = 9, 100
+    lib.pa_decode_tree(**a, out=out.fill_(7.0))
+    assert lib.pa_get_status() == -8
+    assert (out[:4] == 7.0).all() and torch.equal(out[4:], ref[4:])
+    for ctx in (-1, 2 ** 31 - 1):
+        a = b.device()
+        a["ctx_lens"][1] = ctx
+        lib.pa_decode_tree(**a, out=out.fill_(7.0))
+        assert lib.pa_get_status() == -8
+        assert (out[4:13] == 7.0).all() and torch.equal(out[:4], ref[:4])
+    a = b.device()
+    a["cu_q_lens"][2] = 2  # falls
+    lib.pa_decode_tree(**a, out=out)
+    assert lib.pa_get_status() == -8
+    a = b.device()
+    a["cu_q_lens"][3] = 99
+    lib.pa_decode_tree(**a, out=out)
+    assert lib.pa_get_status() == -8
+
+
+def test_bad_parents_and_blocks(lib):
+    for dtype in ("bf16", "f32"):
+        b = tree_batch(17, dtype, [100, 50], [9, 9], 8, 2, 128)
+        a = b.device()
+        ref = lib.pa_decode_tree(**a)
+        for up in (5, 9, 10 ** 6, -2):
+            a = b.device()
+            a["parents"][4] = up
+            got = lib.pa_decode_tree(**a)
+            assert lib.pa_get_status() == -1
+            assert torch.equal(got[9:], ref[9:])
+        for blk in (-1, a["k_cache"].shape[0], 2 ** 30):
+            a = b.device()
+            a["block_tables"][0, 2] = blk
+            got = lib.pa_decode_tree(**a)
+            assert lib.pa_get_status() == -7
+            assert torch.equal(got[9:], ref[9:])
