@@ -17,7 +17,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libpagedattn.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_prefill.cu", "pa_cascade.cu", "pa_noalloc.cu",
-           "pa_selftest.cu", "pa_tree.cu", "pa_verify.cu", "pa_compact.cu"]
+           "pa_selftest.cu", "pa_tree.cu", "pa_tree_tc.cu",
+           "pa_verify.cu", "pa_compact.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -16,9 +16,9 @@
 namespace pa {
 
 // ---------------------------------------------------------------------------
-// CUDA-core kernel: exact fp32 arithmetic. 128 threads, a query tile of 32
-// rows (row = node * group + head), key tiles of 32 positions widened to fp32
-// in shared memory. Threads 4r .. 4r+3 own row r: eight scores each (keys
+// CUDA-core kernel (fp32 I/O): exact fp32 arithmetic. 128 threads, a query tile of 32
+// rows (row = node * group + head), key tiles of 32 positions in
+// shared memory. Threads 4r .. 4r+3 own row r: eight scores each (keys
 // i, i + 4, ...), then every fourth group of four columns of the output.
 // ---------------------------------------------------------------------------
 namespace ts {
@@ -31,10 +31,9 @@ __host__ __device__ constexpr int smem_bytes(int d) {
 }
 }  // namespace ts
 
-template <typename T, typename S, int D, bool E5>
+template <int D>
 __global__ void __launch_bounds__(ts::kThreads) tree_simt_kernel(const TreeParams p) {
   using namespace ts;
-  constexpr bool KV8 = sizeof(S) == 1;
   extern __shared__ float4 smem4[];
   float* qs = reinterpret_cast<float*>(smem4);  // [kRows][D + 4]
   float* ks = qs + kRows * (D + 4);             // [kKeys][D + 4]
@@ -51,7 +50,7 @@ __global__ void __launch_bounds__(ts::kThreads) tree_simt_kernel(const TreeParam
   TreePiece c;
   while (walk.next(p, c)) {
     const int32_t* parents = p.parents + c.s.q0;
-    tree_check_parents<kThreads>(p, c);
+    tree_check_parents<kThreads>(p, c, threadIdx.x);
     const int32_t* table = p.block_tables + (int64_t)c.seq * p.max_blocks_per_seq;
     const int rows = c.s.nodes * p.group;
     const int r = c.qt * kRows + row;  // row of the unit
@@ -63,8 +62,8 @@ __global__ void __launch_bounds__(ts::kThreads) tree_simt_kernel(const TreeParam
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (ur < rows) {
         const int nd = ur / p.group, h = c.kvh * p.group + ur - nd * p.group;
-        const T* src = static_cast<const T*>(p.q) + ((int64_t)(c.s.q0 + nd) * p.num_q_heads + h) * D + d4;
-        x = make_float4(to_f32(src[0]), to_f32(src[1]), to_f32(src[2]), to_f32(src[3]));
+        x = __ldg(reinterpret_cast<const float4*>(
+            static_cast<const float*>(p.q) + ((int64_t)(c.s.q0 + nd) * p.num_q_heads + h) * D + d4));
       }
       *reinterpret_cast<float4*>(qs + rr * (D + 4) + d4) = x;
     }
@@ -95,21 +94,8 @@ __global__ void __launch_bounds__(ts::kThreads) tree_simt_kernel(const TreeParam
         if (id >= 0 && k0 + key < kv_len) {
           const int64_t tile = (int64_t)id * p.num_kv_heads + c.kvh;
           const int64_t at = (tile * p.block_size + (k0 + key) % p.block_size) * D + d4;
-          const S* kp = static_cast<const S*>(p.k_cache) + at;
-          const S* vp = static_cast<const S*>(p.v_cache) + at;
-          if constexpr (KV8) {
-            uint32_t lo, hi;
-            const float2 sc = __ldg(reinterpret_cast<const float2*>(p.kv_scales) + tile);
-            fp8x4_to_f16x4<E5>(*reinterpret_cast<const uint32_t*>(kp), lo, hi);
-            float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo)), b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-            k = make_float4(a.x * sc.x, a.y * sc.x, b.x * sc.x, b.y * sc.x);
-            fp8x4_to_f16x4<E5>(*reinterpret_cast<const uint32_t*>(vp), lo, hi);
-            a = __half22float2(*reinterpret_cast<__half2*>(&lo)), b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-            v = make_float4(a.x * sc.y, a.y * sc.y, b.x * sc.y, b.y * sc.y);
-          } else {
-            k = make_float4(to_f32(kp[0]), to_f32(kp[1]), to_f32(kp[2]), to_f32(kp[3]));
-            v = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
-          }
+          k = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.k_cache) + at));
+          v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.v_cache) + at));
         }
         *reinterpret_cast<float4*>(ks + key * (D + 4) + d4) = k;
         *reinterpret_cast<float4*>(vs + key * D + d4) = v;
@@ -178,7 +164,7 @@ __global__ void __launch_bounds__(ts::kThreads) tree_simt_kernel(const TreeParam
       if (r < rows) {
         const float inv = 1.f / l;
         const int h = c.kvh * p.group + r - node * p.group;
-        T* out = static_cast<T*>(p.out) + ((int64_t)(c.s.q0 + node) * p.num_q_heads + h) * D;
+        float* out = static_cast<float*>(p.out) + ((int64_t)(c.s.q0 + node) * p.num_q_heads + h) * D;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
           store4(out + (part + 4 * j) * 4, make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv));
@@ -235,35 +221,25 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
   }
 }
 
-template <typename T, typename S, int D, bool E5 = false>
+template <int D>
 static int run_simt(const TreeParams& p, int ctas, cudaStream_t stream) {
-  auto kern = tree_simt_kernel<T, S, D, E5>;
+  auto kern = tree_simt_kernel<D>;
   constexpr int smem = ts::smem_bytes(D);
   if (set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem) != PA_OK) return PA_ERR_CUDA;
   kern<<<ctas, ts::kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-template <typename T>
-static int run_simt16(const TreeParams& p, int ctas, cudaStream_t stream) {
-  if (p.kv_scales)
-    return p.kv_fmt == PA_KV_E5M2 ? run_simt<T, uint8_t, 128, true>(p, ctas, stream)
-                                  : run_simt<T, uint8_t, 128>(p, ctas, stream);
-  return p.head_dim == 64 ? run_simt<T, T, 64>(p, ctas, stream) : run_simt<T, T, 128>(p, ctas, stream);
-}
-
-int launch_tree_simt(const TreeParams& p, int ctas, pa_dtype dt, cudaStream_t stream) {
-  if (dt == PA_BF16) return run_simt16<__nv_bfloat16>(p, ctas, stream);
-  if (dt == PA_F16) return run_simt16<__half>(p, ctas, stream);
+static int launch_tree_simt(const TreeParams& p, int ctas, cudaStream_t stream) {
   switch (p.head_dim) {
-    case 32: return run_simt<float, float, 32>(p, ctas, stream);
-    case 64: return run_simt<float, float, 64>(p, ctas, stream);
-    case 96: return run_simt<float, float, 96>(p, ctas, stream);
-    case 128: return run_simt<float, float, 128>(p, ctas, stream);
-    case 160: return run_simt<float, float, 160>(p, ctas, stream);
-    case 192: return run_simt<float, float, 192>(p, ctas, stream);
-    case 224: return run_simt<float, float, 224>(p, ctas, stream);
-    case 256: return run_simt<float, float, 256>(p, ctas, stream);
+    case 32: return run_simt<32>(p, ctas, stream);
+    case 64: return run_simt<64>(p, ctas, stream);
+    case 96: return run_simt<96>(p, ctas, stream);
+    case 128: return run_simt<128>(p, ctas, stream);
+    case 160: return run_simt<160>(p, ctas, stream);
+    case 192: return run_simt<192>(p, ctas, stream);
+    case 224: return run_simt<224>(p, ctas, stream);
+    case 256: return run_simt<256>(p, ctas, stream);
   }
   return PA_ERR_UNSUPPORTED;
 }
@@ -309,10 +285,19 @@ TreeLayout tree_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_hea
   if (num_seqs == 0 || total_q == 0) return w;
   if (max_q_len < 1 || max_kv_len < 1) return fail(PA_ERR_ARG);
   if (num_seqs > 65535 || max_q_len > kMaxTreeNodes) return fail(PA_ERR_UNSUPPORTED);
-  w.tile_rows = w.tile_m = ts::kRows;
-  w.tile_keys = ts::kKeys;
-  w.min_tiles = 4;
-  const int64_t per_sm = head_dim <= 128 ? 4 : 2;
+  int per_sm;
+  if (dt == PA_F32) {
+    w.tile_rows = w.tile_m = ts::kRows;
+    w.tile_keys = ts::kKeys;
+    w.min_tiles = 4;
+    per_sm = head_dim <= 128 ? 4 : 2;
+  } else {
+    w.tile_m = kTreeTcRows;
+    w.tile_rows = kTreeTcRows / group * group;
+    w.tile_keys = kTreeTcKeys;
+    w.min_tiles = 2;
+    per_sm = 2;
+  }
   // Most key tiles there can be: one more query tile than its rows fill for every sequence.
   const double units = ((double)total_q * group / w.tile_rows + std::min(num_seqs, total_q)) * num_kv_heads;
   const double most = units * ((max_kv_len + w.tile_keys - 1) / w.tile_keys) / w.min_tiles + 1;
@@ -379,7 +364,7 @@ int decode_tree(const void* q, int32_t total_q, const int32_t* cu_q_lens, const 
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   p.status = st;
-  const int rc = launch_tree_simt(p, w.ctas, dtype, stream);
+  const int rc = dtype == PA_F32 ? launch_tree_simt(p, w.ctas, stream) : launch_tree_tc(p, w.ctas, dtype, stream);
   if (rc != PA_OK) return rc;
   return launch_tree_join(p, w.ctas, dtype, stream);
 }

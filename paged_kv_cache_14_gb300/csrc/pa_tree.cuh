@@ -235,17 +235,18 @@ __device__ __forceinline__ uint32_t tree_ancestors(const int32_t* parents, int n
 // Reports parents that are not below their node, once per sequence: by the
 // CTA with the last key tile of its first unit.
 template <int THREADS>
-__device__ __forceinline__ void tree_check_parents(const TreeParams& p, const TreePiece& c) {
+__device__ __forceinline__ void tree_check_parents(const TreeParams& p, const TreePiece& c, int tid) {
   if (c.kvh || c.qt || c.t1 != c.s.ktiles) return;
-  for (int j = threadIdx.x; j < c.s.nodes; j += THREADS) {
+  for (int j = tid; j < c.s.nodes; j += THREADS) {
     const int up = __ldg(p.parents + c.s.q0 + j);
     if (up < -1 || up >= j) record_error(p.status, PA_ERR_ARG);
   }
 }
 
 // The tensor-core kernel (fp16 / bf16 q; head_dim 64 or 128, 128 for 8-bit
-// caches), the fp32 kernel, and the join kernel behind either.
+// caches): query tiles of 128 rows, key tiles of 64 positions.
+constexpr int kTreeTcRows = 128;
+constexpr int kTreeTcKeys = 64;
 int launch_tree_tc(const TreeParams& p, int ctas, pa_dtype dt, cudaStream_t stream);
-int launch_tree_simt(const TreeParams& p, int ctas, pa_dtype dt, cudaStream_t stream);
 
 }  // namespace pa
