@@ -14,19 +14,37 @@
 //
 // The token is a whole number that has to come out the same whatever the
 // order of the sum, so sums are taken over integers: a weight in [0, 1] is
-// rounded once to a multiple of 2^-45 (below 2^18 of them fit 64 bits), and
-// integer sums do not depend on their order.
+// rounded once to a multiple of 2^-44 (2^18 of them fit 62 bits), and integer
+// sums do not depend on their order. p - C q is formed in pairs of floats
+// (exact product, exact difference), since double arithmetic runs at a
+// fraction of the rate.
+//
+// A sequence is one cluster of 1 to 8 CTAs, each with a slice of the
+// vocabulary; all of them walk the tree by themselves and exchange only sums.
+// A warp sums chunks of 512 entries (16 bytes a load, a chunk's loads all in
+// flight) and every chunk's sum is kept, so the entry where the running sum
+// passes the threshold takes a second look at one chunk only. What bounds it
+// is the rows' one pass from HBM; with few sequences, the latency of its
+// dependent loads and cluster barriers.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
 namespace pa {
+namespace cg = cooperative_groups;
 
 constexpr int kVerifyMaxNodes = 1024;
 constexpr int kVerifyMaxVocab = 1 << 18;
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyChunk = 512;
+constexpr int kVerifyMaxChunks = kVerifyMaxVocab / kVerifyChunk + 1;  // + 1: a row may start inside a 16-byte line
+constexpr int kVerifyMaxCluster = 8;
+constexpr double kVerifyUnit = 1.0 / 17592186044416.0;  // 2^-44
+constexpr unsigned kAll = 0xffffffffu;
 
 struct VerifyParams {
   const void* target;
@@ -48,165 +66,307 @@ struct VerifyParams {
 template <typename T>
 __device__ __forceinline__ float prob(T x) { return __saturatef(to_f32(x)); }
 
-// max(0, p - C q) as a multiple of 2^-45.
-__device__ __forceinline__ long long weight_fixed(float p, float q, double C) {
-  const double w = (double)p - C * (double)q;
-  return w > 0.0 ? __double2ll_rn(w * 35184372088832.0) : 0ll;
+// max(0, p - C q) in units of 2^-44, as hi * 2^22 + lo with 0 <= hi <= 2^22 and
+// |lo| <= 2^21. C = c + cl (cl: what a float of C leaves over).
+__device__ __forceinline__ void weight_parts(float p, float q, float c, float cl, uint32_t& hi, int& lo) {
+  const float m = c * q;
+  const float me = fmaf(cl, q, fmaf(c, q, -m));  // C q = m + me
+  const float d = p - m;
+  const float bb = d - p;
+  const float e = ((p - (d - bb)) - (m + bb)) - me;  // p - C q = d + e
+  const float magic = 12582912.f;                   // 1.5 * 2^23: adding it rounds to a whole number
+  const float t = fmaf(d, 4194304.f, magic);
+  const float rest = fmaf(e, 4194304.f, fmaf(d, 4194304.f, magic - t));
+  const bool some = d + e > 0.f;
+  hi = some ? __float_as_uint(t) - __float_as_uint(magic) : 0u;
+  lo = some ? __float2int_rn(rest * 4194304.f) : 0;
+}
+
+__device__ __forceinline__ long long joined(uint32_t hi, int lo) { return ((long long)hi << 22) + lo; }
+
+// N entries from y on of a row of V (those outside count as 0). `line`: the
+// address of entry y is a multiple of 16.
+template <typename T, int N>
+__device__ __forceinline__ void load_probs(const T* row, int y, int V, bool line, float (&x)[N]) {
+  if (line && y >= 0 && y + N <= V) {
+    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row + y));
+    const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = prob(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = y + i >= 0 && y + i < V ? prob(row[y + i]) : 0.f;
+  }
 }
 
 template <typename T, bool DRAFT>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+  constexpr int N = 16 / sizeof(T);                // entries of one load
+  constexpr int kLoads = kVerifyChunk / (32 * N);  // loads of a lane in a chunk
+  constexpr int kMine = kLoads * N;                // entries of a lane in a chunk
   __shared__ int16_t parent[kVerifyMaxNodes];
   __shared__ int tok[kVerifyMaxNodes];
   __shared__ float px[kVerifyMaxNodes], qx[kVerifyMaxNodes], ua[kVerifyMaxNodes];
-  __shared__ long long wsum[kVerifyWarps];
-  __shared__ int bad, state[4];
-  __shared__ double mult;
-  const int seq = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ bool again[kVerifyMaxNodes];  // an earlier sibling has the same token
+  __shared__ long long chunk_sum[kVerifyMaxChunks];
+  __shared__ long long slice_sum[2][kVerifyMaxCluster];  // every CTA's, written by it
+  __shared__ unsigned long long acc;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int seq = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto started = cluster.barrier_arrive();  // peers' shared memory may be written once all have arrived
   int32_t* path = p.path + (int64_t)seq * p.max_path_len;
   const int q0 = p.cu_q_lens[seq];
   const int64_t n64 = (int64_t)p.cu_q_lens[seq + 1] - q0;
-  if (tid == 0) bad = n64 < 0 || q0 < 0 || q0 + n64 > p.total_q || n64 > p.max_q_len;
-  __syncthreads();
-  const int n = bad ? 0 : (int)n64;
+  const bool bad_len = n64 < 0 || q0 < 0 || q0 + n64 > p.total_q || n64 > p.max_q_len;
+  const int n = bad_len ? 0 : (int)n64;
+  bool bad_tree = false;
   for (int j = tid; j < n; j += kVerifyThreads) {
-    const int up = p.parents[q0 + j];
-    parent[j] = (int16_t)up;
-    if (up < -1 || up >= j || (j == 0 && up != -1)) bad = 1;
-    const int t = p.tokens[q0 + j];
-    const bool real = t >= 0 && t < p.vocab && up >= 0 && up < j;
-    tok[j] = real ? t : -1;
+    const int up = p.parents[q0 + j], t = p.tokens[q0 + j];
     ua[j] = p.u_accept[q0 + j];
+    bad_tree |= up < -1 || up >= j || (j == 0 && up != -1);
+    const bool real = t >= 0 && t < p.vocab && up >= 0 && up < j;
+    parent[j] = real ? (int16_t)up : (int16_t)-1;  // a node without a token is nobody's child
+    tok[j] = t;
     px[j] = real ? prob(static_cast<const T*>(p.target)[(int64_t)(q0 + up) * p.target_stride + t]) : 0.f;
-    qx[j] = real && DRAFT ? prob(static_cast<const T*>(p.draft)[(int64_t)(q0 + up) * p.draft_stride + t]) : 0.f;
+    if constexpr (DRAFT)
+      qx[j] = real ? prob(static_cast<const T*>(p.draft)[(int64_t)(q0 + up) * p.draft_stride + t]) : 0.f;
   }
-  __syncthreads();
-  if (bad || n == 0) {
-    if (tid == 0 && bad) record_error(p.status, n64 < 0 || n64 > p.max_q_len || q0 < 0 || q0 + n64 > p.total_q ? PA_ERR_SEQLEN : PA_ERR_ARG);
-    for (int k = tid; k < p.max_path_len; k += kVerifyThreads) path[k] = -1;
-    if (tid == 0) p.path_lens[seq] = 0, p.next_tokens[seq] = -1;
+  bad_tree = __syncthreads_or(bad_tree);
+  cluster.barrier_wait(std::move(started));
+  if (bad_len || bad_tree || n == 0) {  // (the same in every CTA of the cluster)
+    if (rank == 0) {
+      if (tid == 0 && n64 != 0) record_error(p.status, bad_len ? PA_ERR_SEQLEN : PA_ERR_ARG);
+      for (int k = tid; k < p.max_path_len; k += kVerifyThreads) path[k] = -1;
+      if (tid == 0) p.path_lens[seq] = 0, p.next_tokens[seq] = -1;
+    }
     return;
   }
-  auto row_p = [&](int r) { return static_cast<const T*>(p.target) + (int64_t)(q0 + r) * p.target_stride; };
-  auto row_q = [&](int r) { return static_cast<const T*>(p.draft) + (int64_t)(q0 + r) * p.draft_stride; };
-  // Warp w sums entries [w seg, (w + 1) seg).
-  const int seg = (p.vocab + kVerifyWarps - 1) / kVerifyWarps;
-  const int v0 = min(p.vocab, warp * seg), v1 = min(p.vocab, v0 + seg);
-  auto total = [&](int r, double C) -> long long {
-    const T* a = row_p(r);
-    const T* b = DRAFT ? row_q(r) : a;
-    long long s = 0;
-    for (int y = v0 + lane; y < v1; y += 32) s += weight_fixed(prob(a[y]), DRAFT && C > 0.0 ? prob(b[y]) : 0.f, C);
+  if constexpr (!DRAFT) {
+    for (int j = tid; j < n; j += kVerifyThreads) {
+      bool same = false;
+      const int up = parent[j], t = tok[j];
+      if (up >= 0)
+        for (int i = up + 1; i < j; ++i) same |= parent[i] == up && tok[i] == t;
+      again[j] = same;
+    }
+    __syncthreads();
+  }
+
+  auto row_a = [&](int r) { return static_cast<const T*>(p.target) + (int64_t)(q0 + r) * p.target_stride; };
+  auto row_b = [&](int r) -> const T* {
+    if constexpr (DRAFT) return static_cast<const T*>(p.draft) + (int64_t)(q0 + r) * p.draft_stride;
+    return nullptr;
+  };
+  // Chunks are counted from the 16-byte line in which the target's row starts.
+  auto lead_of = [&](const T* a) { return (int)((reinterpret_cast<uintptr_t>(a) & 15) / sizeof(T)); };
+  // A lane's weights of chunk c: entries (32 u + lane) N + i of it.
+  auto chunk_weights = [&](const T* a, const T* b, int c, float cm, float cl, uint32_t (&hi)[kMine], int (&lo)[kMine]) {
+    float x[kLoads][N], y[kLoads][N];
+    const int at = c * kVerifyChunk - lead_of(a) + lane * N;
+    const bool draft = DRAFT && cm > 0.f;
+    const bool line = draft && ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int u = 0; u < kLoads; ++u) {
+      load_probs<T, N>(a, at + u * 32 * N, p.vocab, true, x[u]);
+      if (draft) load_probs<T, N>(b, at + u * 32 * N, p.vocab, line, y[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        weight_parts(x[u][i], draft ? y[u][i] : 0.f, cm, cl, hi[u * N + i], lo[u * N + i]);
+  };
+  int sums = 0, c_lo = 0;
+  // The sum of w at row r over the vocabulary; this CTA's chunks' sums stay in
+  // chunk_sum. take_out (without a draft row): r's children were refused.
+  auto total = [&](int r, double C, bool take_out) -> long long {
+    const T* a = row_a(r);
+    const T* b = row_b(r);
+    const float cm = (float)C, cl = (float)(C - (double)cm);
+    const int lead = lead_of(a), chunks = (p.vocab + lead + kVerifyChunk - 1) / kVerifyChunk;
+    c_lo = chunks * rank / ranks;
+    const int c_hi = chunks * (rank + 1) / ranks;
+    if (tid == 0) acc = 0;
     __syncthreads();
-    if (lane == 0) wsum[warp] = s;
+    long long mine = 0;
+    for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
+      uint32_t hi[kMine];
+      int lo[kMine];
+      chunk_weights(a, b, c, cm, cl, hi, lo);
+      uint32_t h = 0;
+      int l = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) h += hi[i], l += lo[i];
+      // 512 entries: at most 2^31, and 2^30 either way.
+      const long long s = joined(__reduce_add_sync(kAll, h), __reduce_add_sync(kAll, l));
+      if (lane == 0) chunk_sum[c - c_lo] = s;
+      mine += s;
+    }
+    if (lane == 0) atomicAdd(&acc, (unsigned long long)mine);
     __syncthreads();
+    if (!DRAFT && take_out) {
+      for (int j = r + 1 + tid; j < n; j += kVerifyThreads) {
+        if (parent[j] != r || again[j]) continue;
+        const int c = (tok[j] + lead) / kVerifyChunk;
+        if (c < c_lo || c >= c_hi) continue;
+        uint32_t hi;
+        int lo;
+        weight_parts(px[j], 0.f, 0.f, 0.f, hi, lo);
+        const unsigned long long w = (unsigned long long)-joined(hi, lo);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&chunk_sum[c - c_lo]), w);
+        atomicAdd(&acc, w);
+      }
+      __syncthreads();
+    }
+    long long* here = slice_sum[sums & 1];  // (two in turn: a slow CTA may still be reading the last ones)
+    ++sums;
+    if (tid < ranks) *cluster.map_shared_rank(&here[rank], tid) = (long long)acc;
+    cluster.sync();
     long long all = 0;
-    for (int i = 0; i < kVerifyWarps; ++i) all += wsum[i];
+    for (int i = 0; i < ranks; ++i) all += here[i];
     return all;
   };
 
-  // The walk. Every thread takes the same steps over shared memory.
+  // ---- the walk: every warp of every CTA takes the same steps ----
   int at = 0, len = 1;
-  double C = 0.0;
-  if (tid == 0) path[0] = 0;
+  double C;
+  if (rank == 0 && tid == 0) path[0] = 0;
   while (true) {
     double S = 1.0;
     C = 0.0;
     int step = -1;
-    for (int j = at + 1; j < n && len < p.max_path_len; ++j) {
-      if (parent[j] != at || tok[j] < 0) continue;
-      double w = px[j];
-      if constexpr (DRAFT) {
-        if (C > 0.0 && S < 0.0) S = (double)total(at, C) * (1.0 / 35184372088832.0);  // put off until a child needs it
-        w = fmax(0.0, w - C * (double)qx[j]);
-        if ((double)ua[j] * (double)qx[j] * S < w) step = j;
-        else if (C == 0.0) C = 1.0, S = -1.0;
-        else C += S, S = -1.0;
-      } else {
-        bool again = false;
-        for (int i = at + 1; i < j; ++i) again |= parent[i] == at && tok[i] == tok[j];
-        if (again) w = 0.0;
-        if ((double)ua[j] * S < w) step = j;
-        else S -= w;
+    bool stale = false;  // S has to be summed before it is used
+    for (int base = at + 1; base < n && step < 0 && len < p.max_path_len; base += 32) {
+      unsigned kids = __ballot_sync(kAll, base + lane < n && parent[base + lane] == at);
+      while (kids) {
+        const int j = base + __ffs(kids) - 1;
+        kids &= kids - 1;
+        if constexpr (DRAFT) {
+          if (stale) S = (double)total(at, C, false) * kVerifyUnit;
+          const double w = fmax(0.0, (double)px[j] - C * (double)qx[j]);
+          if ((double)ua[j] * (double)qx[j] * S < w) {
+            step = j;
+            break;
+          }
+          C += S;
+          stale = true;
+        } else {
+          const double w = again[j] ? 0.0 : (double)px[j];
+          if ((double)ua[j] * S < w) {
+            step = j;
+            break;
+          }
+          S -= w;
+        }
       }
-      if (step >= 0) break;
     }
     if (step < 0) break;
     at = step;
-    if (tid == 0) path[len] = at;
+    if (rank == 0 && tid == 0) path[len] = at;
     ++len;
   }
-  const bool tried = len < p.max_path_len;  // a full path keeps nothing more: its last node's children are not tried
-  // The next token: the weights' sum, then the segment and the entry where
-  // the running sum passes u' of it.
-  auto gone = [&](int y) {  // without q: y is the token of a refused child
-    if (DRAFT || !tried) return false;
-    for (int j = at + 1; j < n; ++j)
-      if (parent[j] == at && tok[j] == y) return true;
-    return false;
-  };
-  auto dropped = [&](int lo, int hi) -> long long {  // what refused tokens in [lo, hi) take from a sum of p
-    long long s = 0;
-    if (DRAFT || !tried) return s;
-    for (int j = at + 1; j < n; ++j) {
-      if (parent[j] != at || tok[j] < lo || tok[j] >= hi) continue;
-      bool again = false;
-      for (int i = at + 1; i < j; ++i) again |= parent[i] == at && tok[i] == tok[j];
-      if (!again) s += weight_fixed(px[j], 0.f, 0.0);
-    }
-    return s;
-  };
-  long long all = total(at, C) - dropped(0, p.vocab);
-  bool plain = false;
+
+  // ---- the next token ----
+  bool take_out = !DRAFT && len < p.max_path_len;  // a full path's last node did not try its children
+  long long all = total(at, C, take_out);
   if (all <= 0) {  // nothing left after the refusals: drawn from the target itself
     C = 0.0;
-    plain = true;
-    all = total(at, 0.0);
+    take_out = false;
+    all = total(at, C, false);
   }
   const float us = fminf(__saturatef(p.u_sample[seq]), 0.99999994f);
   const long long tau = (long long)((double)us * (double)all);
-  long long before = 0;
-  for (int i = 0; i < warp; ++i)
-    before += wsum[i] - (plain ? 0 : dropped(min(p.vocab, i * seg), min(p.vocab, (i + 1) * seg)));
-  const long long mine = wsum[warp] - (plain ? 0 : dropped(v0, v1));
-  if (all > 0 && before <= tau && tau < before + mine) {
-    const T* a = row_p(at);
-    const T* b = DRAFT ? row_q(at) : a;
-    long long run = before;
-    for (int y0 = v0; y0 < v1; y0 += 32) {
-      const int y = y0 + lane;
-      long long w = 0;
-      if (y < v1 && (plain || !gone(y))) w = weight_fixed(prob(a[y]), DRAFT && C > 0.0 ? prob(b[y]) : 0.f, C);
+  const long long* slice = slice_sum[(sums - 1) & 1];
+  long long run = 0;
+  for (int i = 0; i < rank; ++i) run += slice[i];
+  if (warp == 0 && run <= tau && tau < run + slice[rank]) {
+    const T* a = row_a(at);
+    const T* b = row_b(at);
+    const int lead = lead_of(a), chunks = (p.vocab + lead + kVerifyChunk - 1) / kVerifyChunk;
+    const int c_hi = chunks * (rank + 1) / ranks;
+    // The first lane whose running sum passes tau; run becomes the sum before it.
+    auto passes = [&](long long mine, int& who) -> bool {
+      long long x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long z = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += z;
+        const long long z = __shfl_up_sync(kAll, x, o);
+        if (lane >= o) x += z;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, run + w > tau);
-      if (hit) {
-        if (lane == 0) p.next_tokens[seq] = y0 + __ffs(hit) - 1;
+      const unsigned hit = __ballot_sync(kAll, run + x > tau);
+      who = hit ? __ffs(hit) - 1 : 31;
+      run += __shfl_sync(kAll, hit ? x - mine : x, who);
+      return hit != 0;
+    };
+    int c = c_lo, who = 0;
+    while (!passes(c + lane < c_hi ? chunk_sum[c + lane - c_lo] : 0, who) && c + 32 < c_hi) c += 32;
+    c += who;
+    uint32_t hi[kMine];
+    int lo[kMine];
+    const float cm = (float)C;
+    chunk_weights(a, b, c, cm, (float)(C - (double)cm), hi, lo);
+    if (take_out)
+      for (int j = at + 1; j < n; ++j) {
+        if (parent[j] != at) continue;
+        const int x = tok[j] + lead - c * kVerifyChunk;  // place in the chunk
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (x == (i / N * 32 + lane) * N + i % N) hi[i] = 0, lo[i] = 0;
+      }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      long long mine = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) mine += joined(hi[u * N + i], lo[u * N + i]);
+      if (passes(mine, who)) {
+        if (lane == who) {
+          int y = c * kVerifyChunk - lead + (u * 32 + lane) * N;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const long long w = joined(hi[u * N + i], lo[u * N + i]);
+            if (run + w > tau) {
+              p.next_tokens[seq] = y + i;
+              break;
+            }
+            run += w;
+          }
+        }
         break;
       }
-      run += __shfl_sync(0xffffffffu, w, 31);
     }
   }
-  if (tid == 0) {
-    p.path_lens[seq] = len;
-    if (all <= 0) {  // a row without any probability
-      p.next_tokens[seq] = -1;
-      record_error(p.status, PA_ERR_ARG);
+  if (rank == 0) {
+    if (tid == 0) {
+      p.path_lens[seq] = len;
+      if (all <= 0) {  // a row without any probability
+        p.next_tokens[seq] = -1;
+        record_error(p.status, PA_ERR_ARG);
+      }
     }
+    for (int k = len + tid; k < p.max_path_len; k += kVerifyThreads) path[k] = -1;
   }
-  for (int k = len + tid; k < p.max_path_len; k += kVerifyThreads) path[k] = -1;
 }
 
 template <typename T>
 static cudaError_t launch_verify(const VerifyParams& p, int num_seqs, cudaStream_t stream) {
-  if (p.draft) verify_kernel<T, true><<<num_seqs, kVerifyThreads, 0, stream>>>(p);
-  else verify_kernel<T, false><<<num_seqs, kVerifyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  // CTAs of a sequence: as many as keep the batch within four per SM and
+  // leave each at least four chunks.
+  int ranks = 1;
+  while (ranks < kVerifyMaxCluster && (int64_t)num_seqs * ranks * 2 <= 4 * num_sms_current_device() &&
+         p.vocab / kVerifyChunk >= ranks * 2 * 4)
+    ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(num_seqs * ranks));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return p.draft ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true>, p)
+                 : cudaLaunchKernelEx(&cfg, verify_kernel<T, false>, p);
 }
 
 }  // namespace pa
