@@ -9,7 +9,9 @@ load() raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -588,34 +590,48 @@ def pa_swap_blocks(src_k: torch.Tensor, src_v: torch.Tensor | None, dst_k: torch
 # Draft trees: attention, verification, compaction of the kept path.
 # ---------------------------------------------------------------------------
 
-def _cuda_here(t, name: str, dtype=None) -> int:
-    """_cuda() of a tensor on the current device: the calls launch there."""
-    p = _cuda(t, name, dtype)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return p
+def _refuse(t, name: str, dtype, dev: int, shape) -> None:
+    """Raise what is wrong with an argument that _arg does not take."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _scratch(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor that a call on `stream` may use: its memory is not handed out
-    again before that stream is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    h = _stream(stream)
-    if h != torch.cuda.current_stream().cuda_stream:
-        t.record_stream(torch.cuda.ExternalStream(h))
+def _arg(t, name: str, dtype, dev: int, shape) -> int:
+    """Pointer of a contiguous tensor of this type and shape on device dev
+    (the current one: the calls launch there)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _refuse(t, name, dtype, dev, shape)
+    return t.data_ptr()
+
+
+def _place(t, name: str, stream) -> tuple[int, int, object]:
+    """The current device, the stream's handle, and the stream if tensors
+    made here have to be recorded on it (it is not the current one)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    here = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is None:
+        return dev, here, None
+    handle = _stream(stream)
+    return dev, handle, None if handle == here else torch.cuda.ExternalStream(handle)
+
+
+def _scratch(like: torch.Tensor, shape, dtype, side) -> torch.Tensor:
+    """A new tensor that a call on another stream (side) may use: its memory
+    is not handed out again before that stream is done with it."""
+    t = like.new_empty(shape, dtype=dtype)
+    if side is not None:
+        t.record_stream(side)
     return t
-
-
-def _shape(t, name: str, *dims) -> None:
-    """Check t's dimensions (None: any)."""
-    if t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims}")
-
-
-def _dtype_code(t, name: str) -> int:
-    if t.dtype not in _DT:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return _DT[t.dtype]
 
 
 def pa_decode_tree_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
@@ -639,6 +655,7 @@ def pa_decode_tree_fp8(q: torch.Tensor, cu_q_lens: torch.Tensor, parents: torch.
                        ctx_lens: torch.Tensor, max_q_len: int, max_kv_len: int, scale: float,
                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
+    """pa_decode_tree over e4m3 pools."""
     return _decode_tree("pa_decode_tree_fp8", q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_tables,
                         ctx_lens, max_q_len, max_kv_len, scale, out, workspace, stream)
 
@@ -648,56 +665,52 @@ def pa_decode_tree_e5m2(q: torch.Tensor, cu_q_lens: torch.Tensor, parents: torch
                         ctx_lens: torch.Tensor, max_q_len: int, max_kv_len: int, scale: float,
                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                         stream=None) -> torch.Tensor:
+    """pa_decode_tree over e5m2 pools."""
     return _decode_tree("pa_decode_tree_e5m2", q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_tables,
                         ctx_lens, max_q_len, max_kv_len, scale, out, workspace, stream)
 
 
 def _decode_tree(sym, q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_tables, ctx_lens, max_q_len,
                  max_kv_len, scale, out, workspace, stream) -> torch.Tensor:
+    lib = load()
+    dev, handle, side = _place(q, "q", stream)
     T, hq, D = q.shape
-    P, hkv, B, _ = k_cache.shape
-    n = ctx_lens.shape[0]
-    dt = q.dtype
-    code = _dtype_code(q, "q")
+    P, hkv, B, _ = pool = k_cache.shape
+    n, mb = block_tables.shape
+    dt, i32 = q.dtype, torch.int32
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"q must be float32, float16 or bfloat16, got {dt}")
+    if pool[3] != D:
+        raise ValueError(f"k_cache has shape {tuple(pool)}, q's head_dim is {D}")
     kv = dt if kv_scales is None else torch.uint8
-    _shape(k_cache, "k_cache", P, hkv, B, D)
-    _shape(v_cache, "v_cache", P, hkv, B, D)
-    _shape(cu_q_lens, "cu_q_lens", n + 1)
-    _shape(parents, "parents", T)
-    _shape(block_tables, "block_tables", n, None)
+    qp = _arg(q, "q", dt, dev, q.shape)
     if out is None:
-        out = _scratch((T, hq, D), dt, q.device, stream)
-    _shape(out, "out", T, hq, D)
+        out = _scratch(q, (T, hq, D), dt, side)
     if workspace is None:
-        need = pa_decode_tree_workspace_size(n, hq, hkv, D, B, T, max_q_len, max_kv_len, dt)
-        workspace = _scratch(max(need, 16), torch.uint8, q.device, stream)
-    scales = ()
+        need = lib.pa_decode_tree_workspace_size(n, hq, hkv, D, B, T, max_q_len, max_kv_len, code)
+        workspace = _scratch(q, max(need, 16), torch.uint8, side)
+    pools = (_arg(k_cache, "k_cache", kv, dev, pool), _arg(v_cache, "v_cache", kv, dev, pool))
     if kv_scales is not None:
-        _shape(kv_scales, "kv_scales", P, hkv, 2)
-        scales = (_cuda_here(kv_scales, "kv_scales", torch.float32),)
-    rc = getattr(load(), sym)(
-        _cuda_here(q, "q"), T, _cuda_here(cu_q_lens, "cu_q_lens", torch.int32),
-        _cuda_here(parents, "parents", torch.int32), _cuda_here(k_cache, "k_cache", kv),
-        _cuda_here(v_cache, "v_cache", kv), *scales, _cuda_here(block_tables, "block_tables", torch.int32),
-        block_tables.shape[1], _cuda_here(ctx_lens, "ctx_lens", torch.int32), n, int(max_q_len), int(max_kv_len), hq,
-        hkv, D, B, P, float(scale), _cuda_here(out, "out", dt), _cuda_here(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), code, _stream(stream))
-    _check(rc, sym)
+        pools += (_arg(kv_scales, "kv_scales", torch.float32, dev, (P, hkv, 2)),)
+    rc = getattr(lib, sym)(
+        qp, T, _arg(cu_q_lens, "cu_q_lens", i32, dev, (n + 1,)), _arg(parents, "parents", i32, dev, (T,)), *pools,
+        _arg(block_tables, "block_tables", i32, dev, (n, mb)), mb, _arg(ctx_lens, "ctx_lens", i32, dev, (n,)), n,
+        max_q_len, max_kv_len, hq, hkv, D, B, P, scale, _arg(out, "out", dt, dev, (T, hq, D)),
+        _arg(workspace, "workspace", workspace.dtype, dev, workspace.shape), workspace.nbytes, code, handle)
+    if rc:
+        raise PagedAttnError(rc, sym)
     return out
 
 
-def _rows(t, name: str, dtype, rows: int, cols: int) -> tuple[int, int]:
-    """Pointer and row stride (elements) of a [rows, cols] CUDA tensor whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    _shape(t, name, rows, cols)
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+def _rows(t, name: str, dtype, dev: int, shape) -> tuple[int, int]:
+    """Pointer and row stride (elements) of a 2-D CUDA tensor whose rows are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _refuse(t, name, dtype, dev, shape)
+    step, one = t.stride()
+    if shape[1] > 1 and one != 1 or shape[0] > 1 and step < shape[1]:
         raise ValueError(f"{name}'s rows must be contiguous and not overlap")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.data_ptr(), max(t.stride(0), cols)
+    return t.data_ptr(), max(step, shape[1])
 
 
 def pa_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
@@ -707,32 +720,31 @@ def pa_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
                    stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Keep drafted tokens and draw the next one: (path, path_lens, next_tokens).
     target_probs, draft_probs: [total_q, vocab]; rows may be padded apart."""
-    T, V = target_probs.shape
+    lib = load()
+    dev, handle, side = _place(target_probs, "target_probs", stream)
+    T, V = shape = target_probs.shape
     n = uniform_sample.shape[0]
-    dev = target_probs.device
-    code = _dtype_code(target_probs, "target_probs")
-    tp, ts = _rows(target_probs, "target_probs", target_probs.dtype, T, V)
-    dp, ds = (None, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", target_probs.dtype, T, V)
-    _shape(cu_q_lens, "cu_q_lens", n + 1)
-    for t, name in ((parents, "parents"), (draft_tokens, "draft_tokens"), (uniform_accept, "uniform_accept")):
-        _shape(t, name, T)
+    dt, i32, f32 = target_probs.dtype, torch.int32, torch.float32
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"target_probs must be float32, float16 or bfloat16, got {dt}")
+    tp, ts = _rows(target_probs, "target_probs", dt, dev, shape)
+    dp, ds = (None, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", dt, dev, shape)
+    rows = (T,)
     if path is None:
-        path = _scratch((n, max_path_len), torch.int32, dev, stream)
+        path = _scratch(target_probs, (n, max_path_len), i32, side)
     if path_lens is None:
-        path_lens = _scratch(n, torch.int32, dev, stream)
+        path_lens = _scratch(target_probs, n, i32, side)
     if next_tokens is None:
-        next_tokens = _scratch(n, torch.int32, dev, stream)
-    _shape(path, "path", n, max_path_len)
-    _shape(path_lens, "path_lens", n)
-    _shape(next_tokens, "next_tokens", n)
-    rc = load().pa_verify_tree(
-        tp, ts, dp, ds, _cuda_here(draft_tokens, "draft_tokens", torch.int32),
-        _cuda_here(cu_q_lens, "cu_q_lens", torch.int32), _cuda_here(parents, "parents", torch.int32),
-        _cuda_here(uniform_accept, "uniform_accept", torch.float32),
-        _cuda_here(uniform_sample, "uniform_sample", torch.float32), n, T, int(max_q_len), V, int(max_path_len),
-        _cuda_here(path, "path", torch.int32), _cuda_here(path_lens, "path_lens", torch.int32),
-        _cuda_here(next_tokens, "next_tokens", torch.int32), code, _stream(stream))
-    _check(rc, "pa_verify_tree")
+        next_tokens = _scratch(target_probs, n, i32, side)
+    rc = lib.pa_verify_tree(
+        tp, ts, dp, ds, _arg(draft_tokens, "draft_tokens", i32, dev, rows),
+        _arg(cu_q_lens, "cu_q_lens", i32, dev, (n + 1,)), _arg(parents, "parents", i32, dev, rows),
+        _arg(uniform_accept, "uniform_accept", f32, dev, rows), _arg(uniform_sample, "uniform_sample", f32, dev, (n,)),
+        n, T, max_q_len, V, max_path_len, _arg(path, "path", i32, dev, (n, max_path_len)),
+        _arg(path_lens, "path_lens", i32, dev, (n,)), _arg(next_tokens, "next_tokens", i32, dev, (n,)), code, handle)
+    if rc:
+        raise PagedAttnError(rc, "pa_verify_tree")
     return path, path_lens, next_tokens
 
 
@@ -757,36 +769,47 @@ def pa_compact_tree_e5m2(k_caches, v_caches, kv_scales, block_tables: torch.Tens
                   stream)
 
 
+_LAYOUT = operator.attrgetter("dtype", "shape")
+
+
+def _pools(pools, name: str, dtype, dev: int, shape) -> array.array:
+    """Pointers of the layers' pools, as _arg. The checks run as loops in C:
+    a model has dozens of layers, and this is most of a call's host time."""
+    T = torch.Tensor
+    if not (set(map(_LAYOUT, pools)) == {(dtype, shape)} and set(map(T.get_device, pools)) == {dev}
+            and all(map(T.is_contiguous, pools))):
+        for i, t in enumerate(pools):
+            _arg(t, f"{name}[{i}]", dtype, dev, shape)
+    return array.array("Q", map(T.data_ptr, pools))
+
+
 def _compact_tree(sym, k_caches, v_caches, kv_scales, block_tables, ctx_lens, path, path_lens, stream) -> None:
+    lib = load()
     layers = len(k_caches)
     if len(v_caches) != layers or (kv_scales is not None and len(kv_scales) != layers):
         raise ValueError("k_caches, v_caches and kv_scales must list the same layers")
     if layers == 0:
         return
-    P, hkv, B, D = k_caches[0].shape
-    dt = torch.uint8 if kv_scales is not None else k_caches[0].dtype
-    code = () if kv_scales is not None else (_dtype_code(k_caches[0], "k_caches"),)
-    n = ctx_lens.shape[0]
-
-    def pointers(pools, name, dtype, *dims):
-        out = (ctypes.c_void_p * layers)()
-        here = torch.cuda.current_device()
-        for i, t in enumerate(pools):
-            if t.dtype != dtype or t.shape != dims or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor of {dtype} and shape {dims}")
-            if t.device.index != here:
-                raise ValueError(f"{name}[{i}] is on {t.device}, the current device is cuda:{here}")
-            out[i] = t.data_ptr()
-        return out
-
-    kp = pointers(k_caches, "k_caches", dt, P, hkv, B, D)
-    vp = pointers(v_caches, "v_caches", dt, P, hkv, B, D)
-    sp = () if kv_scales is None else (pointers(kv_scales, "kv_scales", torch.float32, P, hkv, 2),)
-    _shape(block_tables, "block_tables", n, None)
-    _shape(path, "path", n, None)
-    _shape(path_lens, "path_lens", n)
-    rc = getattr(load(), sym)(
-        kp, vp, *sp, layers, _cuda_here(block_tables, "block_tables", torch.int32), block_tables.shape[1],
-        _cuda_here(ctx_lens, "ctx_lens", torch.int32), _cuda_here(path, "path", torch.int32),
-        _cuda_here(path_lens, "path_lens", torch.int32), n, path.shape[1], P, B, hkv, D, *code, _stream(stream))
-    _check(rc, sym)
+    k_caches, v_caches, kv_scales = (x.unbind(0) if isinstance(x, torch.Tensor) else x
+                                     for x in (k_caches, v_caches, kv_scales))
+    dev, handle, _ = _place(k_caches[0], "k_caches[0]", stream)
+    P, hkv, B, D = shape = k_caches[0].shape
+    n, mb = block_tables.shape
+    width = path.shape[1]
+    i32 = torch.int32
+    if kv_scales is None:
+        dt = k_caches[0].dtype
+        code = (_DT.get(dt),)
+        if code[0] is None:
+            raise TypeError(f"k_caches must be float32, float16 or bfloat16, got {dt}")
+    else:
+        dt, code = torch.uint8, ()
+    lists = [_pools(k_caches, "k_caches", dt, dev, shape), _pools(v_caches, "v_caches", dt, dev, shape)]
+    if kv_scales is not None:
+        lists.append(_pools(kv_scales, "kv_scales", torch.float32, dev, torch.Size((P, hkv, 2))))
+    rc = getattr(lib, sym)(
+        *(x.buffer_info()[0] for x in lists), layers, _arg(block_tables, "block_tables", i32, dev, (n, mb)), mb,
+        _arg(ctx_lens, "ctx_lens", i32, dev, (n,)), _arg(path, "path", i32, dev, (n, width)),
+        _arg(path_lens, "path_lens", i32, dev, (n,)), n, width, P, B, hkv, D, *code, handle)
+    if rc:
+        raise PagedAttnError(rc, sym)

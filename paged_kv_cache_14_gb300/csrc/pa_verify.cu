@@ -66,41 +66,106 @@ struct VerifyParams {
 template <typename T>
 __device__ __forceinline__ float prob(T x) { return __saturatef(to_f32(x)); }
 
+// What C is: nothing refused yet (w = p), one refusal (C = 1), or more.
+enum VerifyMode { kVerifyPlain, kVerifyOne, kVerifyMore };
+
 // max(0, p - C q) in units of 2^-44, as hi * 2^22 + lo with 0 <= hi <= 2^22 and
 // |lo| <= 2^21. C = c + cl (cl: what a float of C leaves over).
+template <int MODE>
 __device__ __forceinline__ void weight_parts(float p, float q, float c, float cl, uint32_t& hi, int& lo) {
-  const float m = c * q;
-  const float me = fmaf(cl, q, fmaf(c, q, -m));  // C q = m + me
-  const float d = p - m;
-  const float bb = d - p;
-  const float e = ((p - (d - bb)) - (m + bb)) - me;  // p - C q = d + e
-  const float magic = 12582912.f;                   // 1.5 * 2^23: adding it rounds to a whole number
+  float d = p, e = 0.f;  // p - C q = d + e
+  if constexpr (MODE != kVerifyPlain) {
+    float m = q, me = 0.f;  // C q = m + me
+    if constexpr (MODE == kVerifyMore) {
+      m = c * q;
+      me = fmaf(cl, q, fmaf(c, q, -m));
+    }
+    d = p - m;
+    const float bb = d - p;
+    e = (p - (d - bb)) - (m + bb);
+    if constexpr (MODE == kVerifyMore) e -= me;
+  }
+  const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
   const float t = fmaf(d, 4194304.f, magic);
-  const float rest = fmaf(e, 4194304.f, fmaf(d, 4194304.f, magic - t));
-  const bool some = d + e > 0.f;
+  float rest = fmaf(d, 4194304.f, magic - t);
+  if constexpr (MODE != kVerifyPlain) rest = fmaf(e, 4194304.f, rest);
+  const bool some = MODE == kVerifyPlain || d + e > 0.f;
   hi = some ? __float_as_uint(t) - __float_as_uint(magic) : 0u;
   lo = some ? __float2int_rn(rest * 4194304.f) : 0;
 }
 
 __device__ __forceinline__ long long joined(uint32_t hi, int lo) { return ((long long)hi << 22) + lo; }
 
-// N entries from y on of a row of V (those outside count as 0). `line`: the
-// address of entry y is a multiple of 16.
-template <typename T, int N>
-__device__ __forceinline__ void load_probs(const T* row, int y, int V, bool line, float (&x)[N]) {
-  if (line && y >= 0 && y + N <= V) {
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(row + y));
-    const T* t = reinterpret_cast<const T*>(&raw);
+template <typename T>
+__device__ __forceinline__ float entry(const uint4& raw, int i) {
+  return prob(reinterpret_cast<const T*>(&raw)[i]);
+}
+
+// The 16 bytes of a row of V that hold entries y .. of it; entries outside
+// the row come as 0. `line`: the address of entry y is a multiple of 16.
+template <typename T>
+__device__ __forceinline__ uint4 load_line(const T* row, int y, int V, bool line) {
+  constexpr int N = 16 / sizeof(T);
+  if (line && y >= 0 && y + N <= V) return __ldg(reinterpret_cast<const uint4*>(row + y));
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  T* t = reinterpret_cast<T*>(&raw);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = prob(t[i]);
-  } else {
+  for (int i = 0; i < N; ++i)
+    if (y + i >= 0 && y + i < V) t[i] = row[y + i];
+  return raw;
+}
+
+// A lane's weights of one chunk, at(u, i, hi, lo) for each: entry (32 u +
+// lane) N + i of the chunk. y: the row's entry that the lane's first one is.
+template <typename T, int MODE, typename F>
+__device__ __forceinline__ void chunk_weights(const T* a, const T* b, int y, int V, float c, float cl, F at) {
+  constexpr int N = 16 / sizeof(T), kLoads = kVerifyChunk / (32 * N);
+  const bool line = ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+  uint4 x[kLoads], z[kLoads];
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = y + i >= 0 && y + i < V ? prob(row[y + i]) : 0.f;
+  for (int u = 0; u < kLoads; ++u) {
+    x[u] = load_line(a, y + u * 32 * N, V, true);
+    if constexpr (MODE != kVerifyPlain) z[u] = load_line(b, y + u * 32 * N, V, line);
   }
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t hi;
+      int lo;
+      float q = 0.f;
+      if constexpr (MODE != kVerifyPlain) q = entry<T>(z[u], i);
+      weight_parts<MODE>(entry<T>(x[u], i), q, c, cl, hi, lo);
+      at(u, i, hi, lo);
+    }
+}
+
+// The sums of a slice's chunks, one warp a chunk at a time; returns this
+// warp's share of their total.
+template <typename T, int MODE>
+__device__ __forceinline__ long long slice_sums(const T* a, const T* b, int lead, int V, float c, float cl, int c_lo,
+                                                int c_hi, long long* chunk_sum) {
+  constexpr int N = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  long long mine = 0;
+#pragma unroll 1
+  for (int k = c_lo + (threadIdx.x >> 5); k < c_hi; k += kVerifyWarps) {
+    uint32_t h = 0;
+    int l = 0;
+    chunk_weights<T, MODE>(a, b, k * kVerifyChunk - lead + lane * N, V, c, cl, [&](int, int, uint32_t hi, int lo) {
+      h += hi;
+      l += lo;
+    });
+    // 512 entries: at most 2^31, and 2^30 either way.
+    const long long s = joined(__reduce_add_sync(kAll, h), __reduce_add_sync(kAll, l));
+    if (lane == 0) chunk_sum[k - c_lo] = s;
+    mine += s;
+  }
+  return mine;
 }
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify_kernel(const VerifyParams p) {
   constexpr int N = 16 / sizeof(T);                // entries of one load
   constexpr int kLoads = kVerifyChunk / (32 * N);  // loads of a lane in a chunk
   constexpr int kMine = kLoads * N;                // entries of a lane in a chunk
@@ -160,23 +225,6 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
   };
   // Chunks are counted from the 16-byte line in which the target's row starts.
   auto lead_of = [&](const T* a) { return (int)((reinterpret_cast<uintptr_t>(a) & 15) / sizeof(T)); };
-  // A lane's weights of chunk c: entries (32 u + lane) N + i of it.
-  auto chunk_weights = [&](const T* a, const T* b, int c, float cm, float cl, uint32_t (&hi)[kMine], int (&lo)[kMine]) {
-    float x[kLoads][N], y[kLoads][N];
-    const int at = c * kVerifyChunk - lead_of(a) + lane * N;
-    const bool draft = DRAFT && cm > 0.f;
-    const bool line = draft && ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      load_probs<T, N>(a, at + u * 32 * N, p.vocab, true, x[u]);
-      if (draft) load_probs<T, N>(b, at + u * 32 * N, p.vocab, line, y[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        weight_parts(x[u][i], draft ? y[u][i] : 0.f, cm, cl, hi[u * N + i], lo[u * N + i]);
-  };
   int sums = 0, c_lo = 0;
   // The sum of w at row r over the vocabulary; this CTA's chunks' sums stay in
   // chunk_sum. take_out (without a draft row): r's children were refused.
@@ -189,20 +237,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const int c_hi = chunks * (rank + 1) / ranks;
     if (tid == 0) acc = 0;
     __syncthreads();
-    long long mine = 0;
-    for (int c = c_lo + warp; c < c_hi; c += kVerifyWarps) {
-      uint32_t hi[kMine];
-      int lo[kMine];
-      chunk_weights(a, b, c, cm, cl, hi, lo);
-      uint32_t h = 0;
-      int l = 0;
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) h += hi[i], l += lo[i];
-      // 512 entries: at most 2^31, and 2^30 either way.
-      const long long s = joined(__reduce_add_sync(kAll, h), __reduce_add_sync(kAll, l));
-      if (lane == 0) chunk_sum[c - c_lo] = s;
-      mine += s;
-    }
+    const long long mine =
+        C == 0.0 ? slice_sums<T, kVerifyPlain>(a, a, lead, p.vocab, cm, cl, c_lo, c_hi, chunk_sum)
+        : C == 1.0 ? slice_sums<T, DRAFT ? kVerifyOne : kVerifyPlain>(a, b, lead, p.vocab, cm, cl, c_lo, c_hi, chunk_sum)
+                   : slice_sums<T, DRAFT ? kVerifyMore : kVerifyPlain>(a, b, lead, p.vocab, cm, cl, c_lo, c_hi, chunk_sum);
     if (lane == 0) atomicAdd(&acc, (unsigned long long)mine);
     __syncthreads();
     if (!DRAFT && take_out) {
@@ -212,7 +250,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         if (c < c_lo || c >= c_hi) continue;
         uint32_t hi;
         int lo;
-        weight_parts(px[j], 0.f, 0.f, 0.f, hi, lo);
+        weight_parts<kVerifyPlain>(px[j], 0.f, 0.f, 0.f, hi, lo);
         const unsigned long long w = (unsigned long long)-joined(hi, lo);
         atomicAdd(reinterpret_cast<unsigned long long*>(&chunk_sum[c - c_lo]), w);
         atomicAdd(&acc, w);
@@ -303,8 +341,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     c += who;
     uint32_t hi[kMine];
     int lo[kMine];
-    const float cm = (float)C;
-    chunk_weights(a, b, c, cm, (float)(C - (double)cm), hi, lo);
+    const float cm = (float)C, cl = (float)(C - (double)cm);
+    const int y0 = c * kVerifyChunk - lead + lane * N;
+    auto keep = [&](int u, int i, uint32_t h, int l) { hi[u * N + i] = h, lo[u * N + i] = l; };
+    if (C == 0.0) chunk_weights<T, kVerifyPlain>(a, a, y0, p.vocab, cm, cl, keep);
+    else chunk_weights<T, DRAFT ? kVerifyMore : kVerifyPlain>(a, b, y0, p.vocab, cm, cl, keep);
     if (take_out)
       for (int j = at + 1; j < n; ++j) {
         if (parent[j] != at) continue;

@@ -287,3 +287,28 @@ def test_bad_parents_and_blocks(lib):
             got = lib.pa_decode_tree(**a)
             assert lib.pa_get_status() == -7
             assert torch.equal(got[9:], ref[9:])
+
+
+def test_binding_refuses(lib):
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    i32 = torch.int32
+    good = dict(q=z(4, 8, 128), cu_q_lens=z(2, dt=i32), parents=z(4, dt=i32), k_cache=z(3, 2, 16, 128),
+                v_cache=z(3, 2, 16, 128), block_tables=z(1, 3, dt=i32), ctx_lens=z(1, dt=i32), max_q_len=4,
+                max_kv_len=20, scale=0.1)
+    for name, bad in (("parents", z(5, dt=i32)), ("cu_q_lens", z(3, dt=i32)), ("v_cache", z(3, 2, 16, 64)),
+                      ("k_cache", z(3, 2, 16, 64)), ("ctx_lens", z(2, dt=i32)), ("out", z(3, 8, 128)),
+                      ("q", z(8, 4, 128).transpose(0, 1)), ("k_cache", z(3, 16, 2, 128).transpose(1, 2)),
+                      ("workspace", z(4096, 2)[:, 0])):
+        with pytest.raises(ValueError, match=name):
+            lib.pa_decode_tree(**dict(good, **{name: bad}))
+    for name, bad in (("q", z(4, 8, 128, dt=torch.float64)), ("parents", z(4, dt=torch.int64)),
+                      ("k_cache", z(3, 2, 16, 128, dt=torch.float16)), ("ctx_lens", torch.zeros(1, dtype=i32))):
+        with pytest.raises(TypeError, match=name):
+            lib.pa_decode_tree(**dict(good, **{name: bad}))
+    with pytest.raises(lib.PagedAttnError):
+        lib.pa_decode_tree(**dict(good, workspace=z(16, dt=torch.uint8)))
+    pool, odd = z(3, 2, 16, 64), z(3, 2, 16, 128)
+    tail = (z(1, 3, dt=i32), z(1, dt=i32), z(1, 4, dt=i32), z(1, dt=i32))
+    for k, v in (([pool, odd], [pool, pool]), ([pool, pool], [pool, pool.float()]), ([odd[..., :64]], [pool])):
+        with pytest.raises((ValueError, TypeError), match="_caches"):
+            lib.pa_compact_tree(k, v, *tail)

@@ -118,27 +118,18 @@ def test_compact_host_checks(lib):
 def test_binding_refuses_host_tensors():
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
     i32 = torch.int32
-    with pytest.raises((TypeError, ValueError, RuntimeError)):
+    with pytest.raises(TypeError, match="CUDA"):
         pa.pa_decode_tree(z(4, 8, 128), z(2, dt=i32), z(4, dt=i32), z(3, 2, 16, 128), z(3, 2, 16, 128), z(1, 3, dt=i32),
                           z(1, dt=i32), 4, 20, 0.1, out=z(4, 8, 128), workspace=z(16, dt=torch.uint8))
-    with pytest.raises((TypeError, ValueError, RuntimeError)):
+    with pytest.raises(TypeError, match="CUDA"):
         pa.pa_verify_tree(z(4, 10), None, z(4, dt=i32), z(2, dt=i32), z(4, dt=i32), z(4), z(1), 4, 4)
-    with pytest.raises((TypeError, ValueError, RuntimeError, AssertionError)):
+    with pytest.raises(TypeError, match="CUDA"):
         pa.pa_compact_tree([z(3, 2, 16, 64)], [z(3, 2, 16, 64)], z(1, 3, dt=i32), z(1, dt=i32), z(1, 4, dt=i32),
                            z(1, dt=i32))
 
 
-def test_binding_refuses_shapes():
+def test_binding_refuses_layer_lists():
     z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
     i32 = torch.int32
-    good = dict(q=z(4, 8, 128), cu_q_lens=z(2, dt=i32), parents=z(4, dt=i32), k_cache=z(3, 2, 16, 128),
-                v_cache=z(3, 2, 16, 128), block_tables=z(1, 3, dt=i32), ctx_lens=z(1, dt=i32), max_q_len=4,
-                max_kv_len=20, scale=0.1)
-    for name, bad in (("parents", z(5, dt=i32)), ("cu_q_lens", z(3, dt=i32)), ("v_cache", z(3, 2, 16, 64)),
-                      ("k_cache", z(3, 2, 16, 64)), ("block_tables", z(2, 3, dt=i32)), ("out", z(3, 8, 128))):
-        with pytest.raises(ValueError, match=name):
-            pa.pa_decode_tree(**dict(good, **{name: bad}))
-    with pytest.raises(TypeError):
-        pa.pa_decode_tree(**dict(good, q=z(4, 8, 128, dt=torch.float64)))
     with pytest.raises(ValueError, match="same layers"):
         pa.pa_compact_tree([z(3, 2, 16, 64)], [], z(1, 3, dt=i32), z(1, dt=i32), z(1, 4, dt=i32), z(1, dt=i32))
