@@ -57,7 +57,10 @@ struct TreeParams {
   int32_t tile_rows;  // rows of a query tile in use: a multiple of the group, or any number (fp32)
   int32_t tile_m;     // rows of a partial tile in the workspace
   int32_t tile_keys;
-  int32_t min_tiles;  // a CTA takes at least this many key tiles, if there are any
+  // A key tile's time in pieces of the join: splitting a unit of n tiles into
+  // pieces of t costs t * piece_cost + n / t, so a CTA takes at least
+  // sqrt(n / piece_cost) tiles.
+  int32_t piece_cost;
   float scale_log2;
   TreeMerge* merge;   // [ctas]
   float* part_o;      // [2 * ctas][tile_m][head_dim]
@@ -106,31 +109,39 @@ struct TreeRange {
 
 // The scan: threads 0 .. THREADS-1 of the CTA (all of them) sum the tiles of
 // a run of sequences each; the one whose run holds the CTA's first tile
-// walks it. `sm` is THREADS / 32 + 4 words of 8 bytes.
+// walks it. `sm` is THREADS / 16 + 2 words of 8 bytes.
 template <int THREADS>
 __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int per = (p.num_seqs + THREADS - 1) / THREADS;
   const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += tree_seq(p, s, blockIdx.x == 0).tiles(p);
+  int64_t mine = 0, my_units = 0;
+  for (int s = s0; s < s1; ++s) {
+    const TreeSeq q = tree_seq(p, s, blockIdx.x == 0);
+    mine += q.tiles(p);
+    my_units += q.qtiles;
+  }
   int64_t x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) sm[w] = x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) my_units += __shfl_xor_sync(0xffffffffu, my_units, o);
+  if (lane == 31) sm[w] = x, sm[THREADS / 32 + w] = my_units;
   __syncthreads();
-  int64_t base = x - mine, total = 0;
+  int64_t base = x - mine, total = 0, units = 0;
   for (int i = 0; i < THREADS / 32; ++i) {
     const int64_t t = sm[i];
     if (i < w) base += t;
     total += t;
+    units += sm[THREADS / 32 + i] * p.num_kv_heads;
   }
   TreeRange r;
   r.total = total;
-  const int64_t most = (total + p.min_tiles - 1) / p.min_tiles;
+  const float least = sqrtf((float)total / ((float)max(units, (int64_t)1) * p.piece_cost));
+  const int64_t most = (int64_t)((float)total / fmaxf(1.f, least));
   r.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, most));
   r.begin = 0;
   r.left = 0;
@@ -140,7 +151,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm
     r.begin = total * blockIdx.x / r.ctas;
     r.left = total * (blockIdx.x + 1) / r.ctas - r.begin;
   }
-  int64_t* found = sm + THREADS / 32;
+  int64_t* found = sm + THREADS / 16;
   if (r.left > 0 && r.begin >= base && r.begin < base + mine) {
     int64_t at = base;
     for (int s = s0; s < s1; ++s) {
