@@ -157,6 +157,21 @@ int make_kv_tensor_map(CUtensorMap* map, const void* base, int64_t rows, int32_t
   return make_2d_tensor_map(map, base, rows, head_dim, head_dim, dt, box_rows, 64);
 }
 
+int make_kv_group_map(CUtensorMap* map, const void* base, int64_t rows, int32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return PA_ERR_CUDA;
+  // Rows of 256 bytes (128 16-bit elements, moved unchanged) as groups of
+  // eight rows x two 128-byte halves: (column, row in group, half, group).
+  cuuint64_t gdim[4] = {64u, 8u, 2u, (cuuint64_t)rows / 8};
+  cuuint64_t gstride[3] = {256u, 128u, 2048u};
+  cuuint32_t box[4] = {64u, 8u, 2u, (cuuint32_t)box_rows / 8};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), gdim, gstride, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
 static int32_t auto_partition(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t max_seq_len) {
   // Work items are (sequence, partition, KV head group); the persistent
   // decode kernel (two CTAs per SM) pulls them from a counter. Use the

@@ -191,6 +191,10 @@ int make_kv_tensor_map(CUtensorMap* map, const void* base, int64_t rows, int32_t
                        int32_t box_rows);
 // Same view of an e4m3 (one byte per element) pool: box = [box_rows rows][128 bytes].
 int make_u8_tensor_map(CUtensorMap* map, const void* base, int64_t rows, int32_t head_dim, int32_t box_rows);
+// A pool of 16-bit rows of head_dim 128: box = box_rows rows as [row group of
+// 8][64-column half][8 rows][64 elements], each 8 x 64 an atom of the 128-byte
+// swizzle; coordinates (0, 0, 0, row / 8).
+int make_kv_group_map(CUtensorMap* map, const void* base, int64_t rows, int32_t box_rows);
 // 3-D map over a [d2][d1][d0] tensor (d0 contiguous), box [b2][b1][b0], 128-byte swizzle.
 int make_3d_tensor_map(CUtensorMap* map, const void* base, int64_t d2, int64_t d1, int64_t d0, pa_dtype dt,
                        int32_t b2, int32_t b1, int32_t b0);

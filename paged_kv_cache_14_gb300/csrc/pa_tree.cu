@@ -275,9 +275,9 @@ __device__ __forceinline__ void join_rows(const TreeParams& p, const TreeMerge& 
   constexpr int LOOK = 32 / ROWS;  // pieces whose weights are at hand
   static_assert(LOOK % BATCH == 0, "whole batches");
   const int D = p.head_dim, lane = threadIdx.x & 31, parts = mg.parts;
-  // Piece k of row r: slot 2b + 1 for the first, 2 (b + k) for the others.
+  // Piece k of row r: slot 2b + 1 for the first, 2 (b + k team) for the others.
   auto slot = [&](int r, int k) -> int64_t {
-    return (int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * p.tile_m + r;
+    return (int64_t)(2 * (blockIdx.x + k * p.team) + (k == 0 ? 1 : 0)) * p.tile_m + r;
   };
   const int mr = min(r0 + lane / LOOK, rows - 1), mk = lane % LOOK;
   auto piece_ml = [&](int k) -> float2 {
@@ -400,7 +400,7 @@ bool aligned16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) ==
 // Tiles, grid and workspace of a call; what the size query and the launch share.
 struct TreeLayout {
   int rc = PA_OK;
-  int ctas = 0, tile_rows = 0, tile_m = 0, tile_keys = 0, piece_cost = 1;
+  int ctas = 0, tile_rows = 0, tile_m = 0, tile_keys = 0, team = 1, piece_cost = 1;
   size_t merge = 0, part_o = 0, part_ml = 0, total = 0;
 };
 
@@ -436,11 +436,15 @@ TreeLayout tree_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_hea
     w.tile_keys = kTreeTcKeys;
     w.piece_cost = 3;
     per_sm = 2;
+    // Teams of two where trees may fill several query tiles. An odd number of
+    // KV heads would leave a member idle at every odd last tile.
+    if ((int64_t)max_q_len * group > w.tile_rows && num_kv_heads % 2 == 0) w.team = 2;
   }
   // Most key tiles there can be: one more query tile than its rows fill for every sequence.
   const double units = ((double)total_q * group / w.tile_rows + std::min(num_seqs, total_q)) * num_kv_heads;
   const double most = units * ((max_kv_len + w.tile_keys - 1) / w.tile_keys) + 1;
   w.ctas = (int)std::max(1.0, std::min(most, (double)per_sm * num_sms_current_device()));
+  w.ctas = (w.ctas + w.team - 1) / w.team * w.team;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   w.part_o = up((size_t)w.ctas * sizeof(TreeMerge));
   w.part_ml = up(w.part_o + (size_t)2 * w.ctas * w.tile_m * head_dim * 4);
@@ -496,6 +500,7 @@ int decode_tree(const void* q, int32_t total_q, const int32_t* cu_q_lens, const 
   p.tile_rows = w.tile_rows;
   p.tile_m = w.tile_m;
   p.tile_keys = w.tile_keys;
+  p.team = w.team;
   p.piece_cost = w.piece_cost;
   p.scale_log2 = scale * 1.4426950408889634f;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

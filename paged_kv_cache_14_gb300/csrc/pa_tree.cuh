@@ -13,6 +13,14 @@
 // earlier CTA, slot 2b + 1 that of a unit begun here. So the partials need
 // 2 N tiles whatever the batch is, and there is no plan kernel: every CTA
 // finds its place with a scan of the lengths.
+//
+// Where trees fill more than one query tile, the tiles of one KV head read
+// the same keys. One after another they would read them from HBM again (304
+// CTAs' keys do not stay in L2: 2.4 TB read per TB of keys, 403 us for the
+// 70B-shaped batch of wide trees), so CTAs then work in teams of two on the
+// line: a place on it is two query tiles of one KV head, member r taking the
+// tile 2 i + r, and an odd last tile's place is two KV heads. The members run
+// side by side, and the second read of a key tile finds it in L2.
 #pragma once
 
 #include "pa_common.cuh"
@@ -31,6 +39,7 @@ struct TreeMerge {
   int32_t qt;
   int32_t pad[3];
 };
+static_assert(sizeof(TreeMerge) == 32, "laid out in the workspace");
 
 struct TreeParams {
   const void* q;
@@ -57,6 +66,7 @@ struct TreeParams {
   int32_t tile_rows;  // rows of a query tile in use: a multiple of the group, or any number (fp32)
   int32_t tile_m;     // rows of a partial tile in the workspace
   int32_t tile_keys;
+  int32_t team;       // CTAs that share a place on the line: 1 or 2
   // A key tile's time in pieces of the join: splitting a unit of n tiles into
   // pieces of t costs t * piece_cost + n / t, so a CTA takes at least
   // sqrt(n / piece_cost) tiles.
@@ -68,13 +78,11 @@ struct TreeParams {
   int* status;
 };
 
-// Work of one sequence: key tiles and query tiles; 0 units for an empty or
-// illegal one.
+// Work of one sequence: key tiles, query tiles and places (units of a team);
+// none for an empty or illegal one.
 struct TreeSeq {
-  int q0, nodes, ctx, ktiles, qtiles;
-  __device__ __forceinline__ int64_t tiles(const TreeParams& p) const {
-    return (int64_t)ktiles * qtiles * p.num_kv_heads;
-  }
+  int q0, nodes, ctx, ktiles, qtiles, places;
+  __device__ __forceinline__ int64_t tiles() const { return (int64_t)ktiles * places; }
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int i, bool report) {
@@ -83,7 +91,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int i, bool rep
   const int64_t n = (int64_t)p.cu_q_lens[i + 1] - s.q0;
   s.ctx = p.ctx_lens[i];
   s.nodes = 0;
-  s.ktiles = s.qtiles = 0;
+  s.ktiles = s.qtiles = s.places = 0;
   const int64_t kv = s.ctx + n;
   const int64_t cap = min((int64_t)p.max_kv_len, (int64_t)p.max_blocks_per_seq * p.block_size);
   if (n == 0) return s;
@@ -94,15 +102,18 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int i, bool rep
   s.nodes = (int)n;
   s.ktiles = (int)((kv + p.tile_keys - 1) / p.tile_keys);
   s.qtiles = (int)((n * p.group + p.tile_rows - 1) / p.tile_rows);
+  s.places = p.team == 1 ? s.qtiles * p.num_kv_heads
+                         : (s.qtiles >> 1) * p.num_kv_heads + (s.qtiles & 1) * ((p.num_kv_heads + 1) >> 1);
   return s;
 }
 
-// A CTA's place on the line of tiles.
+// A team's place on the line of tiles.
 struct TreeRange {
-  int64_t begin;  // first tile of this CTA
-  int64_t left;   // tiles of this CTA
+  int64_t begin;  // first tile of this team
+  int64_t left;   // tiles of this team
   int64_t total;  // tiles of the batch
-  int ctas;       // CTAs that share it
+  int teams;      // teams that share it
+  int team;       // this CTA's
   int seq;        // sequence that holds the first tile, and the tile's place in it
   int64_t off;
 };
@@ -118,8 +129,8 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm
   int64_t mine = 0, my_units = 0;
   for (int s = s0; s < s1; ++s) {
     const TreeSeq q = tree_seq(p, s, blockIdx.x == 0);
-    mine += q.tiles(p);
-    my_units += q.qtiles;
+    mine += q.tiles();
+    my_units += q.places;
   }
   int64_t x = mine;
 #pragma unroll
@@ -136,26 +147,27 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm
     const int64_t t = sm[i];
     if (i < w) base += t;
     total += t;
-    units += sm[THREADS / 32 + i] * p.num_kv_heads;
+    units += sm[THREADS / 32 + i];
   }
   TreeRange r;
   r.total = total;
   const float least = sqrtf((float)total / ((float)max(units, (int64_t)1) * p.piece_cost));
   const int64_t most = (int64_t)((float)total / fmaxf(1.f, least));
-  r.ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, most));
+  r.teams = (int)max((int64_t)1, min((int64_t)(gridDim.x / p.team), most));
+  r.team = blockIdx.x / p.team;
   r.begin = 0;
   r.left = 0;
   r.seq = 0;
   r.off = 0;
-  if ((int)blockIdx.x < r.ctas) {
-    r.begin = total * blockIdx.x / r.ctas;
-    r.left = total * (blockIdx.x + 1) / r.ctas - r.begin;
+  if (r.team < r.teams) {
+    r.begin = total * r.team / r.teams;
+    r.left = total * (r.team + 1) / r.teams - r.begin;
   }
   int64_t* found = sm + THREADS / 16;
   if (r.left > 0 && r.begin >= base && r.begin < base + mine) {
     int64_t at = base;
     for (int s = s0; s < s1; ++s) {
-      const int64_t t = tree_seq(p, s, false).tiles(p);
+      const int64_t t = tree_seq(p, s, false).tiles();
       if (r.begin < at + t) {
         found[0] = s;
         found[1] = r.begin - at;
@@ -191,24 +203,37 @@ struct TreeWalk {
   __device__ __forceinline__ explicit TreeWalk(const TreeRange& range)
       : r(range), at(range.begin), seq(range.seq), off(range.off), left(range.left) {}
   __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& c) {
-    if (left <= 0) return false;
-    c.s = tree_seq(p, seq, false);
-    while (off >= c.s.tiles(p)) {  // also steps over sequences without work
-      off -= c.s.tiles(p);
-      c.s = tree_seq(p, ++seq, false);
+    while (left > 0) {
+      c.s = tree_seq(p, seq, false);
+      while (off >= c.s.tiles()) {  // also steps over sequences without work
+        off -= c.s.tiles();
+        c.s = tree_seq(p, ++seq, false);
+      }
+      c.seq = seq;
+      const int place = (int)(off / c.s.ktiles);
+      c.t0 = (int)(off - (int64_t)place * c.s.ktiles);
+      c.t1 = (int)min((int64_t)c.s.ktiles, c.t0 + left);
+      if (p.team == 1) {
+        c.kvh = place / c.s.qtiles;
+        c.qt = place - c.kvh * c.s.qtiles;
+      } else {
+        const int r = blockIdx.x & 1, pairs = c.s.qtiles >> 1;
+        if (place < pairs * p.num_kv_heads) {
+          c.kvh = place / pairs;
+          c.qt = 2 * (place - c.kvh * pairs) + r;
+        } else {
+          c.kvh = 2 * (place - pairs * p.num_kv_heads) + r;
+          c.qt = c.s.qtiles - 1;
+        }
+      }
+      c.at = at;
+      const int n = c.t1 - c.t0;
+      off += n;
+      at += n;
+      left -= n;
+      if (c.kvh < p.num_kv_heads) return true;  // (else an odd last head: nothing for this member)
     }
-    c.seq = seq;
-    const int unit = (int)(off / c.s.ktiles);
-    c.t0 = (int)(off - (int64_t)unit * c.s.ktiles);
-    c.t1 = (int)min((int64_t)c.s.ktiles, c.t0 + left);
-    c.kvh = unit / c.s.qtiles;
-    c.qt = unit - c.kvh * c.s.qtiles;
-    c.at = at;
-    const int n = c.t1 - c.t0;
-    off += n;
-    at += n;
-    left -= n;
-    return true;
+    return false;
   }
 };
 
@@ -216,11 +241,11 @@ struct TreeWalk {
 __device__ __forceinline__ int tree_slot(const TreePiece& c) { return 2 * blockIdx.x + (c.t0 == 0 ? 1 : 0); }
 
 __device__ __forceinline__ void tree_note_merge(const TreeParams& p, const TreeRange& r, const TreePiece& c) {
-  // CTA of tile w: the b with floor(W b / N) <= w, the largest such b.
+  // Team of tile w: the b with floor(W b / N) <= w, the largest such b.
   const int64_t last = c.at - c.t0 + c.s.ktiles - 1;
-  const int64_t e = ((last + 1) * r.ctas - 1) / r.total;
+  const int64_t e = ((last + 1) * r.teams - 1) / r.total;
   TreeMerge m;
-  m.parts = (int)(e - blockIdx.x + 1);
+  m.parts = (int)(e - r.team + 1);
   m.q0 = c.s.q0;
   m.nodes = c.s.nodes;
   m.kvh = c.kvh;

@@ -10,8 +10,8 @@
 // rows are all in use or not. Two CTAs share an SM: one's prologue, epilogue
 // and piece switches run under the other's stream.
 //
-//   warp 0      producer: Q tile of each piece, K and V tiles through the
-//               block table into rings of NK and NV stages;
+//   warps 0, 6  producers: Q tile of each piece and K tiles, V tiles, through
+//               the block table into rings of NK and NV stages;
 //   warp 1      tensor memory (256 columns: two S tiles of 64, O of head_dim)
 //               and, one lane, the MMAs: S(g) before O += P(g-1) V(g-1), so the
 //               softmax of a tile runs under the next tile's S;
@@ -20,7 +20,7 @@
 //               tree, running max and sum in registers, P (16-bit) over S, O
 //               rescaled in tensor memory when the max has moved by more than
 //               2^8, and the output or partial at the end of a piece;
-//   warps 6-7   (8-bit cache) widen the codes of each stage to fp16 in place
+//   warps 7-9   (8-bit cache) widen the codes of each stage to fp16 in place
 //               and move a bf16 Q tile into fp16, a power of two per row.
 // All roles walk the CTA's pieces; stages, S tiles and their barriers are
 // counted over all tiles of the CTA, so the rings run on across pieces.
@@ -50,13 +50,24 @@ constexpr int kN = 64;
 constexpr int kHalf = kN * 128;       // 64 columns of a K / V tile: 64 rows of 128 bytes
 constexpr int kQHalf = kM * 128;
 constexpr int kSoftmaxWarp0 = 2;
-constexpr int kConvWarp0 = 6;
-constexpr int kConvWarps = 2;
-template <int D>
+constexpr int kVWarp = 6;
+constexpr int kConvWarp0 = 7;
+constexpr int kConvK = 2;              // warps that widen K; one more widens V
+constexpr int kConvWarps = kConvK + 1;
+constexpr int kQSlots = 3;            // pieces whose Q exponents are kept (8-bit cache)
+constexpr int kScaleSlots = 8;        // tiles whose scales are kept (8-bit cache)
+template <int D, bool KV8>
 struct Cfg {
   static constexpr int kH = D / 64;            // 64-column halves
-  static constexpr int NK = D == 64 ? 6 : 3;   // stages
-  static constexpr int NV = D == 64 ? 5 : 2;
+  // K / V stage: groups of eight rows of 128 bytes (the swizzle's atom). At
+  // head_dim 128 a 16-bit group's two halves lie side by side, so that one copy
+  // brings a whole block; codes are widened in place, a row's lower half into
+  // the stage's first 8 KB and its upper half over the codes.
+  static constexpr int kGroup = D == 128 && !KV8 ? 2048 : 1024;  // distance of groups
+  static constexpr int kHalfOff = KV8 ? kHalf : 1024;            // of a group's halves
+  // Stages. A V tile waits for the softmax of its keys, a K tile does not.
+  static constexpr int NK = D == 64 ? 5 : 2;
+  static constexpr int NV = D == 64 ? 6 : 3;
   static constexpr int kStage = kH * kHalf;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kH * kQHalf;
@@ -68,23 +79,26 @@ struct Cfg {
   // a wait for tile g then cannot meet tile g - 1's phase, and tile g - 2's is
   // over once S(g) is known to be computed.
   static constexpr int kBarS = 4, kBarP = 6, kBarPv = 8;
-  // 8-bit cache: piece i's Q is in fp16 (i % 4: the MMAs may be two pieces of
+  // 8-bit cache: piece i's Q is in fp16 (i % 3: the MMAs may be two pieces of
   // one tile each ahead of the softmax, which waits for it too).
   static constexpr int kBarQConv = 10;
-  static constexpr int kBarKFull = 14, kBarKEmpty = kBarKFull + NK, kBarKCode = kBarKEmpty + NK;
+  static constexpr int kBarKFull = 13, kBarKEmpty = kBarKFull + NK, kBarKCode = kBarKEmpty + NK;
   static constexpr int kBarVFull = kBarKCode + NK, kBarVEmpty = kBarVFull + NV, kBarVCode = kBarVEmpty + NV;
   static constexpr int kNumBars = kBarVCode + NV;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tensor-memory base, any-poison flag
   static constexpr int kOffPoison = kOffMisc + 16;          // node bits; before that the scan's scratch
-  static constexpr int kOffQExp = kOffPoison + kMaxTreeNodes / 8;
-  static constexpr int kSmem16 = kOffQExp;
-  static constexpr int kSmem8 = kOffQExp + 4 * kM;          // exponents of the Q rows of four pieces
+  static constexpr int kOffScale = kOffPoison + kMaxTreeNodes / 8;  // [kScaleSlots][kN / 16] (K, V)
+  static constexpr int kOffQExp = kOffScale + (KV8 ? kScaleSlots * (kN / 16) * 8 : 0);
+  static constexpr int kSmem = kOffQExp + (KV8 ? kQSlots * kM : 0);
 };
-static_assert(Cfg<128>::kSmem8 <= 115712, "two CTAs per SM");
+static_assert(Cfg<128, true>::kSmem <= 115712 && Cfg<128, false>::kSmem <= 115712, "two CTAs per SM");
 constexpr int kTmemCols = 256;
 constexpr int kColO = 2 * kN;
 template <bool KV8>
-__host__ __device__ constexpr int threads() { return KV8 ? 256 : 192; }
+__host__ __device__ constexpr int threads() { return KV8 ? 320 : 224; }
+static_assert((threads<false>() / 16 + 2) * 8 <= Cfg<64, false>::kSmem - Cfg<64, false>::kOffPoison &&
+                  (threads<true>() / 16 + 2) * 8 <= Cfg<128, true>::kSmem - Cfg<128, true>::kOffPoison,
+              "the scan's scratch");
 }  // namespace tt
 
 // mbar_wait by a whole warp: the same answer in every lane.
@@ -109,7 +123,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
     tree_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
   using namespace tt;
-  using C = Cfg<D>;
+  using C = Cfg<D, KV8>;
   using MT = typename std::conditional<KV8, __half, T>::type;  // the MMA's 16-bit type
   constexpr bool kBf16 = std::is_same<MT, __nv_bfloat16>::value;
   constexpr uint32_t kIdescS = idesc_f16(kM, kN, kBf16, false);
@@ -129,7 +143,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
     if ((sbase & 1023u) != 0) record_error(p.status, PA_ERR_ALIGN);
     mbar_init(bar(C::kBarQFull), 1);
     mbar_init(bar(C::kBarQEmpty), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(bar(C::kBarQConv + i), kConvWarps);
+    for (int i = 0; i < kQSlots; ++i) mbar_init(bar(C::kBarQConv + i), kConvWarps);
     mbar_init(bar(C::kBarSoft), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kBarS + i), 1);
@@ -137,12 +151,12 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
       mbar_init(bar(C::kBarPv + i), 1);
     }
     for (int i = 0; i < C::NK; ++i) {
-      mbar_init(bar(C::kBarKFull + i), KV8 ? kConvWarps : 1);
+      mbar_init(bar(C::kBarKFull + i), KV8 ? kConvK : 1);
       mbar_init(bar(C::kBarKEmpty + i), 1);
       mbar_init(bar(C::kBarKCode + i), 1);
     }
     for (int i = 0; i < C::NV; ++i) {
-      mbar_init(bar(C::kBarVFull + i), KV8 ? kConvWarps : 1);
+      mbar_init(bar(C::kBarVFull + i), 1);
       mbar_init(bar(C::kBarVEmpty + i), 1);
       mbar_init(bar(C::kBarVCode + i), 1);
     }
@@ -171,10 +185,19 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
   int piece = 0;
   if ((sbase & 1023u) != 0) {
     // (misaligned shared memory, reported above: nothing can run)
-  } else if (warp == 0) {
-    // ============================== producer ==============================
+  } else if (warp == 0 || warp == kVWarp) {
+    // ============================= producers ==============================
+    // Issuing a copy takes its warp about 80 cycles, and a wait 200, so K (with
+    // Q) and V have a warp each: with one for both, the 8-bit kernel's tiles
+    // were spaced by their issue (2000 of 3300 cycles).
+    const bool is_v = warp == kVWarp;
+    const int ns = is_v ? C::NV : C::NK;
+    const CUtensorMap* map = is_v ? &vmap : &kmap;
+    const int full0 = KV8 ? (is_v ? C::kBarVCode : C::kBarKCode) : (is_v ? C::kBarVFull : C::kBarKFull);
+    const int empty0 = is_v ? C::kBarVEmpty : C::kBarKEmpty;
+    const uint32_t stage0 = sbase + (is_v ? C::kOffV : C::kOffK) + (KV8 ? kHalf : 0);
     bool bad = false;
-    int q_issued = 0, k_issued = 0, v_issued = 0;
+    int q_issued = 0;
     while (!bad && walk.next(p, c)) {
       const int32_t* table = p.block_tables + (int64_t)c.seq * p.max_blocks_per_seq;
       const int nblk = (c.kv_len() + BS - 1) / BS;
@@ -189,41 +212,54 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           id = table[b];
           if (id < 0 || id >= p.num_blocks) {
             record_error(p.status, PA_ERR_BLOCK_OOB);
-            id = 0;
+            id = -1;
           }
         }
         return id;
       };
-      int id_cur = load_batch(c.t0), id_next = load_batch(c.t0 + kBatch);
-      auto issue = [&](int gi, int first_lane, bool is_v) {  // one K or V tile
-        const int ns = is_v ? C::NV : C::NK, st = gi % ns;
-        const uint32_t full = bar((KV8 ? (is_v ? C::kBarVCode : C::kBarKCode) : (is_v ? C::kBarVFull : C::kBarKFull)) + st);
-        const uint32_t empty = bar((is_v ? C::kBarVEmpty : C::kBarKEmpty) + st);
-        constexpr int kBoxes = KV8 ? 1 : C::kH;  // boxes per block
-        const int u = lane / kBoxes, h = lane - u * kBoxes;
-        const int id = __shfl_sync(0xffffffffu, id_cur, first_lane + (u < kBlocks ? u : 0));
-        if (lane == 0) {
-          if (gi >= ns && !mbar_wait(empty, ((gi / ns) & 1) ^ 1, p.status)) bad = true;
-          else mbar_arrive_expect_tx(full, kBlocks * kBoxes * BS * 128);
-        }
-        bad = __shfl_sync(0xffffffffu, bad, 0);
-        if (bad) return;
-        if (u < kBlocks) {
-          const int row = (id * p.num_kv_heads + c.kvh) * BS;
-          const uint32_t dst = sbase + (is_v ? C::kOffV : C::kOffK) + st * C::kStage + (KV8 ? kHalf : h * kHalf) + u * BS * 128;
-          tma_load_2d(dst, is_v ? &vmap : &kmap, h * 64, row, full);
-        }
-        if (is_v) v_issued = gi + 1;
-        else k_issued = gi + 1;
+      // 8-bit cache: the (K, V) scales of a batch's blocks, 0 where there is
+      // none, requested with the batch.
+      auto load_scales = [&](int t, int id) -> float2 {
+        float2 r = make_float2(0.f, 0.f);
+        if (KV8 && !is_v && t * kBlocks + lane < nblk && t < c.t1 && id >= 0)
+          r = __ldg(reinterpret_cast<const float2*>(p.kv_scales) + (int64_t)id * p.num_kv_heads + c.kvh);
+        return r;
       };
+      int id_cur = load_batch(c.t0), id_next = load_batch(c.t0 + kBatch);
+      float2 sc_cur = load_scales(c.t0, id_cur), sc_next = make_float2(0.f, 0.f);
       for (int t = c.t0; t < c.t1 && !bad; ++t, ++g) {
         const int in = (t - c.t0) % kBatch;
         if (t > c.t0 && in == 0) {
           id_cur = id_next;
+          sc_cur = sc_next;
           id_next = load_batch(t + kBatch);
         }
-        issue(g, in * kBlocks, false);
-        if (t == c.t0 && !bad) {
+        if (KV8 && in == kBatch / 2) sc_next = load_scales(t - in + kBatch, id_next);
+        const int st = g % ns;
+        const uint32_t full = bar(full0 + st);
+        if (lane == 0) {
+          if (g >= ns && !mbar_wait(bar(empty0 + st), ((g / ns) & 1) ^ 1, p.status)) bad = true;
+        }
+        bad = __shfl_sync(0xffffffffu, bad, 0);
+        if (bad) break;
+        if constexpr (KV8) {
+          // Group u's scales, for the softmax: published by the arrival below.
+          if (!is_v && lane >= in * kBlocks && lane < (in + 1) * kBlocks) {
+            float2* to = reinterpret_cast<float2*>(smem + C::kOffScale) + (g % kScaleSlots) * (kN / 16);
+#pragma unroll
+            for (int i = 0; i < BS / 16; ++i) to[(lane - in * kBlocks) * (BS / 16) + i] = sc_cur;
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? kHalf : C::kStage);
+        const int id = __shfl_sync(0xffffffffu, id_cur, in * kBlocks + lane % kBlocks);
+        if (lane < kBlocks) {
+          const int row = (max(id, 0) * p.num_kv_heads + c.kvh) * BS;
+          const uint32_t dst = stage0 + st * C::kStage + lane * (BS / 8) * (KV8 ? 1024 : C::kGroup);
+          if constexpr (D == 128 && !KV8) tma_load_4d(dst, map, 0, 0, 0, row / 8, full);
+          else tma_load_2d(dst, map, 0, row, full);
+        }
+        if (!is_v && t == c.t0) {
           // Q after the piece's first K tile: its place is free once the
           // previous piece's last S has been computed.
           if (lane == 0) {
@@ -240,27 +276,22 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           }
           bad = __shfl_sync(0xffffffffu, bad, 0);
         }
-        if (!bad) issue(g, in * kBlocks, true);
       }
       ++piece;
     }
-    if (bad) {
-      if (lane == 0) {  // copies in flight land before the CTA ends
-        if (q_issued > 0) mbar_wait(bar(C::kBarQFull), (q_issued - 1) & 1, nullptr);
-        for (int j = max(0, k_issued - C::NK); j < k_issued; ++j)
-          mbar_wait(bar((KV8 ? C::kBarKCode : C::kBarKFull) + j % C::NK), (j / C::NK) & 1, nullptr);
-        for (int j = max(0, v_issued - C::NV); j < v_issued; ++j)
-          mbar_wait(bar((KV8 ? C::kBarVCode : C::kBarVFull) + j % C::NV), (j / C::NV) & 1, nullptr);
-      }
+    if (bad && lane == 0) {  // copies in flight land before the CTA ends
+      if (q_issued > 0) mbar_wait(bar(C::kBarQFull), (q_issued - 1) & 1, nullptr);
+      for (int j = max(0, g - ns); j < g; ++j) mbar_wait(bar(full0 + j % ns), (j / ns) & 1, nullptr);
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ================================ MMA =================================
     if (lane == 0) {
       bool bad = false;
       uint32_t last_bar = 0, last_phase = 0;  // the last commit covers every MMA before it
       const uint64_t dq = sdesc_sw128(sbase + C::kOffQ, 16, 1024);
-      const uint64_t dk = sdesc_sw128(sbase + C::kOffK, 16, 1024);
-      const uint64_t dv = sdesc_sw128(sbase + C::kOffV, kHalf, 1024);
+      const uint64_t dk = sdesc_sw128(sbase + C::kOffK, 16, C::kGroup);
+      const uint64_t dv = sdesc_sw128(sbase + C::kOffV, C::kHalfOff, C::kGroup);
       auto commit = [&](uint32_t b, int phase) {
         tc_commit(b);
         last_bar = b;
@@ -273,7 +304,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
         const uint64_t va = dv + (uint64_t)((j % C::NV) * (C::kStage >> 4));
 #pragma unroll
         for (int k = 0; k < kN / 16; ++k)
-          tc_mma_f16_ta(tmem + kColO, tmem + (j & 1) * kN + k * 8, va + ((k * 2048) >> 4), kIdescO,
+          tc_mma_f16_ta(tmem + kColO, tmem + (j & 1) * kN + k * 8, va + ((k * 2 * C::kGroup) >> 4), kIdescO,
                         !first || k > 0 ? 1u : 0u);
         commit(bar(C::kBarVEmpty + j % C::NV), j / C::NV);
         commit(bar(C::kBarPv + (j & 1)), j >> 1);
@@ -283,7 +314,8 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
       while (!bad && walk.next(p, c)) {
         // The previous piece's last product does not wait for this piece's Q.
         if (g > 0 && !issue_pv(g - 1, first_prev)) bad = true;
-        if (!bad && !mbar_wait(KV8 ? bar(C::kBarQConv + (piece & 3)) : bar(C::kBarQFull), KV8 ? (piece >> 2) & 1 : piece & 1, p.status)) bad = true;
+        if (!bad && !mbar_wait(KV8 ? bar(C::kBarQConv + piece % kQSlots) : bar(C::kBarQFull),
+                                KV8 ? (piece / kQSlots) & 1 : piece & 1, p.status)) bad = true;
         for (int t = c.t0; t < c.t1 && !bad; ++t, ++g) {
           if (!mbar_wait(bar(C::kBarKFull + g % C::NK), (g / C::NK) & 1, p.status)) {
             bad = true;
@@ -294,7 +326,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             tc_mma_f16(tmem + (g & 1) * kN, dq + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4),
-                       ka + (((k >> 2) * kHalf + (k & 3) * 32) >> 4), kIdescS, k > 0);
+                       ka + (((k >> 2) * C::kHalfOff + (k & 3) * 32) >> 4), kIdescS, k > 0);
           commit(bar(C::kBarS + (g & 1)), g >> 1);
           commit(bar(C::kBarKEmpty + g % C::NK), g / C::NK);
           if (t + 1 == c.t1) commit(bar(C::kBarQEmpty), piece);
@@ -317,7 +349,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
         if (!bad && std::is_same<T, __nv_bfloat16>::value) {
           // bf16 rows into fp16: x 2^-sh, sh from the row's largest magnitude
           // (then below 2^15), so what lies within 2^24 of it stays exact.
-          uint8_t* qexp = smem + C::kOffQExp + (piece & 3) * kM;
+          uint8_t* qexp = smem + C::kOffQExp + piece % kQSlots * kM;
           for (int r = ct; r < kM; r += 32 * kConvWarps) {
             uint8_t* rb = smem + C::kOffQ + r * 128;
             auto chunk = [&](int i) { return reinterpret_cast<uint4*>(rb + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4)); };
@@ -346,18 +378,20 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::kBarQConv + (piece & 3)));
+        if (lane == 0) mbar_arrive(bar(C::kBarQConv + piece % kQSlots));
+        // The K warps take 32 rows each, the V warp all 64.
+        const bool is_v = ct >= 32 * kConvK;
+        const int ns = is_v ? C::NV : C::NK;
         for (int t = c.t0; t < c.t1 && !bad; ++t, ++g) {
+          const int st = g % ns;
+          if (!mbar_wait_warp(bar((is_v ? C::kBarVCode : C::kBarKCode) + st), (g / ns) & 1, p.status)) {
+            bad = true;
+            break;
+          }
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            const int ns = kv ? C::NV : C::NK, st = g % ns;
-            if (!mbar_wait_warp(bar((kv ? C::kBarVCode : C::kBarKCode) + st), (g / ns) & 1, p.status)) {
-              bad = true;
-              break;
-            }
+          for (int r = is_v ? lane : ct; r < kN; r += is_v ? 32 : 32 * kConvK) {
             // A row's codes lie where its widened upper half goes: read whole, then written.
-            const int r = ct;
-            uint8_t* base = smem + (kv ? C::kOffV : C::kOffK) + st * C::kStage + r * 128;
+            uint8_t* base = smem + (is_v ? C::kOffV : C::kOffK) + st * C::kStage + r * 128;
             uint4 cr[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) cr[i] = *reinterpret_cast<const uint4*>(base + kHalf + ((i ^ (r & 7)) << 4));
@@ -373,10 +407,10 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
               *reinterpret_cast<uint4*>(rb + ((cc ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
               *reinterpret_cast<uint4*>(rb + (((cc + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar((kv ? C::kBarVFull : C::kBarKFull) + st));
           }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar((is_v ? C::kBarVFull : C::kBarKFull) + st));
         }
         ++piece;
       }
@@ -415,45 +449,13 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
       constexpr int kKapUnset = 1 << 20;
       int kap = kKapUnset;
       float pw = 1.f;
-      auto load_scales = [&](int t) -> float2 {  // lane u < 4: the (K, V) scale of 16-key group u
-        float2 r = make_float2(0.f, 0.f);
-        if constexpr (KV8) {
-          const int pos = t * kN + lane * 16;
-          if (lane < kN / 16 && t < c.t1 && pos < kv_len) {
-            const int id = table[pos / BS];
-            if (id >= 0 && id < p.num_blocks)
-              r = __ldg(reinterpret_cast<const float2*>(p.kv_scales) + (int64_t)id * p.num_kv_heads + c.kvh);
-          }
-        }
-        return r;
-      };
-      float2 sc_next = load_scales(c.t0);
       if constexpr (KV8 && std::is_same<T, __nv_bfloat16>::value) {
-        if (!mbar_wait_warp(bar(C::kBarQConv + (piece & 3)), (piece >> 2) & 1, p.status)) bad = true;
-        rf = ldexpf(p.scale_log2, (int)smem[C::kOffQExp + (piece & 3) * kM + row] - 141);
+        if (!mbar_wait_warp(bar(C::kBarQConv + piece % kQSlots), (piece / kQSlots) & 1, p.status)) bad = true;
+        rf = ldexpf(p.scale_log2, (int)smem[C::kOffQExp + piece % kQSlots * kM + row] - 141);
       }
       for (int t = c.t0; t < c.t1 && !bad; ++t, ++g) {
         const int k0 = t * kN;
         const uint32_t ts = tl + (g & 1) * kN, to = tl + kColO;
-        float2 sc = sc_next;
-        float kap_r = 1.f;
-        if constexpr (KV8) {
-          sc_next = load_scales(t + 1);
-          float vmax = sc.y;
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-          vmax = __shfl_sync(0xffffffffu, vmax, 0);
-          if (vmax > 0.f) {
-            // 2^kap brings the largest V scale seen so far below 2^7.
-            const int ex = (int)((__float_as_uint(vmax) >> 23) & 0xffu) - 126;
-            const int kmax = min(7 - ex, 127);
-            if (kmax < kap) {
-              if (kap != kKapUnset) kap_r = __uint_as_float((uint32_t)(max(kmax - kap, -126) + 127) << 23);
-              kap = kmax;
-              pw = __uint_as_float((uint32_t)(kmax + 127) << 23);
-            }
-          }
-        }
         if (!mbar_wait_warp(bar(C::kBarS + (g & 1)), (g >> 1) & 1, p.status)) {
           bad = true;
           break;
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           uint8_t* vst = smem + C::kOffV + sv * C::kStage;
           for (int i = tid; i < (kN - first) * 8 * C::kH; i += 128) {
             const int r = first + i / (8 * C::kH), x = i % (8 * C::kH);
-            uint4* at = reinterpret_cast<uint4*>(vst + (x >> 3) * kHalf + r * 128 + (x & 7) * 16);
+            uint4* at = reinterpret_cast<uint4*>(vst + (r >> 3) * C::kGroup + (x >> 3) * C::kHalfOff + (r & 7) * 128 + (x & 7) * 16);
             if (k0 + r >= kv_len) {
               *at = make_uint4(0, 0, 0, 0);
             } else {
@@ -490,50 +492,39 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           __syncwarp();
         }
         if (live) {
-          uint32_t sr[kN];
-          tmem_ld32(ts, reinterpret_cast<uint32_t(&)[32]>(sr[0]));
-          tmem_ld32(ts + 32, reinterpret_cast<uint32_t(&)[32]>(sr[32]));
-          tmem_ld_wait();
-          if constexpr (KV8) {
-#pragma unroll
-            for (int u = 0; u < kN / 16; ++u) {
-              const float f = __shfl_sync(0xffffffffu, sc.x, u) * rf;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) sr[u * 16 + i] = __float_as_uint(__uint_as_float(sr[u * 16 + i]) * f);
-            }
-          }
-          if (k0 + kN > ctx) {
+          // Keys that the row sees, in tiles that reach into the tree.
+          uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+          const bool masked = k0 + kN > ctx;
+          if (masked) {
             const int first = k0 - ctx;  // node of the tile's first key (below 0: context)
-            uint32_t lo = tree_ancestors(parents, used ? node : -1, first);
-            uint32_t hi = tree_ancestors(parents, used ? node : -1, first + 32);
+            seen[0] = tree_ancestors(parents, used ? node : -1, first);
+            seen[1] = tree_ancestors(parents, used ? node : -1, first + 32);
             if (first < 0) {
-              lo |= first > -32 ? (1u << -first) - 1u : 0xffffffffu;
-              if (first < -32) hi |= (1u << (-first - 32)) - 1u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (!((lo >> i) & 1u)) sr[i] = __float_as_uint(-CUDART_INF_F);
-              if (!((hi >> i) & 1u)) sr[32 + i] = __float_as_uint(-CUDART_INF_F);
+              seen[0] |= first > -32 ? (1u << -first) - 1u : 0xffffffffu;
+              if (first < -32) seen[1] |= (1u << (-first - 32)) - 1u;
             }
             __syncwarp();  // (the walks differ in length)
           }
-          float mx = -CUDART_INF_F;
+          auto mask = [&](uint32_t (&v)[32], uint32_t bits) {
 #pragma unroll
-          for (int i = 0; i < kN; i += 2) mx = fmax3(mx, __uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) v[i] = __float_as_uint(-CUDART_INF_F);
+          };
+          // alpha takes the row to a larger maximum: only when it has moved by
+          // more than 2^8 (weights stay below 256), or from nothing.
           float alpha = 1.f;
-          if (m == -CUDART_INF_F) {
-            m = mx;
-          } else if ((mx - m) * sl2 > 8.f) {
-            alpha = fast_exp2((m - mx) * sl2);
-            m = mx;
-          }
-          const float oalpha = alpha * kap_r;  // O takes the drop of kap too, l does not
-          if (t > c.t0 && __any_sync(0xffffffffu, oalpha != 1.f)) {
-            // The previous product has been added before O changes.
-            if (!mbar_wait_warp(bar(C::kBarPv + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.status)) {
-              bad = true;
-              break;
+          auto update_max = [&](float mx) {
+            if (m == -CUDART_INF_F) {
+              m = mx;
+            } else if ((mx - m) * sl2 > 8.f) {
+              alpha = fast_exp2((m - mx) * sl2);
+              m = mx;
             }
+          };
+          // O times f, once the previous product has been added to it.
+          auto rescale = [&](float f) -> bool {
+            if (t == c.t0 || !__any_sync(0xffffffffu, f != 1.f)) return true;
+            if (!mbar_wait_warp(bar(C::kBarPv + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.status)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int i = 0; i < D / 16; ++i) {
@@ -541,27 +532,113 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
               tmem_ld16(to + i * 16, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * oalpha);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
               tmem_st16(to + i * 16, o);
             }
-          }
-          const float neg = m == -CUDART_INF_F ? 0.f : -m * sl2;
-          const uint64_t sl2x2 = f2_pack(sl2, sl2), negx2 = f2_pack(neg, neg);
+            return true;
+          };
           uint64_t rs2 = f2_pack(0.f, 0.f);
-          uint32_t pk[32];
+          if constexpr (!KV8) {
+            uint32_t sr[2][32];
+            tmem_ld32(ts, sr[0]);
+            tmem_ld32(ts + 32, sr[1]);
+            tmem_ld_wait();
+            if (masked) mask(sr[0], seen[0]), mask(sr[1], seen[1]);
+            float mx = -CUDART_INF_F;
 #pragma unroll
-          for (int u = 0; u < kN / 16; ++u) {
-            const float fv = KV8 ? __shfl_sync(0xffffffffu, sc.y, u) * pw : 1.f;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = u * 16; i < u * 16 + 16; i += 2) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sl2x2, negx2), x0, x1);
-              const float a = fast_exp2(x0), b = fast_exp2(x1);
-              rs2 = f2_add(rs2, f2_pack(a, b));
-              pk[i / 2] = KV8 ? MmaOp<MT>::pack(a * fv, b * fv) : MmaOp<MT>::pack(a, b);
+              for (int i = 0; i < 32; i += 2)
+                mx = fmax3(mx, __uint_as_float(sr[h][i]), __uint_as_float(sr[h][i + 1]));
+            update_max(mx);
+            if (!rescale(alpha)) {
+              bad = true;
+              break;
+            }
+            const float neg = m == -CUDART_INF_F ? 0.f : -m * sl2;
+            const uint64_t sl2x2 = f2_pack(sl2, sl2), negx2 = f2_pack(neg, neg);
+            uint32_t pk[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[h][i]), __uint_as_float(sr[h][i + 1])), sl2x2, negx2), x0,
+                          x1);
+                const float a = fast_exp2(x0), b = fast_exp2(x1);
+                rs2 = f2_add(rs2, f2_pack(a, b));
+                pk[h * 16 + i / 2] = MmaOp<MT>::pack(a, b);
+              }
+            tmem_st32(ts, pk);
+          } else {
+            // Two passes over the S row, 32 keys at a time (registers): the
+            // scores of 16-key group u are s * f_u, f_u >= 0, so a group's
+            // largest is its raw largest times f_u exactly.
+            const float2* scales = reinterpret_cast<const float2*>(smem + C::kOffScale) + (g % kScaleSlots) * (kN / 16);
+            float fk[kN / 16], fv[kN / 16], vmax = 0.f;
+#pragma unroll
+            for (int u = 0; u < kN / 16; ++u) {
+              const float2 x = scales[u];
+              fk[u] = x.x * rf;
+              fv[u] = x.y;
+              vmax = fmaxf(vmax, x.y);
+            }
+            float kap_r = 1.f;  // 2^(new kap - old kap) where kap drops
+            if (vmax > 0.f) {
+              // 2^kap brings the largest V scale seen so far below 2^7.
+              const int ex = (int)((__float_as_uint(vmax) >> 23) & 0xffu) - 126;
+              const int kmax = min(7 - ex, 127);
+              if (kmax < kap) {
+                if (kap != kKapUnset) kap_r = __uint_as_float((uint32_t)(max(kmax - kap, -126) + 127) << 23);
+                kap = kmax;
+                pw = __uint_as_float((uint32_t)(kmax + 127) << 23);
+              }
+            }
+            float mx = -CUDART_INF_F;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[32];
+              tmem_ld32(ts + h * 32, v);
+              tmem_ld_wait();
+              if (masked) mask(v, seen[h]);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                float x = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)
+                  x = fmax3(x, __uint_as_float(v[u * 16 + i]), __uint_as_float(v[u * 16 + i + 1]));
+                mx = fmaxf(mx, x == -CUDART_INF_F ? x : x * fk[h * 2 + u]);  // (-inf times a scale of 0)
+              }
+            }
+            update_max(mx);
+            if (!rescale(alpha * kap_r)) {  // O takes the drop of kap too, l does not
+              bad = true;
+              break;
+            }
+            const float neg = m == -CUDART_INF_F ? 0.f : -m;
+            const uint64_t negx2 = f2_pack(neg, neg);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[32], pk[16];
+              tmem_ld32(ts + h * 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float f = fk[h * 2 + i / 16], w = fv[h * 2 + i / 16] * pw;
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2_pack(f, f), negx2), x0,
+                          x1);
+                float a = fast_exp2(x0), b = fast_exp2(x1);
+                if (masked) {  // (a masked score may be anything)
+                  a = (seen[h] >> i) & 1u ? a : 0.f;
+                  b = (seen[h] >> (i + 1)) & 1u ? b : 0.f;
+                }
+                rs2 = f2_add(rs2, f2_pack(a, b));
+                pk[i / 2] = MmaOp<MT>::pack(a * w, b * w);
+              }
+              tmem_st16(ts + h * 16, pk);  // (columns already read)
             }
           }
-          tmem_st32(ts, pk);
           float rs0, rs1;
           f2_unpack(rs2, rs0, rs1);
           l = l * alpha + (rs0 + rs1);
@@ -660,11 +737,12 @@ static int run_tree_tc(const TreeParams& p, int ctas, pa_dtype dt, cudaStream_t 
   for (int i = 0; i < 2; ++i) {
     const void* pool = i ? p.v_cache : p.k_cache;
     CUtensorMap* map = i ? &vmap : &kmap;
-    rc = KV8 ? make_u8_tensor_map(map, pool, rows, D, BS) : make_kv_tensor_map(map, pool, rows, D, dt, BS);
+    rc = KV8 ? make_u8_tensor_map(map, pool, rows, D, BS)
+             : D == 128 ? make_kv_group_map(map, pool, rows, BS) : make_kv_tensor_map(map, pool, rows, D, dt, BS);
     if (rc != PA_OK) return rc;
   }
   auto kern = tree_tc_kernel<T, BS, D, KV8, E5>;
-  constexpr int smem = KV8 ? tt::Cfg<D>::kSmem8 : tt::Cfg<D>::kSmem16;
+  constexpr int smem = tt::Cfg<D, KV8>::kSmem;
   if (set_max_dynamic_smem(reinterpret_cast<const void*>(kern), smem) != PA_OK) return PA_ERR_CUDA;
   kern<<<ctas, tt::threads<KV8>(), smem, stream>>>(qmap, kmap, vmap, p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
