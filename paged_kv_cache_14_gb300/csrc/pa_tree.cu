@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(ts::kThreads, ts::per_sm(D)) tree_simt_kernel(
   const TreeRange range = tree_range<kThreads>(p, scan);
   if (threadIdx.x == 0) p.merge[blockIdx.x].parts = 0;
   const int row0 = threadIdx.x / kPer * kR, part = threadIdx.x % kPer;
-  TreeWalk walk(range);
+  TreeWalk walk(p, range);
   TreePiece c;
   while (walk.next(p, c)) {
     const int32_t* parents = p.parents + c.s.q0;

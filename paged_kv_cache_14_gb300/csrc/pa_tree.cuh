@@ -85,23 +85,30 @@ struct TreeSeq {
   __device__ __forceinline__ int64_t tiles() const { return (int64_t)ktiles * places; }
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int i, bool report) {
+// Lengths as they stand in memory (sequence i < num_seqs).
+struct TreeLens {
+  int q0, q1, ctx;
+};
+
+__device__ __forceinline__ TreeLens tree_lens(const TreeParams& p, int i) {
+  return {__ldg(p.cu_q_lens + i), __ldg(p.cu_q_lens + i + 1), __ldg(p.ctx_lens + i)};
+}
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, const TreeLens& r, bool report = false) {
   TreeSeq s;
-  s.q0 = p.cu_q_lens[i];
-  const int64_t n = (int64_t)p.cu_q_lens[i + 1] - s.q0;
-  s.ctx = p.ctx_lens[i];
-  s.nodes = 0;
-  s.ktiles = s.qtiles = s.places = 0;
-  const int64_t kv = s.ctx + n;
-  const int64_t cap = min((int64_t)p.max_kv_len, (int64_t)p.max_blocks_per_seq * p.block_size);
+  s.q0 = r.q0;
+  s.ctx = r.ctx;
+  s.nodes = s.ktiles = s.qtiles = s.places = 0;
+  const int64_t n = (int64_t)r.q1 - r.q0, kv = r.ctx + n;
   if (n == 0) return s;
-  if (n < 0 || s.q0 < 0 || s.q0 + n > p.total_q || n > p.max_q_len || s.ctx < 0 || kv > cap) {
+  if (n < 0 || r.q0 < 0 || r.q1 > p.total_q || n > p.max_q_len || r.ctx < 0 ||
+      kv > min((int64_t)p.max_kv_len, (int64_t)p.max_blocks_per_seq * p.block_size)) {
     if (report) record_error(p.status, PA_ERR_SEQLEN);
     return s;
   }
   s.nodes = (int)n;
-  s.ktiles = (int)((kv + p.tile_keys - 1) / p.tile_keys);
-  s.qtiles = (int)((n * p.group + p.tile_rows - 1) / p.tile_rows);
+  s.ktiles = (int)(((uint32_t)kv + p.tile_keys - 1) / (uint32_t)p.tile_keys);
+  s.qtiles = (s.nodes * p.group + p.tile_rows - 1) / p.tile_rows;
   s.places = p.team == 1 ? s.qtiles * p.num_kv_heads
                          : (s.qtiles >> 1) * p.num_kv_heads + (s.qtiles & 1) * ((p.num_kv_heads + 1) >> 1);
   return s;
@@ -128,7 +135,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm
   const int s0 = min(p.num_seqs, (int)threadIdx.x * per), s1 = min(p.num_seqs, s0 + per);
   int64_t mine = 0, my_units = 0;
   for (int s = s0; s < s1; ++s) {
-    const TreeSeq q = tree_seq(p, s, blockIdx.x == 0);
+    const TreeSeq q = tree_seq(p, tree_lens(p, s), blockIdx.x == 0);
     mine += q.tiles();
     my_units += q.places;
   }
@@ -167,7 +174,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams& p, int64_t* sm
   if (r.left > 0 && r.begin >= base && r.begin < base + mine) {
     int64_t at = base;
     for (int s = s0; s < s1; ++s) {
-      const int64_t t = tree_seq(p, s, false).tiles();
+      const int64_t t = tree_seq(p, tree_lens(p, s)).tiles();
       if (r.begin < at + t) {
         found[0] = s;
         found[1] = r.begin - at;
@@ -193,44 +200,55 @@ struct TreePiece {
   __device__ __forceinline__ int kv_len() const { return s.ctx + s.nodes; }
 };
 
-// Walks the pieces of a CTA's range. Every role of a CTA runs its own copy.
+// Walks the pieces of a CTA's range. Every role of a CTA runs its own copy, at
+// the very point where its pipeline is empty, so a step is kept short: the
+// next sequence's lengths are loaded a sequence ahead, and only the first
+// piece takes a 64-bit division.
 struct TreeWalk {
-  TreeRange r;
-  int64_t at;
-  int seq;
-  int64_t off;  // place in the sequence
-  int64_t left;
-  __device__ __forceinline__ explicit TreeWalk(const TreeRange& range)
-      : r(range), at(range.begin), seq(range.seq), off(range.off), left(range.left) {}
+  TreeSeq s;
+  TreeLens ahead;
+  int seq, place, t;
+  int64_t at, left;
+  __device__ __forceinline__ TreeWalk(const TreeParams& p, const TreeRange& r)
+      : seq(r.seq), place(0), t(0), at(r.begin), left(r.left) {
+    if (left > 0) {
+      s = tree_seq(p, tree_lens(p, seq));
+      place = (int)(r.off / s.ktiles);
+      t = (int)(r.off - (int64_t)place * s.ktiles);
+      look(p);
+    }
+  }
+  __device__ __forceinline__ void look(const TreeParams& p) { ahead = tree_lens(p, min(seq + 1, p.num_seqs - 1)); }
   __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& c) {
     while (left > 0) {
-      c.s = tree_seq(p, seq, false);
-      while (off >= c.s.tiles()) {  // also steps over sequences without work
-        off -= c.s.tiles();
-        c.s = tree_seq(p, ++seq, false);
+      while (place >= s.places) {  // also steps over sequences without work
+        ++seq;
+        place = 0;
+        s = tree_seq(p, ahead);
+        look(p);
       }
+      c.s = s;
       c.seq = seq;
-      const int place = (int)(off / c.s.ktiles);
-      c.t0 = (int)(off - (int64_t)place * c.s.ktiles);
-      c.t1 = (int)min((int64_t)c.s.ktiles, c.t0 + left);
+      c.t0 = t;
+      c.t1 = (int)min((int64_t)s.ktiles, t + left);
       if (p.team == 1) {
-        c.kvh = place / c.s.qtiles;
-        c.qt = place - c.kvh * c.s.qtiles;
+        c.kvh = place / s.qtiles;
+        c.qt = place - c.kvh * s.qtiles;
       } else {
-        const int r = blockIdx.x & 1, pairs = c.s.qtiles >> 1;
+        const int r = blockIdx.x & 1, pairs = s.qtiles >> 1;
         if (place < pairs * p.num_kv_heads) {
           c.kvh = place / pairs;
           c.qt = 2 * (place - c.kvh * pairs) + r;
         } else {
           c.kvh = 2 * (place - pairs * p.num_kv_heads) + r;
-          c.qt = c.s.qtiles - 1;
+          c.qt = s.qtiles - 1;
         }
       }
       c.at = at;
-      const int n = c.t1 - c.t0;
-      off += n;
-      at += n;
-      left -= n;
+      at += c.t1 - c.t0;
+      left -= c.t1 - c.t0;
+      ++place;  // (a piece that ends before its unit does is the last one)
+      t = 0;
       if (c.kvh < p.num_kv_heads) return true;  // (else an odd last head: nothing for this member)
     }
     return false;

@@ -55,7 +55,8 @@ constexpr int kConvWarp0 = 7;
 constexpr int kConvK = 2;              // warps that widen K; one more widens V
 constexpr int kConvWarps = kConvK + 1;
 constexpr int kQSlots = 3;            // pieces whose Q exponents are kept (8-bit cache)
-constexpr int kScaleSlots = 8;        // tiles whose scales are kept (8-bit cache)
+constexpr int kScaleSlots = 4;        // tiles whose scales are kept (8-bit cache): a K tile's copy is issued after
+                                      // the softmax of the tile four before it (NK = 2)
 template <int D, bool KV8>
 struct Cfg {
   static constexpr int kH = D / 64;            // 64-column halves
@@ -74,7 +75,8 @@ struct Cfg {
   static constexpr int kOffV = kOffK + NK * kStage;
   static constexpr int kOffBar = kOffV + NV * kStage;
   // barriers
-  static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarSoft = 2;
+  static constexpr int kBarQFull = 0, kBarQEmpty = 1;
+  static constexpr int kBarSoft = 2;  // the four softmax warps
   // S(g), P(g) and the product of P(g) complete barrier g % 2 of their kind:
   // a wait for tile g then cannot meet tile g - 1's phase, and tile g - 2's is
   // over once S(g) is known to be computed.
@@ -85,9 +87,11 @@ struct Cfg {
   static constexpr int kBarKFull = 13, kBarKEmpty = kBarKFull + NK, kBarKCode = kBarKEmpty + NK;
   static constexpr int kBarVFull = kBarKCode + NK, kBarVEmpty = kBarVFull + NV, kBarVCode = kBarVEmpty + NV;
   static constexpr int kNumBars = kBarVCode + NV;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tensor-memory base, any-poison flag
-  static constexpr int kOffPoison = kOffMisc + 16;          // node bits; before that the scan's scratch
-  static constexpr int kOffScale = kOffPoison + kMaxTreeNodes / 8;  // [kScaleSlots][kN / 16] (K, V)
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tensor-memory base, the notes' two flags
+  // Notes of nodes with values that are not finite, by piece parity (a softmax
+  // warp may be one piece ahead of another); before that the scan's scratch.
+  static constexpr int kOffPoison = kOffMisc + 16;
+  static constexpr int kOffScale = kOffPoison + 2 * kMaxTreeNodes / 8;  // [kScaleSlots][kN / 16] (K, V)
   static constexpr int kOffQExp = kOffScale + (KV8 ? kScaleSlots * (kN / 16) * 8 : 0);
   static constexpr int kSmem = kOffQExp + (KV8 ? kQSlots * kM : 0);
 };
@@ -135,7 +139,6 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
   const uint32_t bar0 = sbase + C::kOffBar;
   auto bar = [&](int i) -> uint32_t { return bar0 + 8 * i; };
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
-  uint32_t* poison = reinterpret_cast<uint32_t*>(smem + C::kOffPoison);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_trigger();
@@ -174,12 +177,12 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
   __syncthreads();
   tc_fence_after();
   const TreeRange range = tree_range<kThreads>(p, reinterpret_cast<int64_t*>(smem + C::kOffPoison));
-  __syncthreads();  // the scratch becomes the node bits
+  __syncthreads();  // the scratch becomes the notes
   const uint32_t tmem = misc[0];
   const int G = p.group;
   const int pp = p.tile_rows / G;  // nodes of a query tile
 
-  TreeWalk walk(range);
+  TreeWalk walk(p, range);
   TreePiece c;
   int g = 0;       // tiles of this CTA so far
   int piece = 0;
@@ -422,12 +425,15 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
     const int tid = threadIdx.x - 32 * kSoftmaxWarp0;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     bool bad = false;
+    for (int i = tid; i < 2 * kMaxTreeNodes / 32; i += 128) reinterpret_cast<uint32_t*>(smem + C::kOffPoison)[i] = 0;
+    if (tid < 2) misc[1 + tid] = 0;
     int syncs = 0;
     auto soft_sync = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::kBarSoft));
       return mbar_wait_warp(bar(C::kBarSoft), syncs++ & 1, p.status);
     };
+    bad = !soft_sync();
     while (!bad && walk.next(p, c)) {
       const int32_t* parents = p.parents + c.s.q0;
       const int32_t* table = p.block_tables + (int64_t)c.seq * p.max_blocks_per_seq;
@@ -436,12 +442,9 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
       const bool used = row < pp * G && node < c.s.nodes;
       const bool live = q * 32 < pp * G && c.qt * pp + q * 32 / G < c.s.nodes;  // the warp has a row in use
       const bool tree = c.t1 * kN > ctx;  // the piece reaches into the tree
-      if (tree) {
-        tree_check_parents<128>(p, c, tid);
-        if (tid < kMaxTreeNodes / 32) poison[tid] = 0;
-        if (tid == 0) misc[1] = 0;
-        if (!soft_sync()) break;
-      }
+      uint32_t* poison = reinterpret_cast<uint32_t*>(smem + C::kOffPoison) + (piece & 1) * (kMaxTreeNodes / 32);
+      volatile uint32_t* poisoned = &misc[1 + (piece & 1)];
+      if (tree) tree_check_parents<128>(p, c, tid);
       float m = -CUDART_INF_F, l = 0.f;
       // 8-bit cache: scores are scaled to log2 units before the max.
       const float sl2 = KV8 ? 1.f : p.scale_log2;
@@ -461,36 +464,6 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           break;
         }
         tc_fence_after();
-        // Values behind the sequence become 0, and those in the tree that are
-        // not finite are taken out.
-        if (k0 + kN > ctx) {
-          const int sv = g % C::NV;
-          if (!mbar_wait_warp(bar(C::kBarVFull + sv), (g / C::NV) & 1, p.status)) {
-            bad = true;
-            break;
-          }
-          const int first = max(ctx - k0, 0);
-          uint8_t* vst = smem + C::kOffV + sv * C::kStage;
-          for (int i = tid; i < (kN - first) * 8 * C::kH; i += 128) {
-            const int r = first + i / (8 * C::kH), x = i % (8 * C::kH);
-            uint4* at = reinterpret_cast<uint4*>(vst + (r >> 3) * C::kGroup + (x >> 3) * C::kHalfOff + (r & 7) * 128 + (x & 7) * 16);
-            if (k0 + r >= kv_len) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 w = *at;
-              const bool b0 = strip_not_finite<kBf16>(w.x), b1 = strip_not_finite<kBf16>(w.y);
-              const bool b2 = strip_not_finite<kBf16>(w.z), b3 = strip_not_finite<kBf16>(w.w);
-              if (b0 || b1 || b2 || b3) {
-                *at = w;
-                const int nd = k0 + r - ctx;
-                atomicOr(&poison[nd >> 5], 1u << (nd & 31));
-                misc[1] = 1;
-              }
-            }
-          }
-          fence_async_shared();
-          __syncwarp();
-        }
         if (live) {
           // Keys that the row sees, in tiles that reach into the tree.
           uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
@@ -575,14 +548,9 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
             // scores of 16-key group u are s * f_u, f_u >= 0, so a group's
             // largest is its raw largest times f_u exactly.
             const float2* scales = reinterpret_cast<const float2*>(smem + C::kOffScale) + (g % kScaleSlots) * (kN / 16);
-            float fk[kN / 16], fv[kN / 16], vmax = 0.f;
+            float vmax = 0.f;
 #pragma unroll
-            for (int u = 0; u < kN / 16; ++u) {
-              const float2 x = scales[u];
-              fk[u] = x.x * rf;
-              fv[u] = x.y;
-              vmax = fmaxf(vmax, x.y);
-            }
+            for (int u = 0; u < kN / 16; ++u) vmax = fmaxf(vmax, scales[u].y);
             float kap_r = 1.f;  // 2^(new kap - old kap) where kap drops
             if (vmax > 0.f) {
               // 2^kap brings the largest V scale seen so far below 2^7.
@@ -595,19 +563,20 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
               }
             }
             float mx = -CUDART_INF_F;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               uint32_t v[32];
               tmem_ld32(ts + h * 32, v);
+              const float f0 = scales[h * 2].x * rf, f1 = scales[h * 2 + 1].x * rf;
               tmem_ld_wait();
-              if (masked) mask(v, seen[h]);
+              if (masked) mask(v, h ? seen[1] : seen[0]);
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 float x = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2)
                   x = fmax3(x, __uint_as_float(v[u * 16 + i]), __uint_as_float(v[u * 16 + i + 1]));
-                mx = fmaxf(mx, x == -CUDART_INF_F ? x : x * fk[h * 2 + u]);  // (-inf times a scale of 0)
+                mx = fmaxf(mx, x == -CUDART_INF_F ? x : x * (u ? f1 : f0));  // (-inf times a scale of 0)
               }
             }
             update_max(mx);
@@ -617,21 +586,24 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
             }
             const float neg = m == -CUDART_INF_F ? 0.f : -m;
             const uint64_t negx2 = f2_pack(neg, neg);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               uint32_t v[32], pk[16];
               tmem_ld32(ts + h * 32, v);
+              const float2 s0 = scales[h * 2], s1 = scales[h * 2 + 1];
+              const float f0 = s0.x * rf, f1 = s1.x * rf, w0 = s0.y * pw, w1 = s1.y * pw;
+              const uint32_t bits = h ? seen[1] : seen[0];
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
-                const float f = fk[h * 2 + i / 16], w = fv[h * 2 + i / 16] * pw;
+                const float f = i < 16 ? f0 : f1, w = i < 16 ? w0 : w1;
                 float x0, x1;
                 f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f2_pack(f, f), negx2), x0,
                           x1);
                 float a = fast_exp2(x0), b = fast_exp2(x1);
                 if (masked) {  // (a masked score may be anything)
-                  a = (seen[h] >> i) & 1u ? a : 0.f;
-                  b = (seen[h] >> (i + 1)) & 1u ? b : 0.f;
+                  a = (bits >> i) & 1u ? a : 0.f;
+                  b = (bits >> (i + 1)) & 1u ? b : 0.f;
                 }
                 rs2 = f2_add(rs2, f2_pack(a, b));
                 pk[i / 2] = MmaOp<MT>::pack(a * w, b * w);
@@ -644,57 +616,95 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           l = l * alpha + (rs0 + rs1);
           tmem_st_wait();
         }
+        // Values behind the sequence become 0, and those in the tree that are
+        // not finite are taken out.
+        if (k0 + kN > ctx) {
+          const int sv = g % C::NV;
+          if (!mbar_wait_warp(bar(C::kBarVFull + sv), (g / C::NV) & 1, p.status)) {
+            bad = true;
+            break;
+          }
+          const int first = max(ctx - k0, 0);
+          uint8_t* vst = smem + C::kOffV + sv * C::kStage;
+          for (int i = tid; i < (kN - first) * 8 * C::kH; i += 128) {
+            const int r = first + i / (8 * C::kH), x = i % (8 * C::kH);
+            uint4* at = reinterpret_cast<uint4*>(vst + (r >> 3) * C::kGroup + (x >> 3) * C::kHalfOff + (r & 7) * 128 + (x & 7) * 16);
+            if (k0 + r >= kv_len) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 w = *at;
+              const bool b0 = strip_not_finite<kBf16>(w.x), b1 = strip_not_finite<kBf16>(w.y);
+              const bool b2 = strip_not_finite<kBf16>(w.z), b3 = strip_not_finite<kBf16>(w.w);
+              if (b0 || b1 || b2 || b3) {
+                *at = w;
+                const int nd = k0 + r - ctx;
+                atomicOr(&poison[nd >> 5], 1u << (nd & 31));
+                *poisoned = 1;
+              }
+            }
+          }
+          fence_async_shared();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kBarP + (g & 1)));
       }
       if (bad || !mbar_wait_warp(bar(C::kBarPv + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.status)) break;
       tc_fence_after();
-      if (tree && !soft_sync()) break;  // every warp's notes of values that are not finite
-      if (c.t0 == 0 && !c.whole() && tid == 0) tree_note_merge(p, range, c);
+      // Every warp's notes are made once all have handed over their last P
+      // (the next phase of that barrier needs this warp's next tile but one).
+      if (tree && !mbar_wait_warp(bar(C::kBarP + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.status)) break;
+      if (tree && *poisoned) {
+        // The values taken out above, added for the rows that see their node.
+        if (live) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t o[16];
+            tmem_ld16(tl + kColO + cc * 16, o);
+            tmem_ld_wait();
+            for (int a = used ? node : -1; a >= 0;) {
+              const int pos = ctx + a, id = (poison[a >> 5] >> (a & 31)) & 1u ? table[pos / BS] : -1;
+              if (id >= 0 && id < p.num_blocks) {
+                const int64_t at = (((int64_t)id * p.num_kv_heads + c.kvh) * BS + pos % BS) * D + cc * 16;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float v;
+                  if constexpr (KV8) {
+                    uint32_t x0, x1;
+                    fp8x4_to_f16x4<E5>(static_cast<const uint8_t*>(p.v_cache)[at + i], x0, x1);
+                    v = __half2float(__ushort_as_half((unsigned short)(x0 & 0xffffu)));
+                  } else {
+                    v = to_f32(static_cast<const T*>(p.v_cache)[at + i]);
+                  }
+                  if (not_finite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+                }
+              }
+              const int up = __ldg(parents + a);
+              a = up < a ? up : -1;
+            }
+            __syncwarp();
+            tmem_st16(tl + kColO + cc * 16, o);
+          }
+          tmem_st_wait();
+        }
+        if (!soft_sync()) break;  // read by all
+        if (tid < kMaxTreeNodes / 32) poison[tid] = 0;
+        if (tid == 0) *poisoned = 0;
+        if (!soft_sync()) break;
+      }
+      const bool whole = c.whole();
+      if (c.t0 == 0 && !whole && tid == 0) tree_note_merge(p, range, c);
       if (live) {
-        const bool whole = c.whole();
         const float f = whole ? 1.f / (l * pw) : 1.f / pw;
         const int head = c.kvh * G + row - (row / G) * G;
         T* out = static_cast<T*>(p.out) + ((int64_t)(c.s.q0 + node) * p.num_q_heads + head) * D;
         const int64_t slot = (int64_t)tree_slot(c) * kM + row;
-        const bool dirty = tree && misc[1];
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           __syncwarp();
           tmem_ld32(tl + kColO + cc * 32, o);
           tmem_ld_wait();
-          if (dirty && used) {
-            // The values taken out above, for the nodes that this row sees.
-            for (int a = node; a >= 0;) {
-              if ((poison[a >> 5] >> (a & 31)) & 1u) {
-                const int pos = ctx + a, id = table[pos / BS];
-                if (id >= 0 && id < p.num_blocks) {
-                  const int64_t tile = (int64_t)id * p.num_kv_heads + c.kvh;
-                  const int64_t at = (tile * BS + pos % BS) * D + cc * 32;
-                  for (int i = 0; i < 32; ++i) {
-                    float v;
-                    if constexpr (KV8) {
-                      uint32_t x0, x1;
-                      fp8x4_to_f16x4<E5>(static_cast<const uint8_t*>(p.v_cache)[at + i], x0, x1);
-                      v = __half2float(__ushort_as_half((unsigned short)(x0 & 0xffffu)));
-                    } else {
-                      v = to_f32(static_cast<const T*>(p.v_cache)[at + i]);
-                    }
-                    if (not_finite(v)) {
-#pragma unroll
-                      for (int j = 0; j < 32; ++j)
-                        if (j == i) o[j] = __float_as_uint(__uint_as_float(o[j]) + v);
-                    }
-                  }
-                }
-              }
-              const int up = __ldg(parents + a);
-              if (up >= a) break;
-              a = up;
-            }
-          }
           if (used && whole) {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
@@ -717,7 +727,6 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
         __syncwarp();
         tc_fence_before();
       }
-      if (tree && !soft_sync()) break;  // the notes are read before the next piece clears them
       ++piece;
     }
   }
