@@ -77,14 +77,16 @@ struct Cfg {
   // barriers
   static constexpr int kBarQFull = 0, kBarQEmpty = 1;
   static constexpr int kBarSoft = 2;  // the four softmax warps
-  // S(g), P(g) and the product of P(g) complete barrier g % 2 of their kind:
-  // a wait for tile g then cannot meet tile g - 1's phase, and tile g - 2's is
-  // over once S(g) is known to be computed.
-  static constexpr int kBarS = 4, kBarP = 6, kBarPv = 8;
+  // P(g) completes barrier g % 2: a wait for tile g then cannot meet tile
+  // g - 1's phase, and tile g - 2's is over once S(g) is known to be computed.
+  // S(g) computed is its K stage's release, and P(g)'s product its V stage's: the
+  // softmax waits on those barriers too (a commit takes the MMA thread 60 to
+  // 100 cycles, and it issues without a pause).
+  static constexpr int kBarP = 4;
   // 8-bit cache: piece i's Q is in fp16 (i % 3: the MMAs may be two pieces of
   // one tile each ahead of the softmax, which waits for it too).
-  static constexpr int kBarQConv = 10;
-  static constexpr int kBarKFull = 13, kBarKEmpty = kBarKFull + NK, kBarKCode = kBarKEmpty + NK;
+  static constexpr int kBarQConv = 6;
+  static constexpr int kBarKFull = 9, kBarKEmpty = kBarKFull + NK, kBarKCode = kBarKEmpty + NK;
   static constexpr int kBarVFull = kBarKCode + NK, kBarVEmpty = kBarVFull + NV, kBarVCode = kBarVEmpty + NV;
   static constexpr int kNumBars = kBarVCode + NV;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;   // tensor-memory base, the notes' two flags
@@ -149,9 +151,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
     for (int i = 0; i < kQSlots; ++i) mbar_init(bar(C::kBarQConv + i), kConvWarps);
     mbar_init(bar(C::kBarSoft), 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(C::kBarS + i), 1);
       mbar_init(bar(C::kBarP + i), 4);
-      mbar_init(bar(C::kBarPv + i), 1);
     }
     for (int i = 0; i < C::NK; ++i) {
       mbar_init(bar(C::kBarKFull + i), KV8 ? kConvK : 1);
@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           tc_mma_f16_ta(tmem + kColO, tmem + (j & 1) * kN + k * 8, va + ((k * 2 * C::kGroup) >> 4), kIdescO,
                         !first || k > 0 ? 1u : 0u);
         commit(bar(C::kBarVEmpty + j % C::NV), j / C::NV);
-        commit(bar(C::kBarPv + (j & 1)), j >> 1);
         return true;
       };
       bool first_prev = false;  // tile g - 1 was its piece's first
@@ -330,7 +329,6 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           for (int k = 0; k < D / 16; ++k)
             tc_mma_f16(tmem + (g & 1) * kN, dq + (((k >> 2) * kQHalf + (k & 3) * 32) >> 4),
                        ka + (((k >> 2) * C::kHalfOff + (k & 3) * 32) >> 4), kIdescS, k > 0);
-          commit(bar(C::kBarS + (g & 1)), g >> 1);
           commit(bar(C::kBarKEmpty + g % C::NK), g / C::NK);
           if (t + 1 == c.t1) commit(bar(C::kBarQEmpty), piece);
           if (t > c.t0 && !issue_pv(g - 1, first_prev)) bad = true;
@@ -459,7 +457,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
       for (int t = c.t0; t < c.t1 && !bad; ++t, ++g) {
         const int k0 = t * kN;
         const uint32_t ts = tl + (g & 1) * kN, to = tl + kColO;
-        if (!mbar_wait_warp(bar(C::kBarS + (g & 1)), (g >> 1) & 1, p.status)) {
+        if (!mbar_wait_warp(bar(C::kBarKEmpty + g % C::NK), (g / C::NK) & 1, p.status)) {
           bad = true;
           break;
         }
@@ -497,7 +495,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
           // O times f, once the previous product has been added to it.
           auto rescale = [&](float f) -> bool {
             if (t == c.t0 || !__any_sync(0xffffffffu, f != 1.f)) return true;
-            if (!mbar_wait_warp(bar(C::kBarPv + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.status)) return false;
+            if (!mbar_wait_warp(bar(C::kBarVEmpty + (g - 1) % C::NV), ((g - 1) / C::NV) & 1, p.status)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int i = 0; i < D / 16; ++i) {
@@ -649,7 +647,7 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kBarP + (g & 1)));
       }
-      if (bad || !mbar_wait_warp(bar(C::kBarPv + ((g - 1) & 1)), ((g - 1) >> 1) & 1, p.status)) break;
+      if (bad || !mbar_wait_warp(bar(C::kBarVEmpty + (g - 1) % C::NV), ((g - 1) / C::NV) & 1, p.status)) break;
       tc_fence_after();
       // Every warp's notes are made once all have handed over their last P
       // (the next phase of that barrier needs this warp's next tile but one).
