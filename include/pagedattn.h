@@ -664,8 +664,8 @@ int pa_decode_tree_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_lens
  * w(0) + .. + w(y) > uniform_sample * sum(w); if every w is 0, w = p is used.
  * Probabilities outside [0, 1] are held to it and NaN counts as 0; a row
  * without any probability gives next token -1 and PA_ERR_ARG. Sums are taken
- * over weights rounded to multiples of 2^-44, exactly, so results do not
- * depend on the order in which the device runs. A sequence whose cu_q_lens
+ * over weights formed from whole multiples of 2^-43 (within two of them),
+ * exactly, so results do not depend on the order in which the device runs. A sequence whose cu_q_lens
  * falls, leaves [0, total_q] or has more than max_q_len nodes records
  * PA_ERR_SEQLEN, one with a parent that is not below its node (or a node 0
  * that is no root) PA_ERR_ARG; both get path_lens 0 and next token -1.

@@ -731,11 +731,6 @@ def pa_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
     tp, ts = _rows(target_probs, "target_probs", dt, dev, shape)
     dp, ds = (None, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", dt, dev, shape)
     rows = (T,)
-    if path is None and path_lens is None and next_tokens is None:
-        made = _scratch(target_probs, n * (max_path_len + 2), i32, side)  # (one allocation costs less than three)
-        path = made.as_strided((n, max_path_len), (max_path_len, 1))
-        path_lens = made.as_strided((n,), (1,), n * max_path_len)
-        next_tokens = made.as_strided((n,), (1,), n * (max_path_len + 1))
     if path is None:
         path = _scratch(target_probs, (n, max_path_len), i32, side)
     if path_lens is None:

@@ -13,19 +13,22 @@
 // token is the smallest y with w(0) + .. + w(y) > u' sum w.
 //
 // The token is a whole number that has to come out the same whatever the
-// order of the sum, so sums are taken over integers: a weight in [0, 1] is
-// rounded once to a multiple of 2^-44 (2^18 of them fit 62 bits), and integer
-// sums do not depend on their order. p - C q is formed in pairs of floats
-// (exact product, exact difference), since double arithmetic runs at a
-// fraction of the rate.
+// order of the sum, so sums are taken over integers: p and C q in [0, 1] are
+// rounded once to multiples of 2^-43 (2^18 weights fit 61 bits), and integer
+// sums do not depend on their order. Double arithmetic runs at a fraction of
+// the rate, so a float is split into two whole numbers by adding and taking
+// away 1.5 * 2^23 (four multiply-adds).
 //
 // A sequence is one cluster of 1 to 8 CTAs, each with a slice of the
 // vocabulary; all of them walk the tree by themselves and exchange only sums.
-// A warp sums chunks of 512 entries (16 bytes a load, a chunk's loads all in
-// flight) and every chunk's sum is kept, so the entry where the running sum
-// passes the threshold takes a second look at one chunk only. What bounds it
-// is the rows' one pass from HBM; with few sequences, the latency of its
-// dependent loads and cluster barriers.
+// A warp sums two chunks of 512 entries at a time (16 bytes a load, the chunks'
+// loads all in flight) and every chunk's sum is kept, so the entry where the
+// running sum passes the threshold takes a second look at one chunk only. 96
+// trees over 131072 fp32 tokens take 55 us (100 MB of rows are 15 us of HBM):
+// a sequence makes one to four passes one after another, 10 us each, bound by
+// the loads' latency; one chunk at a time took 61 us, doubles and one CTA a
+// sequence 1018 us. With few sequences it is the latency of the dependent
+// loads and cluster barriers (4 chains over 32000 tokens: 10 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -43,7 +46,8 @@ constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyChunk = 512;
 constexpr int kVerifyMaxChunks = kVerifyMaxVocab / kVerifyChunk + 1;  // + 1: a row may start inside a 16-byte line
 constexpr int kVerifyMaxCluster = 8;
-constexpr double kVerifyUnit = 1.0 / 17592186044416.0;  // 2^-44
+constexpr int kVerifyLow = 21;                           // bits of a weight's lower part
+constexpr double kVerifyUnit = 1.0 / 8796093022208.0;  // 2^-43
 constexpr unsigned kAll = 0xffffffffu;
 
 struct VerifyParams {
@@ -69,75 +73,43 @@ __device__ __forceinline__ float prob(T x) { return __saturatef(to_f32(x)); }
 // What C is: nothing refused yet (w = p), one refusal (C = 1), or more.
 enum VerifyMode { kVerifyPlain, kVerifyOne, kVerifyMore };
 
-// max(0, p - C q) in units of 2^-44, as hi * 2^22 + lo with 0 <= hi <= 2^22 and
-// |lo| <= 2^21. C = c + cl (cl: what a float of C leaves over).
-template <int MODE>
-__device__ __forceinline__ void weight_parts(float p, float q, float c, float cl, uint32_t& hi, int& lo) {
-  float d = p, e = 0.f;  // p - C q = d + e
-  if constexpr (MODE != kVerifyPlain) {
-    float m = q, me = 0.f;  // C q = m + me
-    if constexpr (MODE == kVerifyMore) {
-      m = c * q;
-      me = fmaf(cl, q, fmaf(c, q, -m));
-    }
-    d = p - m;
-    const float bb = d - p;
-    e = (p - (d - bb)) - (m + bb);
-    if constexpr (MODE == kVerifyMore) e -= me;
-  }
-  const float magic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
-  const float t = fmaf(d, 4194304.f, magic);
-  float rest = fmaf(d, 4194304.f, magic - t);
-  if constexpr (MODE != kVerifyPlain) rest = fmaf(e, 4194304.f, rest);
-  const bool some = MODE == kVerifyPlain || d + e > 0.f;
-  hi = some ? __float_as_uint(t) - __float_as_uint(magic) : 0u;
-  lo = some ? __float2int_rn(rest * 4194304.f) : 0;
+// x in [0, 1] as hi * 2^21 + lo in units of 2^-43, |lo| <= 2^20; both above
+// kMagicBits, which differences take out.
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
+constexpr int kMagicBits = 0x4b400000;
+__device__ __forceinline__ void split(float x, int& hi, int& lo) {
+  const float t = fmaf(x, 4194304.f, kMagic);
+  const float rest = fmaf(x, 4194304.f, kMagic - t);  // exact, at most 1/2
+  hi = __float_as_int(t);
+  lo = __float_as_int(fmaf(rest, 2097152.f, kMagic));
 }
 
-__device__ __forceinline__ long long joined(uint32_t hi, int lo) { return ((long long)hi << 22) + lo; }
+// max(0, p - C q) in units of 2^-43 as hi * 2^21 + lo, |lo| <= 2^21, added to
+// h and l. C = c + cl (cl: what a float of C leaves over).
+template <int MODE>
+__device__ __forceinline__ void add_weight(float p, float q, float c, float cl, int& h, int& l) {
+  int ph, pl, qh = kMagicBits, ql = kMagicBits;
+  split(p, ph, pl);
+  bool some = true;
+  if constexpr (MODE == kVerifyOne) {
+    split(q, qh, ql);
+    some = p > q;
+  } else if constexpr (MODE == kVerifyMore) {
+    const float m = c * q;                         // C q = m + me; beyond 1 it takes all of p
+    const float me = fmaf(cl, q, fmaf(c, q, -m));
+    split(fminf(m, 1.f), qh, ql);
+    ql += __float2int_rn(me * 8796093022208.f);
+    some = m <= 1.f && ((ph - qh) * 2097152ll + (pl - ql)) > 0;
+  }
+  h += some ? ph - qh : 0;
+  l += some ? pl - ql : 0;
+}
+
+__device__ __forceinline__ long long joined(int hi, int lo) { return ((long long)hi << kVerifyLow) + lo; }
 
 template <typename T>
 __device__ __forceinline__ float entry(const uint4& raw, int i) {
   return prob(reinterpret_cast<const T*>(&raw)[i]);
-}
-
-// The 16 bytes of a row of V that hold entries y .. of it; entries outside
-// the row come as 0. `line`: the address of entry y is a multiple of 16.
-template <typename T>
-__device__ __forceinline__ uint4 load_line(const T* row, int y, int V, bool line) {
-  constexpr int N = 16 / sizeof(T);
-  if (line && y >= 0 && y + N <= V) return __ldg(reinterpret_cast<const uint4*>(row + y));
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  T* t = reinterpret_cast<T*>(&raw);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (y + i >= 0 && y + i < V) t[i] = row[y + i];
-  return raw;
-}
-
-// A lane's weights of one chunk, at(u, i, hi, lo) for each: entry (32 u +
-// lane) N + i of the chunk. y: the row's entry that the lane's first one is.
-template <typename T, int MODE, typename F>
-__device__ __forceinline__ void chunk_weights(const T* a, const T* b, int y, int V, float c, float cl, F at) {
-  constexpr int N = 16 / sizeof(T), kLoads = kVerifyChunk / (32 * N);
-  const bool line = ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
-  uint4 x[kLoads], z[kLoads];
-#pragma unroll
-  for (int u = 0; u < kLoads; ++u) {
-    x[u] = load_line(a, y + u * 32 * N, V, true);
-    if constexpr (MODE != kVerifyPlain) z[u] = load_line(b, y + u * 32 * N, V, line);
-  }
-#pragma unroll
-  for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint32_t hi;
-      int lo;
-      float q = 0.f;
-      if constexpr (MODE != kVerifyPlain) q = entry<T>(z[u], i);
-      weight_parts<MODE>(entry<T>(x[u], i), q, c, cl, hi, lo);
-      at(u, i, hi, lo);
-    }
 }
 
 // The sums of a slice's chunks, one warp a chunk at a time; returns this
@@ -145,30 +117,61 @@ __device__ __forceinline__ void chunk_weights(const T* a, const T* b, int y, int
 template <typename T, int MODE>
 __device__ __forceinline__ long long slice_sums(const T* a, const T* b, int lead, int V, float c, float cl, int c_lo,
                                                 int c_hi, long long* chunk_sum) {
-  constexpr int N = 16 / sizeof(T);
+  constexpr int N = 16 / sizeof(T), kLoads = kVerifyChunk / (32 * N);
   const int lane = threadIdx.x & 31;
+  const bool line =
+      MODE == kVerifyPlain || ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
   long long mine = 0;
-#pragma unroll 1
-  for (int k = c_lo + (threadIdx.x >> 5); k < c_hi; k += kVerifyWarps) {
-    uint32_t h = 0;
-    int l = 0;
-    chunk_weights<T, MODE>(a, b, k * kVerifyChunk - lead + lane * N, V, c, cl, [&](int, int, uint32_t hi, int lo) {
-      h += hi;
-      l += lo;
-    });
-    // 512 entries: at most 2^31, and 2^30 either way.
-    const long long s = joined(__reduce_add_sync(kAll, h), __reduce_add_sync(kAll, l));
+  auto done = [&](int k, int h, int l) {
+    // 512 entries: h at most 2^31 (as an unsigned sum), l 2^30 either way.
+    const long long s = ((long long)__reduce_add_sync(kAll, (unsigned)h) << kVerifyLow) + __reduce_add_sync(kAll, l);
     if (lane == 0) chunk_sum[k - c_lo] = s;
     mine += s;
+  };
+  auto whole = [&](int k) { return k < c_hi && k * kVerifyChunk >= lead && (k + 1) * kVerifyChunk - lead <= V; };
+#pragma unroll 1
+  for (int k = c_lo + (threadIdx.x >> 5); k < c_hi; k += 2 * kVerifyWarps) {
+    const int k2 = k + kVerifyWarps;
+    if (line && whole(k) && whole(k2)) {
+      uint4 x[2][kLoads], z[2][kLoads];
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int y = (w ? k2 : k) * kVerifyChunk - lead + (u * 32 + lane) * N;
+          x[w][u] = __ldg(reinterpret_cast<const uint4*>(a + y));
+          if constexpr (MODE != kVerifyPlain) z[w][u] = __ldg(reinterpret_cast<const uint4*>(b + y));
+        }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        int h = 0, l = 0;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            add_weight<MODE>(entry<T>(x[w][u], i), MODE == kVerifyPlain ? 0.f : entry<T>(z[w][u], i), c, cl, h, l);
+        done(w ? k2 : k, h, l);
+      }
+      continue;
+    }
+    // The row's ends, and rows whose 16-byte lines do not match.
+#pragma unroll 1
+    for (int kk = k; kk < c_hi && kk <= k2; kk += kVerifyWarps) {
+      int h = 0, l = 0;
+#pragma unroll 4
+      for (int e = lane; e < kVerifyChunk; e += 32) {
+        const int y = kk * kVerifyChunk - lead + e;
+        if (y >= 0 && y < V) add_weight<MODE>(prob(a[y]), MODE == kVerifyPlain ? 0.f : prob(b[y]), c, cl, h, l);
+      }
+      done(kk, h, l);
+    }
   }
   return mine;
 }
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify_kernel(const VerifyParams p) {
-  constexpr int N = 16 / sizeof(T);                // entries of one load
-  constexpr int kLoads = kVerifyChunk / (32 * N);  // loads of a lane in a chunk
-  constexpr int kMine = kLoads * N;                // entries of a lane in a chunk
+__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 2) verify_kernel(const VerifyParams p) {
+  constexpr int kMine = kVerifyChunk / 32;
   __shared__ int16_t parent[kVerifyMaxNodes];
   __shared__ int tok[kVerifyMaxNodes];
   __shared__ float px[kVerifyMaxNodes], qx[kVerifyMaxNodes], ua[kVerifyMaxNodes];
@@ -248,9 +251,8 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
         if (parent[j] != r || again[j]) continue;
         const int c = (tok[j] + lead) / kVerifyChunk;
         if (c < c_lo || c >= c_hi) continue;
-        uint32_t hi;
-        int lo;
-        weight_parts<kVerifyPlain>(px[j], 0.f, 0.f, 0.f, hi, lo);
+        int hi = 0, lo = 0;
+        add_weight<kVerifyPlain>(px[j], 0.f, 0.f, 0.f, hi, lo);
         const unsigned long long w = (unsigned long long)-joined(hi, lo);
         atomicAdd(reinterpret_cast<unsigned long long*>(&chunk_sum[c - c_lo]), w);
         atomicAdd(&acc, w);
@@ -281,11 +283,20 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
         const int j = base + __ffs(kids) - 1;
         kids &= kids - 1;
         if constexpr (DRAFT) {
-          if (stale) S = (double)total(at, C, false) * kVerifyUnit;
-          const double w = fmax(0.0, (double)px[j] - C * (double)qx[j]);
-          if ((double)ua[j] * (double)qx[j] * S < w) {
-            step = j;
-            break;
+          if (C == 0.0) {
+            if (fmaf(ua[j], qx[j], -px[j]) < 0.f) {  // u q < p (one rounding keeps the sign)
+              step = j;
+              break;
+            }
+          } else {
+            // S is put off until it decides: it is at most the last one, so a
+            // child that would be kept with that is kept.
+            const double w = fmax(0.0, (double)px[j] - C * (double)qx[j]);
+            if (stale && !((double)ua[j] * (double)qx[j] * S < w)) S = (double)total(at, C, false) * kVerifyUnit;
+            if ((double)ua[j] * (double)qx[j] * S < w) {
+              step = j;
+              break;
+            }
           }
           C += S;
           stale = true;
@@ -339,41 +350,39 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
     int c = c_lo, who = 0;
     while (!passes(c + lane < c_hi ? chunk_sum[c + lane - c_lo] : 0, who) && c + 32 < c_hi) c += 32;
     c += who;
-    uint32_t hi[kMine];
-    int lo[kMine];
+    // Lane i takes entries 16 i .. 16 i + 15 of the chunk.
     const float cm = (float)C, cl = (float)(C - (double)cm);
-    const int y0 = c * kVerifyChunk - lead + lane * N;
-    auto keep = [&](int u, int i, uint32_t h, int l) { hi[u * N + i] = h, lo[u * N + i] = l; };
-    if (C == 0.0) chunk_weights<T, kVerifyPlain>(a, a, y0, p.vocab, cm, cl, keep);
-    else chunk_weights<T, DRAFT ? kVerifyMore : kVerifyPlain>(a, b, y0, p.vocab, cm, cl, keep);
+    const int y0 = c * kVerifyChunk - lead + lane * kMine;
+    int hi[kMine], lo[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int y = y0 + i;
+      hi[i] = lo[i] = 0;
+      if (y < 0 || y >= p.vocab) continue;
+      const float pp = prob(a[y]);
+      if (!DRAFT || C == 0.0) add_weight<kVerifyPlain>(pp, 0.f, 0.f, 0.f, hi[i], lo[i]);
+      else if (C == 1.0) add_weight<kVerifyOne>(pp, prob(b[y]), cm, cl, hi[i], lo[i]);
+      else add_weight<kVerifyMore>(pp, prob(b[y]), cm, cl, hi[i], lo[i]);
+    }
     if (take_out)
       for (int j = at + 1; j < n; ++j) {
         if (parent[j] != at) continue;
-        const int x = tok[j] + lead - c * kVerifyChunk;  // place in the chunk
+        const int x = tok[j] - y0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
-          if (x == (i / N * 32 + lane) * N + i % N) hi[i] = 0, lo[i] = 0;
+          if (x == i) hi[i] = lo[i] = 0;
       }
+    long long mine = 0;
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      long long mine = 0;
+    for (int i = 0; i < kMine; ++i) mine += joined(hi[i], lo[i]);
+    if (passes(mine, who) && lane == who) {
+      int y = y0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) mine += joined(hi[u * N + i], lo[u * N + i]);
-      if (passes(mine, who)) {
-        if (lane == who) {
-          int y = c * kVerifyChunk - lead + (u * 32 + lane) * N;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const long long w = joined(hi[u * N + i], lo[u * N + i]);
-            if (run + w > tau) {
-              p.next_tokens[seq] = y + i;
-              break;
-            }
-            run += w;
-          }
-        }
-        break;
+      for (int i = 0; i < kMine; ++i) {  // the first entry that passes
+        run += joined(hi[i], lo[i]);
+        y += run <= tau;
       }
+      p.next_tokens[seq] = y;
     }
   }
   if (rank == 0) {
@@ -390,8 +399,9 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 3) verify
 
 template <typename T>
 static cudaError_t launch_verify(const VerifyParams& p, int num_seqs, cudaStream_t stream) {
-  // CTAs of a sequence: as many as keep the batch within four per SM and
-  // leave each at least four chunks.
+  // CTAs of a sequence: as many as keep the batch within four per SM (fewer
+  // are resident with fp32 rows, but a sequence's passes get shorter: 75 us with
+  // half as many for the 96 trees) and leave each at least four chunks.
   int ranks = 1;
   while (ranks < kVerifyMaxCluster && (int64_t)num_seqs * ranks * 2 <= 4 * num_sms_current_device() &&
          p.vocab / kVerifyChunk >= ranks * 2 * 4)

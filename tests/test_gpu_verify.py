@@ -1,6 +1,6 @@
 """Verification of drafted tokens against the fp64 oracle: whole numbers, so
 equal. A drawn token could differ only where the sample lies within the
-sums' rounding (2^-44 a weight) of a border, about one sample in 10^6."""
+sums' rounding (2^-43 a weight) of a border, about one sample in 10^6."""
 from __future__ import annotations
 
 import numpy as np
