@@ -12,6 +12,10 @@ With an e4m3 cache the same step runs pa_copy_blocks_fp8,
 pa_reshape_and_cache_fp8 and pa_decode_fp8 (pa_decode_shared_prefix_fp8,
 pa_chunked_prefill_fp8); with an e5m2 cache the *_e5m2 calls
 (pa_copy_blocks_fp8 moves either format).
+TreeStep is the step of a serving engine that drafts: the nodes of a draft
+tree instead of one new token, their attention in every layer
+(pa_decode_tree), then the choice (pa_verify_tree) and the kept rows' move
+(pa_compact_tree).
 This module only sequences library calls on one stream and owns the device
 buffers the calls need (slot mapping, output, split-KV workspace), allocated
 once with PyTorch.
@@ -254,6 +258,86 @@ def step_from_host(batch, device="cuda", partition_size: int = 0, shared_prefix:
         prefix_lens=dev(batch.prefix_lens, torch.int32) if shared_prefix else None,
         kv_format=kv_format,
     )
+
+
+class TreeStep:
+    """Steps over draft trees on the KV pools of a model's layers.
+
+    The engine fills the step's inputs (device tensors of fixed size, so that
+    a step can be captured once and replayed): ctx_lens, cu_q_lens, parents,
+    draft_tokens and, for every node, new_seq_ids and new_positions (the
+    position ctx_lens[sequence] + node; rows behind the last sequence's are
+    padding and name a place that holds no token). Then slots(), for every
+    layer write() and attend(), and once accept(), after which ctx_lens +
+    path_lens tokens of a sequence are cached, in order.
+    """
+
+    def __init__(self, *, k_caches, v_caches, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
+                 cu_q_lens: torch.Tensor, parents: torch.Tensor, draft_tokens: torch.Tensor,
+                 new_seq_ids: torch.Tensor, new_positions: torch.Tensor, num_q_heads: int, dtype: torch.dtype,
+                 max_q_len: int, max_kv_len: int, scale: float, max_path_len: int | None = None, kv_scales=None,
+                 kv_format: str = "e4m3"):
+        if kv_format not in ("e4m3", "e5m2"):
+            raise ValueError(f"kv_format {kv_format!r}: e4m3 or e5m2")
+        self.k_caches, self.v_caches, self.kv_scales = list(k_caches), list(v_caches), kv_scales
+        self.kv_call_suffix = "fp8" if kv_format == "e4m3" else "e5m2"
+        self.block_tables, self.ctx_lens, self.cu_q_lens = block_tables, ctx_lens, cu_q_lens
+        self.parents, self.draft_tokens = parents, draft_tokens
+        self.new_seq_ids, self.new_positions = new_seq_ids, new_positions
+        self.max_q_len, self.max_kv_len, self.scale = int(max_q_len), int(max_kv_len), float(scale)
+        self.max_path_len = int(max_path_len or max_q_len)
+        self.num_blocks, hkv, self.block_size, d = self.k_caches[0].shape
+        total, n, dev = parents.shape[0], ctx_lens.shape[0], parents.device
+        self.slot_mapping = torch.empty(total, dtype=torch.int64, device=dev)
+        self.out = torch.empty(total, num_q_heads, d, dtype=dtype, device=dev)
+        need = pa.pa_decode_tree_workspace_size(n, num_q_heads, hkv, d, self.block_size, total, self.max_q_len,
+                                                self.max_kv_len, dtype)
+        self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        self.path = torch.empty(n, self.max_path_len, dtype=torch.int32, device=dev)
+        self.path_lens = torch.empty(n, dtype=torch.int32, device=dev)
+        self.next_tokens = torch.empty(n, dtype=torch.int32, device=dev)
+
+    def call_8bit(self, name: str):
+        """The binding's 8-bit form of a call for this cache's format."""
+        return getattr(pa, f"{name}_{self.kv_call_suffix}")
+
+    def slots(self, stream=None) -> torch.Tensor:
+        """The nodes' cache slots: once a step, before the first write()."""
+        return pa.pa_slot_mapping(self.block_tables, self.new_seq_ids, self.new_positions, self.block_size,
+                                  self.num_blocks, slot_mapping=self.slot_mapping, stream=stream)
+
+    def write(self, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+        """Cache the nodes' K/V of one layer."""
+        k, v = self.k_caches[layer], self.v_caches[layer]
+        if self.kv_scales is None:
+            pa.pa_reshape_and_cache(k_new, v_new, self.slot_mapping, k, v, stream=stream)
+        else:
+            self.call_8bit("pa_reshape_and_cache")(k_new, v_new, self.slot_mapping, k, v, self.kv_scales[layer],
+                                                   stream=stream)
+
+    def attend(self, layer: int, q: torch.Tensor, stream=None) -> torch.Tensor:
+        """Attention of the nodes in one layer (out is reused by the next)."""
+        k, v = self.k_caches[layer], self.v_caches[layer]
+        rest = (self.block_tables, self.ctx_lens, self.max_q_len, self.max_kv_len, self.scale)
+        if self.kv_scales is None:
+            return pa.pa_decode_tree(q, self.cu_q_lens, self.parents, k, v, *rest, out=self.out,
+                                     workspace=self.workspace, stream=stream)
+        return self.call_8bit("pa_decode_tree")(q, self.cu_q_lens, self.parents, k, v, self.kv_scales[layer], *rest,
+                                                out=self.out, workspace=self.workspace, stream=stream)
+
+    def accept(self, target_probs: torch.Tensor, draft_probs: torch.Tensor | None, uniform_accept: torch.Tensor,
+               uniform_sample: torch.Tensor, stream=None):
+        """Choose the kept path and the next token, and move the kept rows
+        together in every layer: (path, path_lens, next_tokens)."""
+        pa.pa_verify_tree(target_probs, draft_probs, self.draft_tokens, self.cu_q_lens, self.parents, uniform_accept,
+                          uniform_sample, self.max_q_len, self.max_path_len, path=self.path, path_lens=self.path_lens,
+                          next_tokens=self.next_tokens, stream=stream)
+        tail = (self.block_tables, self.ctx_lens, self.path, self.path_lens)
+        if self.kv_scales is None:
+            pa.pa_compact_tree(self.k_caches, self.v_caches, *tail, stream=stream)
+        else:
+            self.call_8bit("pa_compact_tree")(self.k_caches, self.v_caches, self.kv_scales, *tail, stream=stream)
+        return self.path, self.path_lens, self.next_tokens
 
 
 class HostPipeline:
