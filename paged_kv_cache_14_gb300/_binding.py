@@ -613,8 +613,8 @@ def _arg(t, name: str, dtype, dev: int, shape) -> int:
 
 
 def _place(t, name: str, stream) -> tuple[int, int, object]:
-    """The current device, the stream's handle, and the stream if tensors
-    made here have to be recorded on it (it is not the current one)."""
+    """The current device, the stream's handle, and the stream if it is not
+    the current one."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     dev = torch.cuda.current_device()
@@ -626,11 +626,16 @@ def _place(t, name: str, stream) -> tuple[int, int, object]:
 
 
 def _scratch(like: torch.Tensor, shape, dtype, side) -> torch.Tensor:
-    """A new tensor that a call on another stream (side) may use: its memory
-    is not handed out again before that stream is done with it."""
-    t = like.new_empty(shape, dtype=dtype)
-    if side is not None:
-        t.record_stream(side)
+    """A new tensor for a call on the current stream or on another one (side).
+    Memory comes from the stream that writes it first, so that whatever used
+    it before is over by then; the caller may go on to read it on the current
+    one, which is why that one is recorded."""
+    if side is None:
+        return like.new_empty(shape, dtype=dtype)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(side):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(here)
     return t
 
 
