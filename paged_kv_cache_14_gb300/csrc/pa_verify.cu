@@ -99,9 +99,15 @@ __device__ __forceinline__ void add_weight(float p, float q, float c, float cl, 
     const float me = fmaf(cl, q, fmaf(c, q, -m));
     split(fminf(m, 1.f), qh, ql);
     ql += __float2int_rn(me * 8796093022208.f);
-    some = m <= 1.f && ((ph - qh) * 2097152ll + (pl - ql)) > 0;
+    // m may lie across a multiple of 2^-22 from p although C q < p: the parts
+    // are set right, so that sums of h stay sums of whole numbers >= 0.
+    const long long d = (ph - qh) * 2097152ll + (pl - ql);
+    some = m <= 1.f && d > 0;
+    h += some ? (int)(d >> kVerifyLow) : 0;
+    l += some ? (int)d & ((1 << kVerifyLow) - 1) : 0;
+    return;
   }
-  h += some ? ph - qh : 0;
+  h += some ? ph - qh : 0;  // (rounding keeps p's order to q: not below 0)
   l += some ? pl - ql : 0;
 }
 
@@ -437,6 +443,8 @@ extern "C" int pa_verify_tree(const void* target_probs, int64_t target_stride, c
   if (max_q_len > kVerifyMaxNodes) return PA_ERR_UNSUPPORTED;
   if (target_stride < vocab_size || (draft_probs && draft_stride < vocab_size)) return PA_ERR_ARG;
   if (!cu_q_lens || !path || !path_lens || !next_tokens) return PA_ERR_ARG;
+  const uintptr_t odd = reinterpret_cast<uintptr_t>(target_probs) | reinterpret_cast<uintptr_t>(draft_probs);
+  if (odd & (dtype == PA_F32 ? 3u : 1u)) return PA_ERR_ALIGN;
   if (total_q > 0 && (!target_probs || !draft_tokens || !parents || !uniform_accept || !uniform_sample))
     return PA_ERR_ARG;
   int* st = device_status_ptr();

@@ -229,3 +229,54 @@ def test_captured_and_replayed(lib):
                              d["max_path"])
         for x, r in zip((a["path"], a["path_lens"], a["next_tokens"]), ref):
             assert np.array_equal(x.cpu().numpy(), r)
+
+
+def test_weights_between_neighbouring_floats(lib):
+    """Two refusals leave C = 1 + S with S just above 2^-24: token 3 weighs
+    p - C q > 0 although p < fl(fl(C) q), which lies across a multiple of
+    2^-22 from p. It weighs little, token 599 a thousand times as much."""
+    c = case(15, "f32", [3], 600, kind="star")
+    ulp = 2.0 ** -33
+    p3 = 7782.5 * 2.0 ** -22
+    for name, at3, at599 in (("target", p3, 0.75), ("draft", p3 - ulp, 0.75 - 2.0 ** -24)):
+        c[name].zero_()
+        c[name][0, 3], c[name][0, 599] = at3, at599
+    c["tokens"][:] = [0, 5, 6]  # no probability: refused
+    c["us"][:] = 0.5
+    ref = check(lib, c)
+    assert ref[2][0] == 599
+
+
+def test_rows_in_different_lines(lib):
+    """Target and draft rows that start at different places of their 16-byte lines."""
+    for seed, dtype in ((16, "f32"), (17, "bf16")):
+        c = case(seed, dtype, [5, 1, 7], 5000)
+        t, d = (torch.zeros(13, 5000 + 16, dtype=DT[dtype], device="cuda") for _ in range(2))
+        t[:, 3:5003], d[:, 1:5001] = c["target"].cuda(), c["draft"].cuda()
+        got = call(lib, c, target_probs=t[:, 3:5003], draft_probs=d[:, 1:5001])
+        ref = ot.verify_tree(c["target"], c["draft"], c["tokens"], c["cu"], c["parents"], c["ua"], c["us"],
+                             c["max_path"])
+        for g, r in zip(got, ref):
+            assert np.array_equal(g.cpu().numpy(), r)
+
+
+def test_on_another_stream(lib):
+    """Outputs made for another stream do not take memory that the current
+    stream still has to read."""
+    c = case(18, "f32", [6] * 500, 200)
+    a = dict(target_probs=c["target"].cuda(), draft_probs=c["draft"].cuda(), draft_tokens=torch.as_tensor(c["tokens"]).cuda(),
+             cu_q_lens=torch.as_tensor(c["cu"]).cuda(), parents=torch.as_tensor(c["parents"]).cuda(),
+             uniform_accept=torch.as_tensor(c["ua"]).cuda(), uniform_sample=torch.as_tensor(c["us"]).cuda(),
+             max_q_len=6, max_path_len=6)
+    ref = [x.clone() for x in lib.pa_verify_tree(**a)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.full(sh, 7, dtype=torch.int32, device="cuda") for sh in ((500, 6), (500,), (500,))]
+    torch.cuda._sleep(50_000_000)
+    kept = [x.clone() for x in old]
+    del old
+    got = lib.pa_verify_tree(**a, stream=s)
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in kept)
+    for g, r in zip(got, ref):
+        assert torch.equal(g, r)

@@ -85,6 +85,8 @@ def test_verify_host_checks(lib):
     assert _verify(lib, dt=3) == -2
     assert _verify(lib, v=262145, ts=262145, ds=262145) == -10
     assert _verify(lib, mq=1025) == -10
+    for over in (dict(t=0x1002), dict(d=0x2001), dict(t=0x1001, dt=pa.PA_F16)):
+        assert _verify(lib, **over) == -12, over
     assert _verify(lib, n=0) == 0
 
 
