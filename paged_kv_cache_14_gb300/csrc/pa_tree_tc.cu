@@ -693,7 +693,9 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
       const bool whole = c.whole();
       if (c.t0 == 0 && !whole && tid == 0) tree_note_merge(p, range, c);
       if (live) {
-        const float f = whole ? 1.f / (l * pw) : 1.f / pw;
+        // (1 / l and 1 / pw apart: l * pw overflows for V scales near 2^-120)
+        const float f = whole ? 1.f / l : 1.f, ipw = 1.f / pw;
+        auto val = [&](uint32_t x) { return KV8 ? __uint_as_float(x) * f * ipw : __uint_as_float(x) * f; };
         const int head = c.kvh * G + row - (row / G) * G;
         T* out = static_cast<T*>(p.out) + ((int64_t)(c.s.q0 + node) * p.num_q_heads + head) * D;
         const int64_t slot = (int64_t)tree_slot(c) * kM + row;
@@ -710,15 +712,14 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
               uint32_t* x = &w.x;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                x[j] = MmaOp<T>::pack(__uint_as_float(o[i + 2 * j]) * f, __uint_as_float(o[i + 2 * j + 1]) * f);
+                x[j] = MmaOp<T>::pack(val(o[i + 2 * j]), val(o[i + 2 * j + 1]));
               *reinterpret_cast<uint4*>(out + cc * 32 + i) = w;
             }
           } else if (used) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
               __stcg(reinterpret_cast<float4*>(p.part_o + slot * D + cc * 32 + i),
-                     make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f,
-                                 __uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f));
+                     make_float4(val(o[i]), val(o[i + 1]), val(o[i + 2]), val(o[i + 3])));
           }
         }
         if (used && !whole) __stcg(reinterpret_cast<float2*>(p.part_ml + slot * 2), make_float2(m * sl2, l));

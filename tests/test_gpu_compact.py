@@ -173,3 +173,38 @@ def test_captured_and_replayed(lib):
     torch.cuda.synchronize()
     ref = ot.compact_tree(x, ctx, path, lens, table, 16)
     assert torch.equal(k.cpu(), ref) and torch.equal(v.cpu(), ref)
+
+
+def test_pools_beyond_32_bits(lib):
+    """Rows at byte offsets beyond 2^32 of their pools."""
+    rng, table, P0, ctx, path, lens = case(8, CTX, NODES, KEEP, 16)
+    hkv, d = 8, 128
+    P = (5 << 30) // (hkv * 16 * d * 2)
+    far = P - P0
+    small = [torch.from_numpy(rng.standard_normal((P0, hkv, 16, d)).astype(np.float32)).bfloat16() for _ in range(2)]
+    pools = [torch.zeros(P, hkv, 16, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for x, y in zip(small, pools):
+        y[far:] = x.cuda()
+    lib.pa_compact_tree(pools[:1], pools[1:], *dev(table + far, ctx, path, lens))
+    assert lib.pa_get_status() == 0
+    for x, y in zip(small, pools):
+        assert torch.equal(y[far:].cpu(), ot.compact_tree(x, ctx, path, lens, table, 16))
+        assert not y[:far].any()
+
+
+def test_on_another_stream(lib):
+    """The call runs behind what its stream holds, not beside it."""
+    rng, table, P, ctx, path, lens = case(9, CTX, NODES, KEEP, 16)
+    first = torch.from_numpy(rng.standard_normal((2, P, 2, 16, 64)).astype(np.float32))
+    on, src = torch.zeros(first.shape, device="cuda"), first.cuda()
+    args = dev(table, ctx, path, lens)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        on.copy_(src)
+    lib.pa_compact_tree(on[:1], on[1:], *args, stream=s)
+    torch.cuda.synchronize()
+    assert lib.pa_get_status() == 0
+    for x, y in zip(first, on):
+        assert torch.equal(y.cpu(), ot.compact_tree(x, ctx, path, lens, table, 16))

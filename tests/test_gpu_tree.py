@@ -312,3 +312,86 @@ def test_binding_refuses(lib):
     for k, v in (([pool, odd], [pool, pool]), ([pool, pool], [pool, pool.float()]), ([odd[..., :64]], [pool])):
         with pytest.raises((ValueError, TypeError), match="_caches"):
             lib.pa_compact_tree(k, v, *tail)
+
+
+def test_memory_of_another_stream(lib):
+    """Outputs and workspaces made for another stream do not take memory that
+    the current stream still has to read."""
+    b = tree_batch(23, "bf16", [500, 44], [9, 30], 16, 4, 128)
+    a = b.device()
+    s = torch.cuda.Stream()
+    ws = lib.pa_decode_tree_workspace_size(2, 16, 4, 128, 16, 39, a["max_q_len"], a["max_kv_len"])
+    torch.cuda.synchronize()
+    old = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (ws, a["q"].nbytes)]
+    torch.cuda._sleep(50_000_000)
+    kept = [x.clone() for x in old]
+    del old
+    out = lib.pa_decode_tree(**a, stream=s)
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in kept)
+    assert_tree_close(b, out)
+
+
+def test_two_graphs_on_two_streams(lib):
+    """Captured calls with workspaces of their own, replayed side by side."""
+    bs = [tree_batch(25 + i, dt, [700 * (i + 1), 44], [9, 30], 16, 4, 128) for i, dt in enumerate(("bf16", "f32"))]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in bs]
+    for b in bs:
+        a = b.device()
+        b.call(lib)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(lib.pa_decode_tree(**a))
+        graphs.append((g, a))
+    for _ in range(5):
+        for (g, _a), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for b, o in zip(bs, outs):
+        assert_tree_close(b, o)
+
+
+@pytest.mark.parametrize("hkv", [1, 3, 4])
+@pytest.mark.parametrize("nodes", [[40, 70, 33, 1, 100], [17] * 40])
+@pytest.mark.parametrize("kv", [None, "e4m3"])
+def test_several_query_tiles(lib, hkv, nodes, kv):
+    """Even and odd numbers of query tiles and of KV heads, long and short
+    trees in one batch."""
+    run(lib, tree_batch(27, "bf16", [300 + 37 * i for i in range(len(nodes))], nodes, 8 * hkv, hkv, 128, kv=kv))
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("power", [-100, -118, 60])
+def test_extreme_value_scales(lib, kv, power):
+    """V scales near the ends of fp32: outputs scale with them."""
+    b = tree_batch(29, "bf16", [200, 5, 900], [5, 9, 1], 8, 2, 128, kv=kv)
+    ref = b.call(lib)
+    b.scales[..., 1] *= 2.0 ** power
+    got = b.call(lib)
+    assert lib.pa_get_status() == 0
+    # A power of two: the same sums. (fp32 loses bits below 2^-126.)
+    want = ref.double() * 2.0 ** power
+    assert torch.allclose(got.double(), want, rtol=2.0 ** -7, atol=2.0 ** -133)
+
+
+def test_pools_beyond_32_bits(lib):
+    """Blocks at element offsets beyond 2^31 (and byte offsets beyond 2^32)."""
+    for dtype, d, hkv, need in (("bf16", 128, 8, 5 << 30), ("f32", 256, 8, 9 << 30)):
+        b = tree_batch(31, dtype, [200, 5, 70], [5, 9, 40], 16, hkv, d)
+        a = b.device()
+        P0 = b.k.shape[0]
+        P = (need // b.k.element_size()) // (hkv * 16 * d)
+        far = P - P0
+        for name in ("k_cache", "v_cache"):
+            pool = torch.zeros(P, hkv, 16, d, dtype=b.k.dtype, device="cuda")
+            pool[far:] = a[name]
+            a[name] = pool
+        a["block_tables"] = a["block_tables"] + far
+        out = lib.pa_decode_tree(**a)
+        assert lib.pa_get_status() == 0
+        assert_tree_close(b, out, dtype)
+        a.clear()
+        del pool, out
+        torch.cuda.empty_cache()
