@@ -13,25 +13,29 @@
 // token is the smallest y with w(0) + .. + w(y) > u' sum w.
 //
 // The token is a whole number that has to come out the same whatever the
-// order of the sum, so sums are taken over integers: p and C q in [0, 1] are
-// rounded once to multiples of 2^-43 (2^18 weights fit 61 bits), and integer
-// sums do not depend on their order. Double arithmetic runs at a fraction of
-// the rate, so a float is split into two whole numbers by adding and taking
-// away 1.5 * 2^23 (four multiply-adds).
+// order of the sum, so sums are taken over integers: p - C q is rounded to a
+// multiple of 2^-43 (2^18 weights fit 61 bits), and integer sums do not depend
+// on their order. Double arithmetic runs at a fraction of the rate, so the
+// difference is taken as a float and its rounding error, and split into two
+// whole numbers by adding and taking away 1.5 * 2^23, two entries an
+// instruction.
 //
 // A sequence is one cluster of 1 to 8 CTAs, each with a slice of the
 // vocabulary; all of them walk the tree by themselves and exchange only sums.
 // A warp sums two chunks of 512 entries at a time (16 bytes a load, the chunks'
 // loads all in flight) and every chunk's sum is kept, so the entry where the
 // running sum passes the threshold takes a second look at one chunk only. 96
-// trees over 131072 fp32 tokens take 55 us (100 MB of rows are 15 us of HBM):
-// a sequence makes one to four passes one after another, 10 us each, bound by
-// the loads' latency; one chunk at a time took 61 us, doubles and one CTA a
-// sequence 1018 us. With few sequences it is the latency of the dependent
-// loads and cluster barriers (4 chains over 32000 tokens: 10 us).
+// trees over 131072 fp32 tokens take 49 us (100 MB of rows are 15 us of HBM):
+// a sequence makes one to four passes one after another, some 9 us each at two
+// CTAs an SM, half of that the arithmetic of its 13 instructions an entry, and
+// its start, its exchanges and the draw take 8 us more. One chunk at a time
+// took 61 us, a split of p and C q each 54, doubles and one CTA a sequence
+// 1018. With few sequences it is the latency of the dependent loads and cluster
+// barriers (4 chains over 32000 tokens: 10 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -73,42 +77,57 @@ __device__ __forceinline__ float prob(T x) { return __saturatef(to_f32(x)); }
 // What C is: nothing refused yet (w = p), one refusal (C = 1), or more.
 enum VerifyMode { kVerifyPlain, kVerifyOne, kVerifyMore };
 
-// x in [0, 1] as hi * 2^21 + lo in units of 2^-43, |lo| <= 2^20; both above
-// kMagicBits, which differences take out.
+// Two values x in [-1, 1] as hi * 2^21 + lo in units of 2^-43, |lo| <= 2^20;
+// both above kMagicBits, and lo on top of base's bits (kMagic and whole numbers).
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
 constexpr int kMagicBits = 0x4b400000;
-__device__ __forceinline__ void split(float x, int& hi, int& lo) {
-  const float t = fmaf(x, 4194304.f, kMagic);
-  const float rest = fmaf(x, 4194304.f, kMagic - t);  // exact, at most 1/2
-  hi = __float_as_int(t);
-  lo = __float_as_int(fmaf(rest, 2097152.f, kMagic));
+__device__ __forceinline__ uint64_t both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ void split2(uint64_t x, uint64_t base, uint64_t& hi, uint64_t& lo) {
+  hi = f2_fma(x, both(4194304.f), both(kMagic));
+  const uint64_t rest = f2_fma(x, both(4194304.f), f2_fma(hi, both(-1.f), both(kMagic)));  // exact, at most 1/2
+  lo = f2_fma(rest, both(2097152.f), base);
 }
 
-// max(0, p - C q) in units of 2^-43 as hi * 2^21 + lo, |lo| <= 2^21, added to
-// h and l. C = c + cl (cl: what a float of C leaves over).
+// max(0, p - C q) of two entries in units of 2^-43 as hi * 2^21 + lo, hi >= 0,
+// |lo| < 2^21, added to h and l. C = c + cl (cl: what a float of C leaves
+// over). Differences are taken in floats and their rounding errors, exact
+// floats too (p - d - m), go into the lower part.
+template <int MODE>
+__device__ __forceinline__ void add_weights(float p0, float p1, float q0, float q1, float c, float cl, int& h, int& l) {
+  const uint64_t p = f2_pack(p0, p1), q = f2_pack(q0, q1);
+  const uint64_t minus = both(-1.f);
+  uint64_t d = p, base = both(kMagic), hi, lo;
+  if constexpr (MODE == kVerifyOne) {
+    d = f2_fma(q, minus, p);
+    base = f2_fma(f2_fma(q, minus, f2_fma(d, minus, p)), both(8796093022208.f), base);
+  } else if constexpr (MODE == kVerifyMore) {
+    const uint64_t m = f2_fma(both(c), q, both(0.f));  // C q = m + me
+    const uint64_t me = f2_fma(both(cl), q, f2_fma(both(c), q, f2_fma(m, minus, both(0.f))));
+    d = f2_fma(m, minus, p);
+    const uint64_t e = f2_fma(m, minus, f2_fma(d, minus, p));
+    base = f2_fma(f2_fma(me, minus, e), both(8796093022208.f), base);
+    float d0, d1;
+    f2_unpack(d, d0, d1);
+    d = f2_pack(fmaxf(d0, -1.f), fmaxf(d1, -1.f));
+  }
+  split2(d, base, hi, lo);
+  float t0, t1, s0, s1;
+  f2_unpack(hi, t0, t1);
+  f2_unpack(lo, s0, s1);
+  auto add = [&](float pv, float qv, float t, float s) {
+    const int a = __float_as_int(t) - kMagicBits, b = __float_as_int(s) - kMagicBits;
+    // m may pass p by a rounding although C q < p: the parts decide.
+    const bool some = MODE == kVerifyPlain || (MODE == kVerifyOne ? pv > qv : a > 0 || (a == 0 && b > 0));
+    h += some ? a : 0;
+    l += some ? b : 0;
+  };
+  add(p0, q0, t0, s0);
+  add(p1, q1, t1, s1);
+}
+
 template <int MODE>
 __device__ __forceinline__ void add_weight(float p, float q, float c, float cl, int& h, int& l) {
-  int ph, pl, qh = kMagicBits, ql = kMagicBits;
-  split(p, ph, pl);
-  bool some = true;
-  if constexpr (MODE == kVerifyOne) {
-    split(q, qh, ql);
-    some = p > q;
-  } else if constexpr (MODE == kVerifyMore) {
-    const float m = c * q;                         // C q = m + me; beyond 1 it takes all of p
-    const float me = fmaf(cl, q, fmaf(c, q, -m));
-    split(fminf(m, 1.f), qh, ql);
-    ql += __float2int_rn(me * 8796093022208.f);
-    // m may lie across a multiple of 2^-22 from p although C q < p: the parts
-    // are set right, so that sums of h stay sums of whole numbers >= 0.
-    const long long d = (ph - qh) * 2097152ll + (pl - ql);
-    some = m <= 1.f && d > 0;
-    h += some ? (int)(d >> kVerifyLow) : 0;
-    l += some ? (int)d & ((1 << kVerifyLow) - 1) : 0;
-    return;
-  }
-  h += some ? ph - qh : 0;  // (rounding keeps p's order to q: not below 0)
-  l += some ? pl - ql : 0;
+  add_weights<MODE>(p, 0.f, q, 0.f, c, cl, h, l);
 }
 
 __device__ __forceinline__ long long joined(int hi, int lo) { return ((long long)hi << kVerifyLow) + lo; }
@@ -129,54 +148,71 @@ __device__ __forceinline__ long long slice_sums(const T* a, const T* b, int lead
       MODE == kVerifyPlain || ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
   long long mine = 0;
   auto done = [&](int k, int h, int l) {
-    // 512 entries: h at most 2^31 (as an unsigned sum), l 2^30 either way.
+    // 512 entries: h at most 2^31 (as an unsigned sum), l below 2^30 either way.
     const long long s = ((long long)__reduce_add_sync(kAll, (unsigned)h) << kVerifyLow) + __reduce_add_sync(kAll, l);
     if (lane == 0) chunk_sum[k - c_lo] = s;
     mine += s;
   };
   auto whole = [&](int k) { return k < c_hi && k * kVerifyChunk >= lead && (k + 1) * kVerifyChunk - lead <= V; };
+  // W whole chunks, their loads all in flight.
+  auto chunks = [&](int k, auto W) {
+    uint4 x[W.value][kLoads], z[W.value][kLoads];
+#pragma unroll
+    for (int w = 0; w < W.value; ++w)
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int y = (k + w * kVerifyWarps) * kVerifyChunk - lead + (u * 32 + lane) * N;
+        x[w][u] = __ldg(reinterpret_cast<const uint4*>(a + y));
+        if constexpr (MODE != kVerifyPlain) z[w][u] = __ldg(reinterpret_cast<const uint4*>(b + y));
+      }
+#pragma unroll
+    for (int w = 0; w < W.value; ++w) {
+      int h = 0, l = 0;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+          add_weights<MODE>(entry<T>(x[w][u], i), entry<T>(x[w][u], i + 1),
+                            MODE == kVerifyPlain ? 0.f : entry<T>(z[w][u], i),
+                            MODE == kVerifyPlain ? 0.f : entry<T>(z[w][u], i + 1), c, cl, h, l);
+      done(k + w * kVerifyWarps, h, l);
+    }
+  };
 #pragma unroll 1
   for (int k = c_lo + (threadIdx.x >> 5); k < c_hi; k += 2 * kVerifyWarps) {
-    const int k2 = k + kVerifyWarps;
-    if (line && whole(k) && whole(k2)) {
-      uint4 x[2][kLoads], z[2][kLoads];
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          const int y = (w ? k2 : k) * kVerifyChunk - lead + (u * 32 + lane) * N;
-          x[w][u] = __ldg(reinterpret_cast<const uint4*>(a + y));
-          if constexpr (MODE != kVerifyPlain) z[w][u] = __ldg(reinterpret_cast<const uint4*>(b + y));
-        }
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        int h = 0, l = 0;
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            add_weight<MODE>(entry<T>(x[w][u], i), MODE == kVerifyPlain ? 0.f : entry<T>(z[w][u], i), c, cl, h, l);
-        done(w ? k2 : k, h, l);
+    int odd = k;  // first chunk of the two that is not whole
+    if (line && whole(k)) {
+      odd = k + kVerifyWarps;
+      if (whole(odd)) {
+        chunks(k, std::integral_constant<int, 2>());
+        continue;
       }
-      continue;
+      chunks(k, std::integral_constant<int, 1>());
     }
     // The row's ends, and rows whose 16-byte lines do not match.
 #pragma unroll 1
-    for (int kk = k; kk < c_hi && kk <= k2; kk += kVerifyWarps) {
+    for (; odd < c_hi && odd <= k + kVerifyWarps; odd += kVerifyWarps) {
       int h = 0, l = 0;
 #pragma unroll 4
-      for (int e = lane; e < kVerifyChunk; e += 32) {
-        const int y = kk * kVerifyChunk - lead + e;
-        if (y >= 0 && y < V) add_weight<MODE>(prob(a[y]), MODE == kVerifyPlain ? 0.f : prob(b[y]), c, cl, h, l);
+      for (int e = lane; e < kVerifyChunk; e += 64) {
+        float v[2], u[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int y = odd * kVerifyChunk - lead + e + 32 * i;
+          const bool in = y >= 0 && y < V;
+          v[i] = in ? prob(a[y]) : 0.f;
+          if (MODE != kVerifyPlain && in) u[i] = prob(b[y]);
+        }
+        add_weights<MODE>(v[0], v[1], u[0], u[1], c, cl, h, l);
       }
-      done(kk, h, l);
+      done(odd, h, l);
     }
   }
   return mine;
 }
 
 template <typename T, bool DRAFT>
-__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 2) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 4 ? 2 : DRAFT ? 3 : 4) verify_kernel(const VerifyParams p) {
   constexpr int kMine = kVerifyChunk / 32;
   __shared__ int16_t parent[kVerifyMaxNodes];
   __shared__ int tok[kVerifyMaxNodes];
@@ -405,11 +441,13 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 2 ? 4 : 2) verify
 
 template <typename T>
 static cudaError_t launch_verify(const VerifyParams& p, int num_seqs, cudaStream_t stream) {
-  // CTAs of a sequence: as many as keep the batch within four per SM (fewer
-  // are resident with fp32 rows, but a sequence's passes get shorter: 75 us with
-  // half as many for the 96 trees) and leave each at least four chunks.
+  // CTAs of a sequence: as many as keep the batch within three per SM and leave
+  // each at least four chunks. A sequence's passes get shorter with each (8
+  // trees over 131072 fp32 tokens: 67, 41, 28, 22 us with 1, 2, 4, 8), until
+  // the batch fills the machine (96 trees: 62, 49, 59 us with 2, 4, 8; 64 over
+  // 32000: 23, 23, 33).
   int ranks = 1;
-  while (ranks < kVerifyMaxCluster && (int64_t)num_seqs * ranks * 2 <= 4 * num_sms_current_device() &&
+  while (ranks < kVerifyMaxCluster && (int64_t)num_seqs * ranks * 2 <= 3 * num_sms_current_device() &&
          p.vocab / kVerifyChunk >= ranks * 2 * 4)
     ranks *= 2;
   cudaLaunchConfig_t cfg = {};
