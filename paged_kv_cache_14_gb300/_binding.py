@@ -779,8 +779,13 @@ _LAYOUT = operator.attrgetter("dtype", "shape")
 
 def _pools(pools, name: str, dtype, dev: int, shape) -> array.array:
     """Pointers of the layers' pools, as _arg. The checks run as loops in C:
-    a model has dozens of layers, and this is most of a call's host time."""
+    a model has dozens of layers, and this is most of a call's host time. One
+    tensor of all layers' pools is one check."""
     T = torch.Tensor
+    if isinstance(pools, T):
+        at = _arg(pools, name, dtype, dev, (len(pools), *shape))
+        step = pools[0].nbytes
+        return array.array("Q", range(at, at + len(pools) * step, step) if step else [at] * len(pools))
     if not (set(map(_LAYOUT, pools)) == {(dtype, shape)} and set(map(T.get_device, pools)) == {dev}
             and all(map(T.is_contiguous, pools))):
         for i, t in enumerate(pools):
@@ -795,8 +800,6 @@ def _compact_tree(sym, k_caches, v_caches, kv_scales, block_tables, ctx_lens, pa
         raise ValueError("k_caches, v_caches and kv_scales must list the same layers")
     if layers == 0:
         return
-    k_caches, v_caches, kv_scales = (x.unbind(0) if isinstance(x, torch.Tensor) else x
-                                     for x in (k_caches, v_caches, kv_scales))
     dev, handle, _ = _place(k_caches[0], "k_caches[0]", stream)
     P, hkv, B, D = shape = k_caches[0].shape
     n, mb = block_tables.shape

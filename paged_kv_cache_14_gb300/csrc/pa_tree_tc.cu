@@ -5,10 +5,20 @@
 // once for floor(128 / G) nodes. Per 64-key tile and 128-wide head a CTA reads
 // 32 KB of a 16-bit cache, which takes its share of HBM about 1400 cycles at
 // two CTAs per SM; the two products take 640 tensor-pipe cycles (S = Q K^T
-// re-reads Q from shared memory: 8 steps of 48 cycles; O += P V 4 of 64), so
-// the kernel is bound by HBM up to two query tiles per KV head, whether the
-// rows are all in use or not. Two CTAs share an SM: one's prologue, epilogue
-// and piece switches run under the other's stream.
+// re-reads Q from shared memory: 8 steps of 48 cycles; O += P V 4 of 64),
+// whether the rows are all in use or not. Two CTAs share an SM: one's prologue,
+// epilogue and piece switches run under the other's stream. Measured:
+//   4 sequences of 131072, trees of 12, group 8: 246 us, HBM (6.7 TB/s);
+//   64 of 4096, trees of 16, group 4: 118 us, HBM at 78% of its cycles;
+//   48 of 8192, trees of 40, group 8 (two or three query tiles a KV head):
+//     301 us; the tensor unit is busy 73% of the cycles (50% in its pipe, the
+//     rest on its operands' way), HBM 61%;
+//   64 of 4096 over an e4m3 cache, trees of 16, group 8: 141 us, HBM at 34%:
+//     a tile's 2850 cycles are the latency of one softmax thread's row of 64
+//     scores and of the hand-overs around it. Two threads a row (234 us), one
+//     pass over the row with registers moved between warpgroups (168) and
+//     converters that fetch the codes themselves (164) were slower, as more
+//     warps wait on more barriers.
 //
 //   warps 0, 6  producers: Q tile of each piece and K tiles, V tiles, through
 //               the block table into rings of NK and NV stages;
@@ -24,6 +34,14 @@
 //               and move a bf16 Q tile into fp16, a power of two per row.
 // All roles walk the CTA's pieces; stages, S tiles and their barriers are
 // counted over all tiles of the CTA, so the rings run on across pieces.
+//
+// Scores, maxima, sums and O are held in 32 bits. Two things are rounded to 16:
+// a softmax weight, as the second product's operand (its sum takes it as it
+// was, so a row's error is half a step of its largest weights, the size of the
+// output's own rounding); and over an 8-bit cache a bf16 row of q, into fp16 by
+// a power of two (exact for all that lies within 2^24 of the row's largest),
+// since codes are exact in fp16 only. The V scale of a block is taken into the
+// weight before that rounding, by a power of two that keeps it below 2^15.
 //
 // A row must not see other branches' values, whatever they hold, but P V
 // multiplies every row's weights (0 for those) with every key's values. So
