@@ -629,12 +629,13 @@ def _scratch(like: torch.Tensor, shape, dtype, side) -> torch.Tensor:
     """A new tensor for a call on the current stream or on another one (side).
     Memory comes from the stream that writes it first, so that whatever used
     it before is over by then; the caller may go on to read it on the current
-    one, which is why that one is recorded."""
+    one, which is why that one is recorded. (Tensor.new_empty between kernel
+    launches takes twice torch.empty's time.)"""
     if side is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     here = torch.cuda.current_stream()
     with torch.cuda.stream(side):
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
     t.record_stream(here)
     return t
 
@@ -694,7 +695,7 @@ def _decode_tree(sym, q, cu_q_lens, parents, k_cache, v_cache, kv_scales, block_
         out = _scratch(q, (T, hq, D), dt, side)
     if workspace is None:
         need = lib.pa_decode_tree_workspace_size(n, hq, hkv, D, B, T, max_q_len, max_kv_len, code)
-        workspace = _scratch(q, max(need, 16), torch.uint8, side)
+        workspace = _scratch(q, (max(need, 16),), torch.uint8, side)
     pools = (_arg(k_cache, "k_cache", kv, dev, pool), _arg(v_cache, "v_cache", kv, dev, pool))
     if kv_scales is not None:
         pools += (_arg(kv_scales, "kv_scales", torch.float32, dev, (P, hkv, 2)),)
@@ -739,9 +740,9 @@ def pa_verify_tree(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
     if path is None:
         path = _scratch(target_probs, (n, max_path_len), i32, side)
     if path_lens is None:
-        path_lens = _scratch(target_probs, n, i32, side)
+        path_lens = _scratch(target_probs, (n,), i32, side)
     if next_tokens is None:
-        next_tokens = _scratch(target_probs, n, i32, side)
+        next_tokens = _scratch(target_probs, (n,), i32, side)
     rc = lib.pa_verify_tree(
         tp, ts, dp, ds, _arg(draft_tokens, "draft_tokens", i32, dev, rows),
         _arg(cu_q_lens, "cu_q_lens", i32, dev, (n + 1,)), _arg(parents, "parents", i32, dev, rows),
@@ -774,7 +775,7 @@ def pa_compact_tree_e5m2(k_caches, v_caches, kv_scales, block_tables: torch.Tens
                   stream)
 
 
-_LAYOUT = operator.attrgetter("dtype", "shape")
+_DTYPE, _SHAPE = operator.attrgetter("dtype"), operator.attrgetter("shape")
 
 
 def _pools(pools, name: str, dtype, dev: int, shape) -> array.array:
@@ -786,8 +787,8 @@ def _pools(pools, name: str, dtype, dev: int, shape) -> array.array:
         at = _arg(pools, name, dtype, dev, (len(pools), *shape))
         step = pools[0].nbytes
         return array.array("Q", range(at, at + len(pools) * step, step) if step else [at] * len(pools))
-    if not (set(map(_LAYOUT, pools)) == {(dtype, shape)} and set(map(T.get_device, pools)) == {dev}
-            and all(map(T.is_contiguous, pools))):
+    if not (set(map(_DTYPE, pools)) == {dtype} and list(map(_SHAPE, pools)) == [shape] * len(pools)
+            and set(map(T.get_device, pools)) == {dev} and all(map(T.is_contiguous, pools))):
         for i, t in enumerate(pools):
             _arg(t, f"{name}[{i}]", dtype, dev, shape)
     return array.array("Q", map(T.data_ptr, pools))
