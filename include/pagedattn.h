@@ -594,7 +594,7 @@ int pa_chunked_prefill_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_
  *                of a sequence; a sequence above them, or with a cu_q_lens
  *                that falls or leaves [0, total_q], records PA_ERR_SEQLEN and
  *                its rows are not written
- *   out        : [total_q][num_q_heads][head_dim]
+ *   out        : [total_q][num_q_heads][head_dim]; must not overlap q
  *   workspace  : pa_decode_tree_workspace_size() bytes, 16-byte aligned, no
  *                initialisation needed; not shared by calls that overlap. Its
  *                size depends on the device's SM count, not on the lengths.
@@ -686,8 +686,9 @@ int pa_verify_tree(const void* target_probs, int64_t target_stride, const void* 
  * position ctx_lens[i] + k, as if all were read before any is written. The
  * sequence then has ctx_lens[i] + path_lens[i] cached tokens.
  *   k_caches, v_caches : HOST arrays of num_layers device pointers, the pools
- *                  of each layer (same shape; one block table serves them
- *                  all); read before the call returns
+ *                  of each layer (same shape, none twice; one block table
+ *                  serves them all); the arrays are read before the call
+ *                  returns
  *   path, path_lens : int32 device, as pa_verify_tree writes them; any
  *                  strictly rising path of nodes >= 0 will do, and length 0.
  *                  max_path_len at most 1024.
