@@ -666,13 +666,14 @@ int pa_decode_tree_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_lens
  * Probabilities outside [0, 1] are held to it and NaN counts as 0; a row
  * without any probability gives next token -1 and PA_ERR_ARG. Sums are taken
  * over weights formed from whole multiples of 2^-43 (within two of them),
- * exactly, so results do not depend on the order in which the device runs. A
- * sequence whose cu_q_lens falls, leaves [0, total_q] or has more than
- * max_q_len nodes records PA_ERR_SEQLEN, one with a parent that is not below
- * its node (or a node 0 that is no root) PA_ERR_ARG; both get path_lens 0 and
- * next token -1. vocab_size is at most 262144 (PA_ERR_UNSUPPORTED),
- * max_path_len at least 1. Rows need no alignment beyond their element's
- * (PA_ERR_ALIGN).
+ * exactly, so results do not depend on the order in which the device runs (a
+ * mass of w below some 2^-40 is not resolved; refusals leave that little only
+ * with that probability). A sequence whose cu_q_lens falls, leaves
+ * [0, total_q] or has more than max_q_len nodes records PA_ERR_SEQLEN, one with
+ * a parent that is not below its node (or a node 0 that is no root)
+ * PA_ERR_ARG; both get path_lens 0 and next token -1. vocab_size is at most
+ * 262144 (PA_ERR_UNSUPPORTED), max_path_len at least 1. Rows need no alignment
+ * beyond their element's (PA_ERR_ALIGN).
  */
 int pa_verify_tree(const void* target_probs, int64_t target_stride, const void* draft_probs, int64_t draft_stride,
                    const int32_t* draft_tokens, const int32_t* cu_q_lens, const int32_t* parents,

@@ -326,7 +326,10 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 4 ? 2 : DRAFT ? 3
         kids &= kids - 1;
         if constexpr (DRAFT) {
           if (C == 0.0) {
-            if (fmaf(ua[j], qx[j], -px[j]) < 0.f) {  // u q < p (one rounding keeps the sign)
+            // u q < p: one rounding keeps the sign, 2^64 times as large also that of
+            // subnormal numbers.
+            constexpr float kUp = 18446744073709551616.f;
+            if (fmaf(ua[j], qx[j] * kUp, -px[j] * kUp) < 0.f) {
               step = j;
               break;
             }

@@ -280,3 +280,15 @@ def test_on_another_stream(lib):
     assert all((x == 7).all() for x in kept)
     for g, r in zip(got, ref):
         assert torch.equal(g, r)
+
+
+def test_subnormal_probabilities(lib):
+    """u q < p for equal subnormal p and q and the largest u below 1: kept."""
+    c = case(19, "f32", [2, 2, 2], 40)
+    for i, tiny in enumerate((2.0 ** -149, 2.0 ** -140, 3.0 * 2.0 ** -130)):
+        token = c["tokens"][2 * i + 1]
+        for name in ("target", "draft"):
+            c[name][2 * i, token] = tiny
+    c["ua"][:] = 1 - 2.0 ** -24
+    ref = check(lib, c)
+    assert (ref[1] == 2).all()
