@@ -606,10 +606,12 @@ def _refuse(t, name: str, dtype, dev: int, shape) -> None:
 def _arg(t, name: str, dtype, dev: int, shape) -> int:
     """Pointer of a contiguous tensor of this type and shape on device dev
     (the current one: the calls launch there)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
-            and t.is_contiguous()):
-        _refuse(t, name, dtype, dev, shape)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    _refuse(t, name, dtype, dev, shape)
 
 
 def _place(t, name: str, stream) -> tuple[int, int, object]:
