@@ -13,7 +13,7 @@
 //   48 of 8192, trees of 40, group 8 (two or three query tiles a KV head):
 //     301 us; the tensor unit is busy 73% of the cycles (50% in its pipe, the
 //     rest on its operands' way), HBM 61%;
-//   64 of 4096 over an e4m3 cache, trees of 16, group 8: 141 us, HBM at 34%:
+//   64 of 4096 over an e4m3 cache, trees of 16, group 8: 145 us, HBM at 34%:
 //     a tile's 2850 cycles are the latency of one softmax thread's row of 64
 //     scores and of the hand-overs around it. Two threads a row (234 us), one
 //     pass over the row with registers moved between warpgroups (168) and
@@ -41,7 +41,8 @@
 // output's own rounding); and over an 8-bit cache a bf16 row of q, into fp16 by
 // a power of two (exact for all that lies within 2^24 of the row's largest),
 // since codes are exact in fp16 only. The V scale of a block is taken into the
-// weight before that rounding, by a power of two that keeps it below 2^15.
+// weight before that rounding, by a power of two that keeps it below 2^15: a
+// row's own, from the blocks that it sees a key of.
 //
 // A row must not see other branches' values, whatever they hold, but P V
 // multiplies every row's weights (0 for those) with every key's values. So
@@ -564,9 +565,13 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
             // scores of 16-key group u are s * f_u, f_u >= 0, so a group's
             // largest is its raw largest times f_u exactly.
             const float2* scales = reinterpret_cast<const float2*>(smem + C::kOffScale) + (g % kScaleSlots) * (kN / 16);
+            // Groups that the row sees no key of stay out, here and below: another
+            // branch's block may have any V scale. (A seen group's scale is
+            // that of values the row sees.)
             float vmax = 0.f;
 #pragma unroll
-            for (int u = 0; u < kN / 16; ++u) vmax = fmaxf(vmax, scales[u].y);
+            for (int u = 0; u < kN / 16; ++u)
+              if ((seen[u >> 1] >> (16 * (u & 1))) & 0xffffu) vmax = fmaxf(vmax, scales[u].y);
             float kap_r = 1.f;  // 2^(new kap - old kap) where kap drops
             if (vmax > 0.f) {
               // 2^kap brings the largest V scale seen so far below 2^7.
@@ -607,8 +612,9 @@ __global__ void __launch_bounds__(tt::threads<KV8>(), 2)
               uint32_t v[32], pk[16];
               tmem_ld32(ts + h * 32, v);
               const float2 s0 = scales[h * 2], s1 = scales[h * 2 + 1];
-              const float f0 = s0.x * rf, f1 = s1.x * rf, w0 = s0.y * pw, w1 = s1.y * pw;
               const uint32_t bits = h ? seen[1] : seen[0];
+              const float f0 = s0.x * rf, f1 = s1.x * rf;
+              const float w0 = bits & 0xffffu ? s0.y * pw : 0.f, w1 = bits >> 16 ? s1.y * pw : 0.f;
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {

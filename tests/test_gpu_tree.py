@@ -395,3 +395,61 @@ def test_pools_beyond_32_bits(lib):
         a.clear()
         del pool, out
         torch.cuda.empty_cache()
+
+
+def _with_a_hidden_block(seed, nodes, first, size):
+    """Parents of a tree whose nodes first .. first + size - 1 are leaves: no
+    other node sees them."""
+    rng = np.random.default_rng(seed)
+    out = [-1]
+    for j in range(1, nodes):
+        ok = [a for a in range(max(0, j - 30), j) if not first <= a < first + size]
+        out.append(int(rng.choice(ok or [0])))
+    return out
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), 2.0 ** 22, 2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("ctx", [32, 5024])
+@pytest.mark.parametrize("block", [16, 32])
+def test_scales_of_other_branches_do_not_matter(lib, kv, scale, which, ctx, block):
+    """The scale of a block that holds nodes of other branches alone reaches
+    no row of the others, whatever it is."""
+    nodes, first = 100, 32
+    b = tree_batch(33, "bf16", [ctx, 20], [nodes, 8], 8, 2, 128, block, kv=kv)
+    b.parents[:nodes] = _with_a_hidden_block(34, nodes, first, block)
+    clean = b.call(lib).clone()
+    w = "kv".index(which)
+    b.scales[b.table[0, (ctx + first) // block], :, w] *= np.float32(scale)
+    got = b.call(lib)
+    assert lib.pa_get_status() == 0
+    others = [j for j in range(nodes + 8) if not first <= j < first + block]
+    assert torch.equal(got[others], clean[others])
+    if w and np.isfinite(scale):
+        assert_tree_close(b, got)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "e5m2"])
+def test_a_drafted_infinity_stays_in_its_block(lib, kv):
+    """The cache write gives the block of a V row that is not finite the scale
+    infinity: rows that see nothing of the block are as without it."""
+    nodes, ctx, first = 100, 32, 32
+    b = tree_batch(35, "bf16", [ctx], [nodes], 8, 2, 128, kv=kv)
+    b.parents[:] = _with_a_hidden_block(36, nodes, first, 16)
+    rng = np.random.default_rng(37)
+    k, v = (torch.from_numpy(rng.standard_normal((nodes, 2, 128)).astype(np.float32)).bfloat16() for _ in range(2))
+    pos = ctx + np.arange(nodes)
+    slots = torch.from_numpy(b.table[0, pos // 16].astype(np.int64) * 16 + pos % 16).cuda()
+    form = {"e4m3": "fp8", "e5m2": "e5m2"}[kv]
+    outs = []
+    for value in (1.0, float("inf")):
+        a = b.device()
+        v[first + 8] = value
+        getattr(lib, f"pa_reshape_and_cache_{form}")(k.cuda(), v.cuda(), slots, a["k_cache"], a["v_cache"],
+                                                     a["kv_scales"])
+        outs.append(getattr(lib, f"pa_decode_tree_{form}")(**a))
+    assert lib.pa_get_status() == 0
+    others = [j for j in range(nodes) if not first <= j < first + 16]
+    assert torch.equal(outs[0][others], outs[1][others])
+    assert not torch.isfinite(outs[1][first + 8].float()).any()
