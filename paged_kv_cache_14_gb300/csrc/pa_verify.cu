@@ -334,10 +334,12 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 4 ? 2 : DRAFT ? 3
               break;
             }
           } else {
-            // S is put off until it decides: it is at most the last one, so a
-            // child that would be kept with that is kept.
+            // S is put off until it decides: from the second sum on it is at most
+            // the last one, so a child that would be kept with that is kept.
+            // (Not so the first, C = 1: a row may sum to more than 1.)
             const double w = fmax(0.0, (double)px[j] - C * (double)qx[j]);
-            if (stale && !((double)ua[j] * (double)qx[j] * S < w)) S = (double)total(at, C, false) * kVerifyUnit;
+            if (stale && (C == 1.0 || !((double)ua[j] * (double)qx[j] * S < w)))
+              S = (double)total(at, C, false) * kVerifyUnit;
             if ((double)ua[j] * (double)qx[j] * S < w) {
               step = j;
               break;

@@ -292,3 +292,40 @@ def test_subnormal_probabilities(lib):
     c["ua"][:] = 1 - 2.0 ** -24
     ref = check(lib, c)
     assert (ref[1] == 2).all()
+
+
+def test_masses_above_one(lib):
+    """p sums to 1.8, so the first refusal leaves S = 1.3: 0.7 * 0.5 is below
+    the second child's weight 0.4, 0.7 * 0.5 * S is not."""
+    c = case(20, "f32", [3], 4, kind="star")
+    c["target"][0] = torch.tensor([0.0, 0.0, 0.9, 0.9])
+    c["draft"][0] = torch.tensor([0.5, 0.0, 0.5, 0.0])
+    c["tokens"][:] = [0, 0, 2]
+    c["ua"][:] = [0.0, 0.5, 0.7]
+    ref = check(lib, c)
+    assert ref[1][0] == 1
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_rounded_rows_with_masses_above_one(lib, dtype):
+    """16-bit rows that sum to a little more than 1 and drafts of other tokens:
+    S after the first refusal passes 1, with the second child's random number
+    between w / (q S) and w / q."""
+    rng = np.random.default_rng(21)
+    n, vocab = 64, 2000
+    c = case(21, dtype, [3] * n, vocab, kind="star")
+    p = torch.softmax(3.0 * torch.from_numpy(rng.standard_normal((3 * n, vocab)).astype(np.float32)), -1).to(DT[dtype])
+    q = torch.zeros_like(p)
+    between = 0
+    for r in range(0, 3 * n, 3):
+        order = p[r].argsort()
+        low, x = int(order[0]), int((p[r].double() - 1e-6).abs().argmin())
+        q[r, x], q[r, low] = 0.75 * p[r, x], 1.0 - 2.0 ** -8
+        pr, qr = p[r].double(), q[r].double()
+        S, w = float((pr - qr).clamp(min=0).sum()), float(pr[x] - qr[x])
+        u = np.float32(w / float(qr[x]) * (1 - 2.0 ** -22))
+        c["tokens"][r + 1], c["tokens"][r + 2], c["ua"][r + 1], c["ua"][r + 2] = low, x, 0.999, u
+        between += float(u) * float(qr[x]) < w <= float(u) * float(qr[x]) * S
+    c["target"], c["draft"] = p, q
+    assert between > n // 8
+    check(lib, c)
