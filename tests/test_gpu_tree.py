@@ -453,3 +453,62 @@ def test_a_drafted_infinity_stays_in_its_block(lib, kv):
     others = [j for j in range(nodes) if not first <= j < first + 16]
     assert torch.equal(outs[0][others], outs[1][others])
     assert not torch.isfinite(outs[1][first + 8].float()).any()
+
+
+@pytest.mark.parametrize("kv,code", [("e4m3", 0x7F), ("e4m3", 0xFF), ("e5m2", 0x7C), ("e5m2", 0xFC), ("e5m2", 0x7D)])
+@pytest.mark.parametrize("where", ["k", "v", "one value"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("ctx", [50, 5000])
+def test_codes_of_other_branches_do_not_matter(lib, kv, code, where, dtype, ctx):
+    """8-bit codes that are not finite in nodes of a tree: rows that do not see
+    them are as without them, the others are what the definition says."""
+    nodes = 70
+    b = tree_batch(10, dtype, [ctx, 20], [nodes, 8], 8, 2, 128, kv=kv)
+    bad = [3, 40]
+    below = [j for j in range(nodes) if set(bad) & set(_up(b.parents[:nodes], j))]
+    clean = b.call(lib).clone()
+    for blk, off in [(b.table[0, (ctx + j) // 16], (ctx + j) % 16) for j in bad]:
+        if where == "k":
+            b.k[blk, :, off] = code
+        elif where == "v":
+            b.v[blk, :, off] = code
+        else:
+            b.v[blk, 1, off, 77] = code
+    got = b.call(lib)
+    assert lib.pa_get_status() == 0
+    others = [j for j in range(nodes) if j not in below] + list(range(nodes, nodes + 8))
+    assert torch.equal(got[others], clean[others])
+    if where == "k":  # (128 infinite products of both signs are NaN too)
+        assert torch.isnan(got[below]).all()
+        return
+    ref = b.oracle()[0][below]
+    fine = np.isfinite(ref)
+    g = got[below].double().cpu().numpy()
+    assert (np.isfinite(g) == fine).all()
+    assert np.array_equal(np.isnan(g), np.isnan(ref))
+    assert np.array_equal(g[~fine & ~np.isnan(g)], ref[~fine & ~np.isnan(ref)])
+
+
+@pytest.mark.parametrize("dtype,kv", [("bf16", None), ("f32", None), ("f16", "e5m2"), ("bf16", "e4m3")])
+def test_what_the_neighbours_hold_does_not_matter(lib, dtype, kv):
+    """Other contents in the neighbours' blocks: the same bits. Other lengths
+    and trees beside it, which cut its keys elsewhere: within the tolerance."""
+    b = tree_batch(39, dtype, [800, 333, 470], [12, 8, 30], 32, 8, 128, kv=kv)
+    first = b.call(lib).clone()
+    mine = b.table[1, :-(-341 // 16)]
+    mine = mine.astype(np.int64)
+    other = np.setdiff1d(np.arange(b.k.shape[0]), mine)
+    for x in (b.k, b.v):
+        x[other] = x[other[::-1].copy()]
+    got = run(lib, b)
+    assert torch.equal(got[12:20], first[12:20])
+    assert not torch.equal(got[:12], first[:12])
+    for ctx, nodes in (([0, 333, 5000], [1, 8, 3]), ([70, 333, 64], [100, 8, 0])):
+        c = tree_batch(40, dtype, ctx, nodes, 32, 8, 128, kv=kv)
+        at = [nodes[0], nodes[0] + 8]
+        c.q[at[0]:at[1]], c.parents[at[0]:at[1]] = b.q[12:20], b.parents[12:20]
+        hold = c.table[1, :len(mine)].astype(np.int64)
+        c.k[hold], c.v[hold] = b.k[mine], b.v[mine]
+        if kv:
+            c.scales[hold] = b.scales[mine]
+        run(lib, c)
