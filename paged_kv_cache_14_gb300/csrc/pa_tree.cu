@@ -301,9 +301,11 @@ __device__ __forceinline__ void join_rows(const TreeParams& p, const TreeMerge& 
     for (int k0 = 0; k0 < parts; k0 += LOOK) {
       const float2 ml = k0 == 0 ? first : piece_ml(k0 + mk);
       // A piece whose keys the row sees none of (m = -inf, l = 0) weighs
-      // nothing, whatever the row's maximum is.
+      // nothing, whatever the row's maximum is. One that weighs next to
+      // nothing still counts: 0 times an infinity or NaN that the row sees is
+      // NaN, as it is within a piece.
       const float w = ml.x == -CUDART_INF_F && ml.y == 0.f ? 0.f : exp2f(ml.x - M);
-      L += w == 0.f ? 0.f : w * ml.y;
+      L += w * ml.y;
 #pragma unroll
       for (int k1 = 0; k1 < LOOK; k1 += BATCH) {
         if (k0 + k1 >= parts) break;
@@ -321,12 +323,10 @@ __device__ __forceinline__ void join_rows(const TreeParams& p, const TreeMerge& 
 #pragma unroll
           for (int i = 0; i < ROWS; ++i) {
             const float wk = __shfl_sync(0xffffffffu, w, i * LOOK + k1 + k);
-            if (wk != 0.f) {
-              acc[i].x = fmaf(wk, v[i][k].x, acc[i].x);
-              acc[i].y = fmaf(wk, v[i][k].y, acc[i].y);
-              acc[i].z = fmaf(wk, v[i][k].z, acc[i].z);
-              acc[i].w = fmaf(wk, v[i][k].w, acc[i].w);
-            }
+            acc[i].x = fmaf(wk, v[i][k].x, acc[i].x);
+            acc[i].y = fmaf(wk, v[i][k].y, acc[i].y);
+            acc[i].z = fmaf(wk, v[i][k].z, acc[i].z);
+            acc[i].w = fmaf(wk, v[i][k].w, acc[i].w);
           }
       }
     }

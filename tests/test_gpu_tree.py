@@ -512,3 +512,28 @@ def test_what_the_neighbours_hold_does_not_matter(lib, dtype, kv):
         if kv:
             c.scales[hold] = b.scales[mine]
         run(lib, c)
+
+
+@pytest.mark.parametrize("dtype,kv", [("bf16", None), ("f32", None), ("bf16", "e4m3")])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_not_finite_under_a_small_weight(lib, dtype, kv, what):
+    """A NaN that a row sees reaches it from wherever the context is cut, also
+    from keys whose weights are 0 in fp32 beside the others'."""
+    b = tree_batch(38, dtype, [9000, 20], [6, 2], 8, 2, 128, kv=kv)
+    b.q[:6, :, 0] = 40.0
+    large = b.table[0, 4000 // 16:5000 // 16].astype(np.int64)  # scores of some 1000
+    at, nan = int(b.table[0, 100 // 16]), float("nan")
+    if kv is None:
+        b.k[large, :, :, 0] = 300.0
+    else:
+        b.scales[large, :, 0] = 2.0
+        b.k[large, :, :, 0], nan = 0x77, 0x7F
+    got = b.call(lib)
+    assert torch.isfinite(got).all()
+    (b.k if what == "k" else b.v)[at, :, 100 % 16, 5] = nan
+    got = b.call(lib)
+    assert lib.pa_get_status() == 0
+    assert torch.isnan(got[:6] if what == "k" else got[:6, :, 5]).all()
+    assert torch.isfinite(got[6:]).all()
+    if what == "v":
+        assert torch.isfinite(torch.cat([got[:6, :, :5], got[:6, :, 6:]], -1)).all()
