@@ -624,7 +624,10 @@ def _place(t, name: str, stream) -> tuple[int, int, object]:
     if stream is None:
         return dev, here, None
     handle = _stream(stream)
-    return dev, handle, None if handle == here else torch.cuda.ExternalStream(handle)
+    if handle == here:
+        return dev, handle, None
+    # (ExternalStream makes a new stream of handle 0, which is the default one's.)
+    return dev, handle, torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream(dev)
 
 
 def _scratch(like: torch.Tensor, shape, dtype, side) -> torch.Tensor:

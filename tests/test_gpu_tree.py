@@ -537,3 +537,30 @@ def test_not_finite_under_a_small_weight(lib, dtype, kv, what):
     assert torch.isfinite(got[6:]).all()
     if what == "v":
         assert torch.isfinite(torch.cat([got[:6, :, :5], got[:6, :, 6:]], -1)).all()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_the_default_stream(lib, handle):
+    """A call on the default stream, made while another one is current, takes
+    no memory that some third stream still has to read."""
+    b = tree_batch(41, "bf16", [500, 44], [9, 30], 16, 4, 128)
+    a = b.device()
+    ws = lib.pa_decode_tree_workspace_size(2, 16, 4, 128, 16, 39, a["max_q_len"], a["max_kv_len"])
+    current = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # Streams come from a ring of 32: the next one given out is the first again.
+    # (A few are enough; with all of them the call would wait for a place on the device.)
+    streams = [torch.cuda.Stream() for _ in range(32)][:3]
+    for sleep in (0, 50_000_000):  # (the first time for the streams' memory, which takes longer than the sleep)
+        kept = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                old = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in (ws, a["q"].nbytes)]
+                torch.cuda._sleep(sleep)
+                kept += [x.clone() for x in old]
+                del old
+    with torch.cuda.stream(current):
+        out = lib.pa_decode_tree(**a, stream=0 if handle else torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    assert all((x == 7).all() for x in kept)
+    assert_tree_close(b, out)
