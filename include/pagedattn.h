@@ -591,9 +591,10 @@ int pa_chunked_prefill_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_
  *   q          : [total_q][num_q_heads][head_dim]
  *   ctx_lens   : int32 [num_seqs]; committed tokens before the tree (>= 0)
  *   max_q_len, max_kv_len : host upper bounds of the nodes and of ctx + nodes
- *                of a sequence; a sequence above them, or with a cu_q_lens
- *                that falls or leaves [0, total_q], records PA_ERR_SEQLEN and
- *                its rows are not written
+ *                of a sequence (no sequence may have more than 2^31 - 64); a
+ *                sequence above them, or with a cu_q_lens that falls or leaves
+ *                [0, total_q], records PA_ERR_SEQLEN and its rows are not
+ *                written
  *   out        : [total_q][num_q_heads][head_dim]; must not overlap q
  *   workspace  : pa_decode_tree_workspace_size() bytes, 16-byte aligned, no
  *                initialisation needed; not shared by calls that overlap. Its

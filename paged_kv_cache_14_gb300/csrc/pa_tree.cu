@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdint>
 
 #include "pa_tree.cuh"
 
@@ -445,7 +446,7 @@ TreeLayout tree_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_hea
   }
   // Most key tiles there can be: one more query tile than its rows fill for every sequence.
   const double units = ((double)total_q * group / w.tile_rows + std::min(num_seqs, total_q)) * num_kv_heads;
-  const double most = units * ((max_kv_len + w.tile_keys - 1) / w.tile_keys) + 1;
+  const double most = units * (((int64_t)max_kv_len + w.tile_keys - 1) / w.tile_keys) + 1;
   w.ctas = (int)std::max(1.0, std::min(most, (double)per_sm * num_sms_current_device()));
   w.ctas = (w.ctas + w.team - 1) / w.team * w.team;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -493,7 +494,8 @@ int decode_tree(const void* q, int32_t total_q, const int32_t* cu_q_lens, const 
   p.num_seqs = num_seqs;
   p.total_q = total_q;
   p.max_q_len = max_q_len;
-  p.max_kv_len = max_kv_len;
+  // Positions are 32-bit, also that behind a last tile.
+  p.max_kv_len = std::min(max_kv_len, INT32_MAX - 63);
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
   p.head_dim = head_dim;

@@ -564,3 +564,24 @@ def test_memory_of_the_default_stream(lib, handle):
     torch.cuda.synchronize()
     assert all((x == 7).all() for x in kept)
     assert_tree_close(b, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_beyond_32_bits(lib, dtype):
+    """A sequence whose last tile would end behind position 2^31 is reported
+    and left alone, also under the largest bound."""
+    b = tree_batch(42, dtype, [100, 50], [4, 9], 8, 2, 64)
+    a = b.device()
+    ref = lib.pa_decode_tree(**a).clone()
+    a["max_kv_len"] = 2 ** 31 - 1
+    wide = torch.zeros(2, 2 ** 27, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = a["block_tables"]
+    a["block_tables"] = wide
+    out = torch.full_like(ref, 7.0)
+    assert_tree_close(b, lib.pa_decode_tree(**a, out=out))
+    assert lib.pa_get_status() == 0
+    for ctx in (2 ** 31 - 12, 2 ** 31 - 72):
+        a["ctx_lens"][1] = ctx
+        lib.pa_decode_tree(**a, out=out.fill_(7.0))
+        assert lib.pa_get_status() == -8
+        assert (out[4:] == 7.0).all() and torch.equal(out[:4], ref[:4])

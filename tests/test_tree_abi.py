@@ -135,3 +135,12 @@ def test_binding_refuses_layer_lists():
     i32 = torch.int32
     with pytest.raises(ValueError, match="same layers"):
         pa.pa_compact_tree([z(3, 2, 16, 64)], [], z(1, 3, dt=i32), z(1, dt=i32), z(1, 4, dt=i32), z(1, dt=i32))
+
+
+def test_tree_workspace_at_the_largest_bounds():
+    """Bounds up to 2^31 - 1 do not wrap: the workspace is that of a full machine."""
+    size = pa.pa_decode_tree_workspace_size
+    for dtype in (torch.bfloat16, torch.float32):
+        full = size(64, 64, 8, 128, 16, 4096, 64, 10 ** 6, dtype)
+        for bound in (2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 32, 2 ** 31 - 1):
+            assert size(64, 64, 8, 128, 16, 4096, 64, bound, dtype) == full
