@@ -601,11 +601,12 @@ int pa_chunked_prefill_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_
  *                size depends on the device's SM count, not on the lengths.
  * A parent that is not below its node records PA_ERR_ARG (the node then
  * counts as a root); a block outside the pool records PA_ERR_BLOCK_OOB, and
- * the rows that see it are unspecified. fp16/bf16: head_dim 64 or 128, a GQA group of at most
- * 128 and scale > 0 (PA_ERR_UNSUPPORTED, PA_ERR_ARG otherwise); the softmax
- * weights are rounded to the 16-bit type for the second product, as in
- * pa_decode. fp32: head_dim a multiple of 32 up to 256, exact fp32
- * arithmetic, any finite scale. Rows are computed from their own sequence
+ * the rows that see it are unspecified. num_seqs is at most 65535. fp16/bf16:
+ * head_dim 64 or 128, a GQA group of at most 128, pools of fewer than 2^31 rows
+ * (num_blocks * num_kv_heads * block_size) and scale > 0 (PA_ERR_UNSUPPORTED,
+ * PA_ERR_ARG otherwise); the softmax weights are rounded to the 16-bit type for
+ * the second product, as in pa_decode. fp32: head_dim a multiple of 32 up to
+ * 256, exact fp32 arithmetic, any finite scale. Rows are computed from their own sequence
  * alone; results do not depend on the order in which the device runs.
  */
 size_t pa_decode_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,

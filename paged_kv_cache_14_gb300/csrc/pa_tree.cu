@@ -469,7 +469,8 @@ int decode_tree(const void* q, int32_t total_q, const int32_t* cu_q_lens, const 
   if (dtype != PA_F32 && !(scale > 0.f)) return PA_ERR_ARG;
   if (kv8 && dtype == PA_F32) return PA_ERR_DTYPE;
   if (kv8 && head_dim != 128) return PA_ERR_UNSUPPORTED;
-  if ((int64_t)num_blocks * num_kv_heads * block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  // (Rows are 32-bit coordinates of a tensor map there.)
+  if (dtype != PA_F32 && (int64_t)num_blocks * num_kv_heads * block_size >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0 || total_q == 0) return PA_OK;
   if (!q || !cu_q_lens || !parents || !k_cache || !v_cache || !block_tables || !ctx_lens || !out) return PA_ERR_ARG;
   if (kv8 && !kv_scales) return PA_ERR_ARG;

@@ -144,3 +144,13 @@ def test_tree_workspace_at_the_largest_bounds():
         full = size(64, 64, 8, 128, 16, 4096, 64, 10 ** 6, dtype)
         for bound in (2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 32, 2 ** 31 - 1):
             assert size(64, 64, 8, 128, 16, 4096, 64, bound, dtype) == full
+
+
+def test_tree_pool_sizes(lib):
+    """Pools of 2^31 rows: refused where tensor maps address them, taken by
+    the fp32 call, whose offsets are 64-bit."""
+    for nb, hkv in ((2 ** 27, 2), (2 ** 26, 2), (2 ** 27, 1)):
+        assert _tree(lib, nb=nb, hkv=hkv) == -10
+        assert _tree(lib, "pa_decode_tree_fp8", nb=nb, hkv=hkv) == -10
+        assert _tree(lib, nb=nb, hkv=hkv, dt=pa.PA_F32) == NO_WORKSPACE
+    assert _tree(lib, nb=2 ** 26 - 1, hkv=2) == NO_WORKSPACE
