@@ -101,12 +101,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, const TreeLens&
   s.ctx = r.ctx;
   s.nodes = s.ktiles = s.qtiles = s.places = 0;
   const int64_t n = (int64_t)r.q1 - r.q0, kv = r.ctx + n;
-  if (n == 0) return s;
-  if (n < 0 || r.q0 < 0 || r.q1 > p.total_q || n > p.max_q_len || r.ctx < 0 ||
-      kv > min((int64_t)p.max_kv_len, (int64_t)p.max_blocks_per_seq * p.block_size)) {
+  // (A sequence without nodes sits the step out, whatever its context is.)
+  if (n < 0 || r.q0 < 0 || r.q1 > p.total_q ||
+      (n > 0 && (n > p.max_q_len || r.ctx < 0 ||
+                 kv > min((int64_t)p.max_kv_len, (int64_t)p.max_blocks_per_seq * p.block_size)))) {
     if (report) record_error(p.status, PA_ERR_SEQLEN);
     return s;
   }
+  if (n == 0) return s;
   s.nodes = (int)n;
   s.ktiles = (int)(((uint32_t)kv + p.tile_keys - 1) / (uint32_t)p.tile_keys);
   s.qtiles = (s.nodes * p.group + p.tile_rows - 1) / p.tile_rows;

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kVerifyThreads, sizeof(T) == 4 ? 2 : DRAFT ? 3
   cluster.barrier_wait(std::move(started));
   if (bad_len || bad_tree || n == 0) {  // (the same in every CTA of the cluster)
     if (rank == 0) {
-      if (tid == 0 && n64 != 0) record_error(p.status, bad_len ? PA_ERR_SEQLEN : PA_ERR_ARG);
+      if (tid == 0 && (bad_len || bad_tree)) record_error(p.status, bad_len ? PA_ERR_SEQLEN : PA_ERR_ARG);
       for (int k = tid; k < p.max_path_len; k += kVerifyThreads) path[k] = -1;
       if (tid == 0) p.path_lens[seq] = 0, p.next_tokens[seq] = -1;
     }

@@ -585,3 +585,20 @@ def test_sequences_beyond_32_bits(lib, dtype):
         lib.pa_decode_tree(**a, out=out.fill_(7.0))
         assert lib.pa_get_status() == -8
         assert (out[4:] == 7.0).all() and torch.equal(out[:4], ref[:4])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_empty_sequences_outside_the_rows(lib, dtype):
+    """A cu_q_lens that leaves [0, total_q] is reported for a sequence without
+    nodes too; one inside it is not, whatever its context says."""
+    b = tree_batch(43, dtype, [100, 50, 70], [4, 0, 9], 8, 2, 64)
+    ref = b.call(lib).clone()
+    a = b.device()
+    a["ctx_lens"][1] = 10 ** 6
+    assert torch.equal(lib.pa_decode_tree(**a), ref)
+    assert lib.pa_get_status() == 0
+    a = b.device()
+    for cu, status in (([0, 4, 13, 13], 0), ([13] * 4, 0), ([14] * 4, -8), ([-1] * 4, -8), ([0, 4, 13, 14], -8)):
+        a["cu_q_lens"].copy_(torch.tensor(cu, dtype=torch.int32))
+        lib.pa_decode_tree(**a)
+        assert lib.pa_get_status() == status, cu

@@ -329,3 +329,14 @@ def test_rounded_rows_with_masses_above_one(lib, dtype):
     c["target"], c["draft"] = p, q
     assert between > n // 8
     check(lib, c)
+
+
+def test_empty_sequences_outside_the_rows(lib):
+    """A cu_q_lens that leaves [0, total_q] is reported for a sequence without
+    nodes too."""
+    c = case(22, "f32", [5, 0, 5], 100)
+    check(lib, c)
+    for first in (-1, 11, 2 ** 31 - 1):
+        got = call(lib, dict(c, cu=np.full(4, first, np.int32)), max_q_len=5)
+        assert lib.pa_get_status() == -8
+        assert (got[1] == 0).all() and (got[2] == -1).all()
