@@ -689,9 +689,9 @@ int pa_verify_tree(const void* target_probs, int64_t target_stride, const void* 
  * position ctx_lens[i] + k, as if all were read before any is written. The
  * sequence then has ctx_lens[i] + path_lens[i] cached tokens.
  *   k_caches, v_caches : HOST arrays of num_layers device pointers, the pools
- *                  of each layer (same shape, none twice; one block table
- *                  serves them all); the arrays are read before the call
- *                  returns
+ *                  of each layer (same shape, none twice: PA_ERR_ARG; one
+ *                  block table serves them all; layers that share a pool list
+ *                  it once); the arrays are read before the call returns
  *   path, path_lens : int32 device, as pa_verify_tree writes them; any
  *                  strictly rising path of nodes >= 0 will do, and length 0.
  *                  max_path_len at most 1024.

@@ -12,6 +12,9 @@
 // HBM needs; 4 sequences in one layer 3.3 us, a launch and three dependent
 // loads (lengths, path, blocks, rows).
 #include <algorithm>
+#include <functional>
+#include <memory>
+#include <new>
 
 #include "pa_common.cuh"
 #include "pa_fp8.cuh"
@@ -172,6 +175,20 @@ __global__ void __launch_bounds__(kCompactThreads) compact_8bit_kernel(const Com
   }
 }
 
+// Whether a pool (or scale array) is listed twice: its rows would be moved twice,
+// by CTAs that know nothing of each other.
+static int listed_twice(void* const* k, void* const* v, float* const* scales, int32_t n) {
+  std::unique_ptr<const void*[]> all(new (std::nothrow) const void*[2 * (size_t)n]);
+  if (!all) return PA_ERR_CUDA;
+  auto twice = [&](const void** end) {
+    std::sort(all.get(), end, std::less<const void*>());
+    return std::adjacent_find(all.get(), end) != static_cast<const void**>(end);
+  };
+  if (twice(std::copy(v, v + n, std::copy(k, k + n, all.get())))) return PA_ERR_ARG;
+  if (scales && twice(std::copy(scales, scales + n, all.get()))) return PA_ERR_ARG;
+  return PA_OK;
+}
+
 static int compact(void* const* k_caches, void* const* v_caches, float* const* kv_scales, int32_t num_layers,
                    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* ctx_lens,
                    const int32_t* path, const int32_t* path_lens, int32_t num_seqs, int32_t max_path_len,
@@ -194,6 +211,8 @@ static int compact(void* const* k_caches, void* const* v_caches, float* const* k
     if (!aligned16(k_caches[i]) || !aligned16(v_caches[i])) return PA_ERR_ALIGN;
     if (kv8 && (reinterpret_cast<uintptr_t>(kv_scales[i]) & 3u)) return PA_ERR_ALIGN;
   }
+  const int twice = listed_twice(k_caches, v_caches, kv8 ? kv_scales : nullptr, num_layers);
+  if (twice != PA_OK) return twice;
   int* st = device_status_ptr();
   if (!st) return PA_ERR_CUDA;
   CompactParams p{};

@@ -154,3 +154,18 @@ def test_tree_pool_sizes(lib):
         assert _tree(lib, "pa_decode_tree_fp8", nb=nb, hkv=hkv) == -10
         assert _tree(lib, nb=nb, hkv=hkv, dt=pa.PA_F32) == NO_WORKSPACE
     assert _tree(lib, nb=2 ** 26 - 1, hkv=2) == NO_WORKSPACE
+
+
+def test_compact_refuses_pools_listed_twice(lib):
+    """Two layers that share a pool, or a layer's K and V, would be moved twice."""
+    two, many = ctypes.c_void_p * 2, ctypes.c_void_p * 200
+    for name in ("pa_compact_tree", "pa_compact_tree_fp8", "pa_compact_tree_e5m2"):
+        go = lambda **o: _compact(lib, name, **o)  # noqa: E731
+        assert go(k=two(0x1000, 0x1000)) == -1
+        assert go(v=two(0x3000, 0x3000)) == -1
+        assert go(v=two(0x3000, 0x1000)) == -1
+        far = [0x100000 + 0x100 * i for i in range(400)]
+        far[399] = far[0]  # a V pool of another launch's layer
+        assert go(layers=200, k=many(*far[:200]), v=many(*far[200:]),
+                  sc=many(*[0x900000 + 0x10 * i for i in range(200)])) == -1
+    assert _compact(lib, "pa_compact_tree_fp8", sc=two(0x5000, 0x5000)) == -1
