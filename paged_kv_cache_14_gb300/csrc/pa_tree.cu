@@ -440,8 +440,8 @@ TreeLayout tree_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_hea
     w.tile_keys = kTreeTcKeys;
     w.piece_cost = 3;
     per_sm = 2;
-    // Teams of two where trees may fill several query tiles. An odd number of
-    // KV heads would leave a member idle at every odd last tile.
+    // Teams of two where trees may fill several query tiles, of an even number of
+    // KV heads (an odd one would leave a member idle at every odd last tile).
     if ((int64_t)max_q_len * group > w.tile_rows && num_kv_heads % 2 == 0) w.team = 2;
   }
   // Most key tiles there can be: one more query tile than its rows fill for every sequence.

@@ -19,9 +19,10 @@
 // CTAs' keys do not stay in L2: 2.4 TB read per TB of keys), so CTAs then work
 // in teams of two on the line: a place on it is two query tiles of one KV head,
 // member r taking the tile 2 i + r, and an odd last tile's place is two KV
-// heads. The members run side by side, and the second read of a key tile finds
-// it in L2 (1.38 TB read; 48 sequences of 8192 with trees of 40: 403 us
-// without teams, 316 with them).
+// heads (so there are teams only where the number of KV heads is even). The
+// members run side by side, and the second read of a key tile finds it in L2
+// (1.38 TB read; 48 sequences of 8192 with trees of 40: 403 us without teams,
+// 316 with them).
 #pragma once
 
 #include "pa_common.cuh"
@@ -112,8 +113,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, const TreeLens&
   s.nodes = (int)n;
   s.ktiles = (int)(((uint32_t)kv + p.tile_keys - 1) / (uint32_t)p.tile_keys);
   s.qtiles = (s.nodes * p.group + p.tile_rows - 1) / p.tile_rows;
-  s.places = p.team == 1 ? s.qtiles * p.num_kv_heads
-                         : (s.qtiles >> 1) * p.num_kv_heads + (s.qtiles & 1) * ((p.num_kv_heads + 1) >> 1);
+  s.places = (s.qtiles * p.num_kv_heads) >> (p.team - 1);
   return s;
 }
 
@@ -223,38 +223,36 @@ struct TreeWalk {
   }
   __device__ __forceinline__ void look(const TreeParams& p) { ahead = tree_lens(p, min(seq + 1, p.num_seqs - 1)); }
   __device__ __forceinline__ bool next(const TreeParams& p, TreePiece& c) {
-    while (left > 0) {
-      while (place >= s.places) {  // also steps over sequences without work
-        ++seq;
-        place = 0;
-        s = tree_seq(p, ahead);
-        look(p);
-      }
-      c.s = s;
-      c.seq = seq;
-      c.t0 = t;
-      c.t1 = (int)min((int64_t)s.ktiles, t + left);
-      if (p.team == 1) {
-        c.kvh = place / s.qtiles;
-        c.qt = place - c.kvh * s.qtiles;
-      } else {
-        const int r = blockIdx.x & 1, pairs = s.qtiles >> 1;
-        if (place < pairs * p.num_kv_heads) {
-          c.kvh = place / pairs;
-          c.qt = 2 * (place - c.kvh * pairs) + r;
-        } else {
-          c.kvh = 2 * (place - pairs * p.num_kv_heads) + r;
-          c.qt = s.qtiles - 1;
-        }
-      }
-      c.at = at;
-      at += c.t1 - c.t0;
-      left -= c.t1 - c.t0;
-      ++place;  // (a piece that ends before its unit does is the last one)
-      t = 0;
-      if (c.kvh < p.num_kv_heads) return true;  // (else an odd last head: nothing for this member)
+    if (left <= 0) return false;
+    while (place >= s.places) {  // also steps over sequences without work
+      ++seq;
+      place = 0;
+      s = tree_seq(p, ahead);
+      look(p);
     }
-    return false;
+    c.s = s;
+    c.seq = seq;
+    c.t0 = t;
+    c.t1 = (int)min((int64_t)s.ktiles, t + left);
+    if (p.team == 1) {
+      c.kvh = place / s.qtiles;
+      c.qt = place - c.kvh * s.qtiles;
+    } else {
+      const int r = blockIdx.x & 1, pairs = s.qtiles >> 1;
+      if (place < pairs * p.num_kv_heads) {
+        c.kvh = place / pairs;
+        c.qt = 2 * (place - c.kvh * pairs) + r;
+      } else {
+        c.kvh = 2 * (place - pairs * p.num_kv_heads) + r;
+        c.qt = s.qtiles - 1;
+      }
+    }
+    c.at = at;
+    at += c.t1 - c.t0;
+    left -= c.t1 - c.t0;
+    ++place;  // (a piece that ends before its unit does is the last one)
+    t = 0;
+    return true;
   }
 };
 
