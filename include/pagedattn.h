@@ -587,7 +587,8 @@ int pa_chunked_prefill_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_
  * sequence i sits in the cache at position ctx_lens[i] + j and attends to
  * keys 0 .. ctx_lens[i]-1, to itself and to its ancestors, and to nothing
  * else: whatever the K/V rows of other branches or of the positions behind
- * the tree hold (infinities and NaN included) does not reach it.
+ * the tree hold (infinities and NaN included) does not reach it. (In an 8-bit
+ * pool a block's scale is part of the value of each of its rows.)
  *   q          : [total_q][num_q_heads][head_dim]
  *   ctx_lens   : int32 [num_seqs]; committed tokens before the tree (>= 0)
  *   max_q_len, max_kv_len : host upper bounds of the nodes and of ctx + nodes
@@ -598,16 +599,20 @@ int pa_chunked_prefill_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_
  *   out        : [total_q][num_q_heads][head_dim]; must not overlap q
  *   workspace  : pa_decode_tree_workspace_size() bytes, 16-byte aligned, no
  *                initialisation needed; not shared by calls that overlap. Its
- *                size depends on the device's SM count, not on the lengths.
+ *                size follows the bounds given (num_seqs, total_q, max_q_len,
+ *                max_kv_len), not the lengths, up to what the device's SM
+ *                count sets: one made for larger bounds serves smaller ones.
  * A parent that is not below its node records PA_ERR_ARG (the node then
  * counts as a root); a block outside the pool records PA_ERR_BLOCK_OOB, and
  * the rows that see it are unspecified. num_seqs is at most 65535. fp16/bf16:
  * head_dim 64 or 128, a GQA group of at most 128, pools of fewer than 2^31 rows
  * (num_blocks * num_kv_heads * block_size) and scale > 0 (PA_ERR_UNSUPPORTED,
- * PA_ERR_ARG otherwise); the softmax weights are rounded to the 16-bit type for
- * the second product, as in pa_decode. fp32: head_dim a multiple of 32 up to
- * 256, exact fp32 arithmetic, any finite scale. Rows are computed from their own sequence
- * alone; results do not depend on the order in which the device runs.
+ * PA_ERR_ARG otherwise); the softmax weights are rounded to the 16-bit type
+ * (over 8-bit pools to fp16) for the second product, as in pa_decode: a weight
+ * is off by half a step of that type, in fp16 by 2^-25 at most below 2^-14.
+ * fp32: head_dim a multiple of 32 up to 256, exact fp32 arithmetic, any finite
+ * scale. Rows are computed from their own sequence alone; results do not
+ * depend on the order in which the device runs.
  */
 size_t pa_decode_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                      int32_t block_size, int32_t total_q, int32_t max_q_len, int32_t max_kv_len,
@@ -645,7 +650,9 @@ int pa_decode_tree_e5m2(const void* q, int32_t total_q, const int32_t* cu_q_lens
  *   draft_probs  : the same for the draft (draft_stride): row r is the
  *                  distribution that the children of node r were drawn from,
  *                  independently; or NULL: the children were chosen, not
- *                  drawn (a lookup, the likeliest few)
+ *                  drawn (a lookup, the likeliest few). Children drawn without
+ *                  replacement are neither: the kept tokens would not be
+ *                  distributed as the target's.
  *   draft_tokens : int32 [total_q]; the token of each node (a root's is not
  *                  read). A node whose token lies outside [0, vocab_size) is
  *                  padding: never kept.
@@ -697,7 +704,7 @@ int pa_verify_tree(const void* target_probs, int64_t target_stride, const void* 
  *                  max_path_len at most 1024.
  * Bit-exact; every other row stays as it is. The blocks written must be the
  * sequence's own (copy shared ones first). head_dim * sizeof(dtype) must be a
- * multiple of 16. A sequence with a negative context, a length outside
+ * multiple of 16, num_kv_heads * head_dim at most 2^20 (PA_ERR_UNSUPPORTED). A sequence with a negative context, a length outside
  * [0, max_path_len] or a position past its block table records
  * PA_ERR_SEQLEN, a path that does not rise PA_ERR_ARG, a block outside the
  * pool PA_ERR_BLOCK_OOB; nothing of it is moved.

@@ -24,9 +24,10 @@ namespace pa {
 // (a 16-byte shared-memory load takes four of the SM's cycles, so a thread has
 // to use each for several rows). K and V arrive with cp.async in one buffer
 // each: the next K flies while the values are added up, the next V while the
-// scores are. Small calls are bound by the latency of a CTA's few tiles (3
-// sequences of 1500, trees of 11, group 3, head_dim 96: 26 us for 7 tiles a CTA
-// and 7 us of join; one row a thread took 47).
+// scores are. Small calls are latency: 3 sequences of up to 1500, trees of 11,
+// group 3, head_dim 96 give 351 CTAs about two key tiles each (the longest
+// tree's 33 rows take two query tiles a KV head), 27 us from the scan of the
+// lengths to the last store, and 6 us of join; one row a thread took 47.
 // ---------------------------------------------------------------------------
 namespace ts {
 constexpr int kRows = 32;
@@ -266,9 +267,9 @@ __global__ void __launch_bounds__(ts::kThreads, ts::per_sm(D)) tree_simt_kernel(
 // blocks. With few pieces (where many units are split, as in any large batch)
 // a warp takes four rows and four pieces of each at once; with more (few
 // units, a long context), one row and 16 pieces at once. Pieces are added up
-// in their order either way. After the attention's end it takes 8 us for 64
-// sequences of 4096 (15 MB of partials), 14 us for 40 MB of them, 11 us for 4
-// of 131072 and 4 us for one short one.
+// in their order either way. After the attention's end it takes 6 us for 64
+// sequences of 4096 (15 MB of partials), 7 to 11 us for 30 MB of them, 6 us for
+// 4 of 131072 and 3 us for one short one.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 4;
 constexpr int kJoinFew = 4;  // pieces of a unit that four rows' loads cover

@@ -8,17 +8,21 @@
 // re-reads Q from shared memory: 8 steps of 48 cycles; O += P V 4 of 64),
 // whether the rows are all in use or not. Two CTAs share an SM: one's prologue,
 // epilogue and piece switches run under the other's stream. Measured:
-//   4 sequences of 131072, trees of 12, group 8: 246 us, HBM (6.7 TB/s);
+//   4 sequences of 131072, trees of 12, group 8: 248 us, HBM (6.7 TB/s);
 //   64 of 4096, trees of 16, group 4: 118 us, HBM at 78% of its cycles;
 //   48 of 8192, trees of 40, group 8 (two or three query tiles a KV head):
-//     301 us; the tensor unit is busy 73% of the cycles (50% in its pipe, the
+//     303 us; the tensor unit is busy 73% of the cycles (50% in its pipe, the
 //     rest on its operands' way), HBM 61%;
-//   64 of 4096 over an e4m3 cache, trees of 16, group 8: 145 us, HBM at 34%:
-//     a tile's 2850 cycles are the latency of one softmax thread's row of 64
-//     scores and of the hand-overs around it. Two threads a row (234 us), one
-//     pass over the row with registers moved between warpgroups (168) and
-//     converters that fetch the codes themselves (164) were slower, as more
-//     warps wait on more barriers.
+//   64 of 4096 over an e4m3 cache, trees of 16, group 8: 143 us, HBM at 34%,
+//     70 key tiles a CTA. In long pieces (4 sequences of 131072: 166 tiles a
+//     CTA in 247 us, no less than over a 16-bit cache) a tile takes 1.5 us, 2850
+//     cycles: the latency of one softmax thread's row of 64 scores, read
+//     twice, and of the hand-overs around it. That is some 104 of the 143 us;
+//     the rest is start-up and a CTA's 2.7 pieces, each of which waits for Q and
+//     for its conversion. Two threads a row (234 us), one pass over the row
+//     with registers moved between warpgroups (168) and converters that fetch
+//     the codes themselves (164) were slower, as more warps wait on more
+//     barriers.
 //
 //   warps 0, 6  producers: Q tile of each piece and K tiles, V tiles, through
 //               the block table into rings of NK and NV stages;
@@ -35,14 +39,15 @@
 // All roles walk the CTA's pieces; stages, S tiles and their barriers are
 // counted over all tiles of the CTA, so the rings run on across pieces.
 //
-// Scores, maxima, sums and O are held in 32 bits. Two things are rounded to 16:
-// a softmax weight, as the second product's operand (its sum takes it as it
-// was, so a row's error is half a step of its largest weights, the size of the
-// output's own rounding); and over an 8-bit cache a bf16 row of q, into fp16 by
-// a power of two (exact for all that lies within 2^24 of the row's largest),
-// since codes are exact in fp16 only. The V scale of a block is taken into the
-// weight before that rounding, by a power of two that keeps it below 2^15: a
-// row's own, from the blocks that it sees a key of.
+// Scores, maxima, sums and O are held in 32 bits. Two things are rounded to 16.
+// A softmax weight is, as the second product's operand, while the row's sum takes
+// it as it was: it is off by at most half a step, the size of the output's own
+// rounding, and in fp16 below 2^-14 by at most 2^-25, which over n such keys can
+// add up to n 2^-25 of their values. And over an 8-bit cache a bf16 row of q is,
+// into fp16 by a power of two (exact for all that lies within 2^24 of the row's
+// largest), since codes are exact in fp16 only. The V scale of a block is taken
+// into the weight before that rounding, by a power of two that keeps it below
+// 2^15: a row's own, from the blocks that it sees a key of.
 //
 // A row must not see other branches' values, whatever they hold, but P V
 // multiplies every row's weights (0 for those) with every key's values. So

@@ -25,13 +25,14 @@
 // A warp sums two chunks of 512 entries at a time (16 bytes a load, the chunks'
 // loads all in flight) and every chunk's sum is kept, so the entry where the
 // running sum passes the threshold takes a second look at one chunk only. 96
-// trees over 131072 fp32 tokens take 49 us (100 MB of rows are 15 us of HBM):
-// a sequence makes one to four passes one after another, some 9 us each at two
-// CTAs an SM, half of that the arithmetic of its 13 instructions an entry, and
-// its start, its exchanges and the draw take 8 us more. One chunk at a time
-// took 61 us, a split of p and C q each 54, doubles and one CTA a sequence
-// 1018. With few sequences it is the latency of the dependent loads and cluster
-// barriers (4 chains over 32000 tokens: 10 us).
+// trees over 131072 fp32 tokens take 48 us (100 MB of rows are 15 us of HBM):
+// a sequence makes one to four passes one after another, some 9 us each, and
+// its start, its exchanges and the draw take 8 us more. A pass is bound by the
+// latency of its loads: what is in flight waits in registers, which at two CTAs
+// an SM is too little to fill HBM (busy 21%) or to issue without a pause (34%
+// of the cycles). One chunk at a time took 61 us, a split of p and C q each 54,
+// doubles and one CTA a sequence 1018. With few sequences it is the latency of
+// the dependent loads and cluster barriers (4 chains over 32000 tokens: 9 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
