@@ -29,7 +29,7 @@
 // a sequence makes one to four passes one after another, some 9 us each, and
 // its start, its exchanges and the draw take 8 us more. A pass is bound by the
 // latency of its loads: what is in flight waits in registers, which at two CTAs
-// an SM is too little to fill HBM (busy 21%) or to issue without a pause (34%
+// an SM is too little to fill HBM (busy 22%) or to issue without a pause (34%
 // of the cycles). One chunk at a time took 61 us, a split of p and C q each 54,
 // doubles and one CTA a sequence 1018. With few sequences it is the latency of
 // the dependent loads and cluster barriers (4 chains over 32000 tokens: 9 us).
