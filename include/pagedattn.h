@@ -740,6 +740,202 @@ int pa_compact_tree_e5m2(void* const* k_caches, void* const* v_caches, float* co
                          void* stream);
 
 /*
+ * Long contexts: a decode step that reads part of the cache. A step rotates
+ * its new tokens' queries and keys by their positions and caches them
+ * (pa_rope_and_cache), keeps an 8-bit summary of the keys of every block
+ * (pa_block_summaries), chooses for every sequence and KV head the blocks
+ * whose summaries promise the largest scores (pa_select_blocks), and attends
+ * to these (pa_decode_sparse). The block tables are those of section 1.2 of
+ * the "High-Throughput Local LLM Infrastructure" page; the chosen blocks are a
+ * subset of each table's entries.
+ */
+
+/* How pa_rope_table scales the frequencies f_i = base^(-2 i / rot_dim) of the
+ * pairs i = 0 .. rot_dim/2 - 1. */
+#define PA_ROPE_NONE 0
+#define PA_ROPE_LINEAR 1 /* f_i / factor */
+#define PA_ROPE_BASE 2   /* base * factor^(rot_dim / (rot_dim - 2)) in base's place */
+#define PA_ROPE_BANDS 3  /* by turns: with t = original_len f_i / (2 pi) and
+                          * w = (t - low) / (high - low) held to [0, 1],
+                          * w f_i + (1 - w) f_i / factor */
+#define PA_ROPE_RAMP 4   /* by pair: with d(t) = rot_dim ln(original_len / (2 pi t)) / (2 ln base),
+                          * a = max(floor(d(high)), 0), z = min(ceil(d(low)), rot_dim - 1) and
+                          * w = (i - a) / max(z - a, 0.001) held to [0, 1],
+                          * (1 - w) f_i + w f_i / factor */
+
+/*
+ * pa_rope_table - cosines and sines of positions first_position ..
+ * first_position + num_positions - 1:
+ *   cos_sin : float [num_positions][rot_dim] (output), 16-byte aligned; row
+ *             p holds amplitude cos(a_i) at [i] and amplitude sin(a_i) at
+ *             [rot_dim/2 + i], a_i = (first_position + p) f_i
+ * Angles are reduced in 64-bit fixed point from frequencies held in 64 bits:
+ * an entry of amplitude 1 is within 2^-22 of the cosine or sine. Positions lie below 2^31; rot_dim is
+ * even, 2 to 256 (PA_ERR_UNSUPPORTED); base > 1, factor > 0 (not read by
+ * PA_ROPE_NONE), 0 < low < high and original_len >= 1 (read by PA_ROPE_BANDS
+ * and PA_ROPE_RAMP only), amplitude finite (PA_ERR_ARG).
+ */
+int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions, int32_t rot_dim, double base,
+                  int32_t scaling, double factor, int32_t original_len, double low, double high, double amplitude,
+                  void* stream);
+
+/*
+ * pa_rope_and_cache - new tokens' queries and keys rotated by their
+ * positions, keys and values written into their cache slots.
+ *   q, k, v    : [num_tokens][heads][head_dim] of dtype, tokens q_stride,
+ *                k_stride, v_stride elements apart (parts of one wider row
+ *                may be given in place); 16-byte aligned, strides multiples of
+ *                16 bytes (PA_ERR_ALIGN)
+ *   positions  : int32 [num_tokens]
+ *   slot_mapping : int64 [num_tokens], as pa_reshape_and_cache
+ *   cos_sin    : float [num_positions][rot_dim], row p for position p, as
+ *                pa_rope_table writes it
+ *   interleaved: 0: pair i is elements i and rot_dim/2 + i of a head;
+ *                otherwise elements 2 i and 2 i + 1
+ *   q_out      : [num_tokens][num_q_heads][head_dim]; q itself (if q_stride is
+ *                num_q_heads * head_dim), or apart from every input
+ * With c, s the pair's entries, (x, y) becomes (x c - y s, y c + x s), every
+ * product, sum and difference rounded to fp32, the result then to dtype;
+ * elements from rot_dim on stay. A token with slot < 0 is padding: nothing of
+ * it is written. A slot outside the pool records PA_ERR_BLOCK_OOB, a position
+ * outside [0, num_positions) PA_ERR_SEQLEN; such a token is skipped too.
+ * num_q_heads 0 caches alone (q and q_out may be NULL). rot_dim is even, 2 to
+ * min(head_dim, 256); head_dim * sizeof(dtype) a multiple of 16, head_dim at
+ * most 1024; num_tokens * num_kv_heads at most 2^30, and a grid of
+ * ceil(units / 128) CTAs a token below 2^31 (PA_ERR_UNSUPPORTED). Two tokens
+ * with the same slot race.
+ */
+int pa_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, const float* cos_sin,
+                      int32_t num_positions, int32_t rot_dim, int32_t interleaved, int64_t num_tokens, void* q_out,
+                      void* k_cache, void* v_cache, int32_t num_blocks, int32_t block_size, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, pa_dtype dtype, void* stream);
+
+/* pa_rope_and_cache_fp8, pa_rope_and_cache_e5m2 - the same into 8-bit pools:
+ * pa_reshape_and_cache_fp8's scale rule and its order of tokens (those of one
+ * block in one run), the rotated keys encoded from fp32 (they are not rounded
+ * to dtype first). head_dim 64 or 128. */
+int pa_rope_and_cache_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                          const float* cos_sin, int32_t num_positions, int32_t rot_dim, int32_t interleaved,
+                          int64_t num_tokens, void* q_out, void* k_cache, void* v_cache, float* kv_scales,
+                          int32_t num_blocks, int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                          int32_t head_dim, pa_dtype dtype, void* stream);
+int pa_rope_and_cache_e5m2(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                           const float* cos_sin, int32_t num_positions, int32_t rot_dim, int32_t interleaved,
+                           int64_t num_tokens, void* q_out, void* k_cache, void* v_cache, float* kv_scales,
+                           int32_t num_blocks, int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_dim, pa_dtype dtype, void* stream);
+
+/*
+ * pa_block_summaries - the range of every key dimension over the tokens of a
+ * block, for the blocks that hold tokens first_tokens[i] .. seq_lens[i] - 1 of
+ * sequence i.
+ *   first_tokens, seq_lens : int32 [num_seqs]; the summary of a block covers
+ *                all its tokens below seq_lens[i], those before
+ *                first_tokens[i] too; nothing is done where they are equal
+ *   max_new_tokens : host upper bound of seq_lens[i] - first_tokens[i]
+ *   summaries  : int8 [num_blocks][num_kv_heads][2][head_dim] (updated)
+ *   summary_scales : float [num_blocks][num_kv_heads] (updated)
+ * With the block's keys of one KV head: scale = max |k| / 127,
+ * summaries[..][0][d] = min(ceil(max_t k[t][d] / scale), 127),
+ * summaries[..][1][d] = max(floor(min_t k[t][d] / scale), -127), in fp32; codes
+ * 0 where scale is 0, scale +infinity and codes 0 where a key is not finite.
+ * (Over 8-bit pools a key is its code times the block's scale, in fp32.)
+ * Every other entry stays as it is. Sequences that share a block give it the
+ * same number of tokens. first_tokens below 0 or above seq_lens, more new
+ * tokens than max_new_tokens, or a table too short record PA_ERR_SEQLEN, a
+ * block outside the pool PA_ERR_BLOCK_OOB; what they name is left. fp16/bf16
+ * head_dim 64 or 128, 8-bit pools 64 or 128, fp32 a multiple of 32 up to 256.
+ */
+int pa_block_summaries(const void* k_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                       const int32_t* first_tokens, const int32_t* seq_lens, int32_t num_seqs,
+                       int32_t max_new_tokens, int32_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                       int32_t head_dim, int8_t* summaries, float* summary_scales, pa_dtype dtype, void* stream);
+int pa_block_summaries_fp8(const void* k_cache, const float* kv_scales, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* first_tokens, const int32_t* seq_lens,
+                           int32_t num_seqs, int32_t max_new_tokens, int32_t num_blocks, int32_t block_size,
+                           int32_t num_kv_heads, int32_t head_dim, int8_t* summaries, float* summary_scales,
+                           void* stream);
+int pa_block_summaries_e5m2(const void* k_cache, const float* kv_scales, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* first_tokens, const int32_t* seq_lens,
+                            int32_t num_seqs, int32_t max_new_tokens, int32_t num_blocks, int32_t block_size,
+                            int32_t num_kv_heads, int32_t head_dim, int8_t* summaries, float* summary_scales,
+                            void* stream);
+
+/*
+ * pa_select_blocks - the blocks of every sequence and KV head that a decode
+ * query attends to: its first num_sink, its last num_recent, and of the others
+ * those of the highest scores, max_list_len in all.
+ *   q          : [num_seqs][num_q_heads][head_dim] of dtype
+ *   summaries, summary_scales : as pa_block_summaries writes them (those of the
+ *                first num_sink and last num_recent blocks are not read)
+ *   seq_lens   : int32 [num_seqs], 0 allowed; max_seq_len a host upper bound
+ *   block_lists : int32 [num_seqs][num_kv_heads][max_list_len] (output): logical
+ *                block numbers, rising, then -1
+ *   list_lens  : int32 [num_seqs][num_kv_heads] (output)
+ * The score of a block: every query head in 8 bits, s_q = max |q| / 127 and
+ * codes = q / s_q rounded to nearest even (zeros for a head that is not all
+ * finite); with I = sum_d max(code_d hi_d, code_d lo_d), a whole number, the
+ * score is fl32(scale * max over the group's heads of fl32(s_q I)); 0 for a
+ * block of scale 0; a block with an infinite scale comes first. Equal scores go to the lower block, so
+ * results do not depend on the order in which the device runs. For attention
+ * with a negative scale pass -q. A sequence of at most max_list_len blocks
+ * lists them all. A sequence longer than max_seq_len or its table (or of
+ * negative length) records PA_ERR_SEQLEN and lists nothing; a block outside the
+ * pool records PA_ERR_BLOCK_OOB and comes last. head_dim a multiple of 32 up
+ * to 256, a GQA group of at most 128, num_seqs at most 65535, num_sink +
+ * num_recent at most max_list_len (PA_ERR_ARG). A sequence may have some 400000
+ * blocks (8 CTAs' shared memory holds their scores; the bound is the smaller of
+ * max_seq_len and the table; PA_ERR_UNSUPPORTED).
+ */
+int pa_select_blocks(const void* q, const int8_t* summaries, const float* summary_scales, const int32_t* block_tables,
+                     int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs, int32_t max_seq_len,
+                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                     int32_t num_blocks, int32_t max_list_len, int32_t num_sink, int32_t num_recent,
+                     int32_t* block_lists, int32_t* list_lens, pa_dtype dtype, void* stream);
+
+/*
+ * pa_decode_sparse - pa_decode over listed blocks: query head h of sequence i
+ * attends to the tokens below seq_lens[i] of the logical blocks
+ * block_lists[i][kv head][0 .. list_lens[i][kv head] - 1].
+ *   block_lists, list_lens : as pa_select_blocks writes them; any strictly
+ *                rising list of a sequence's blocks will do
+ *   out        : [num_seqs][num_q_heads][head_dim], apart from q; rows of an
+ *                empty list are zeros
+ * No workspace. An entry that is not above the one before it records
+ * PA_ERR_ARG, one past the sequence's end PA_ERR_SEQLEN, a block outside the
+ * pool PA_ERR_BLOCK_OOB; a list_lens outside [0, max_list_len] or a sequence
+ * longer than its table PA_ERR_SEQLEN: the rows concerned are unspecified.
+ * num_seqs at most 65535, max_list_len at most 2^26, a GQA group of at most
+ * 128, any finite scale. fp16/bf16: head_dim 64 or 128; the softmax weights
+ * are rounded to the 16-bit type (over 8-bit pools to fp16) for the second
+ * product, as in pa_decode. fp32: head_dim a multiple of 32 up to 256, exact
+ * fp32 arithmetic. Results do not depend on the order in which the device runs.
+ */
+int pa_decode_sparse(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                     int32_t max_blocks_per_seq, const int32_t* seq_lens, const int32_t* block_lists,
+                     const int32_t* list_lens, int32_t max_list_len, int32_t num_seqs, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                     void* out, pa_dtype dtype, void* stream);
+
+/* pa_decode_sparse_fp8, pa_decode_sparse_e5m2 - the same over 8-bit pools
+ * (kv_scales as for pa_decode_fp8). q/out fp16 or bf16, head_dim 128. */
+int pa_decode_sparse_fp8(const void* q, const void* k_cache, const void* v_cache, const float* kv_scales,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         const int32_t* block_lists, const int32_t* list_lens, int32_t max_list_len,
+                         int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int32_t num_blocks, float scale, void* out, pa_dtype dtype,
+                         void* stream);
+int pa_decode_sparse_e5m2(const void* q, const void* k_cache, const void* v_cache, const float* kv_scales,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                          const int32_t* block_lists, const int32_t* list_lens, int32_t max_list_len,
+                          int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t block_size, int32_t num_blocks, float scale, void* out, pa_dtype dtype,
+                          void* stream);
+
+/*
  * pa_selftest_bounded_wait — exercises the failure path every kernel relies
  * on: one warp waits on an mbarrier that nothing completes; the wait gives up
  * after limit_ns nanoseconds of device time (1 us .. 1 s, else PA_ERR_ARG),

@@ -34,6 +34,9 @@ EXPORTS = (
     "pa_chunked_prefill_fp8", "pa_reshape_and_cache_e5m2", "pa_decode_e5m2", "pa_decode_shared_prefix_e5m2",
     "pa_chunked_prefill_e5m2", "pa_decode_tree_workspace_size", "pa_decode_tree", "pa_decode_tree_fp8",
     "pa_decode_tree_e5m2", "pa_verify_tree", "pa_compact_tree", "pa_compact_tree_fp8", "pa_compact_tree_e5m2",
+    "pa_rope_table", "pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_rope_and_cache_e5m2", "pa_block_summaries",
+    "pa_block_summaries_fp8", "pa_block_summaries_e5m2", "pa_select_blocks", "pa_decode_sparse",
+    "pa_decode_sparse_fp8", "pa_decode_sparse_e5m2",
 )
 
 _i32, _i64, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
@@ -111,8 +114,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "pa_compact_tree_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32,
                                                _i32, _i32, _i32, _vp]),
     })
+    f64, i = ctypes.c_double, ctypes.c_int
+    rope = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp]
+    sparse = [_vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, i, _vp]
+    summary = [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp]
+    sig.update({
+        "pa_rope_table": (i, [_vp, _i64, _i64, _i32, f64, _i32, f64, _i32, f64, f64, f64, _vp]),
+        "pa_rope_and_cache": (i, [*rope, _i32, _i32, _i32, _i32, _i32, i, _vp]),
+        "pa_rope_and_cache_fp8": (i, [*rope, _vp, _i32, _i32, _i32, _i32, _i32, i, _vp]),
+        "pa_block_summaries": (i, [_vp, *summary, i, _vp]),
+        "pa_block_summaries_fp8": (i, [_vp, _vp, *summary, _vp]),
+        "pa_select_blocks": (i, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                 _i32, _vp, _vp, i, _vp]),
+        "pa_decode_sparse": (i, [_vp, _vp, _vp, *sparse]),
+        "pa_decode_sparse_fp8": (i, [_vp, _vp, _vp, _vp, *sparse]),
+    })
     for name in ("reshape_and_cache", "decode", "decode_shared_prefix", "chunked_prefill", "decode_tree",
-                 "compact_tree"):
+                 "compact_tree", "rope_and_cache", "block_summaries", "decode_sparse"):
         sig[f"pa_{name}_e5m2"] = sig[f"pa_{name}_fp8"]  # same arguments, e5m2 codes
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -619,6 +637,10 @@ def _place(t, name: str, stream) -> tuple[int, int, object]:
     the current one."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    return _here(stream)
+
+
+def _here(stream) -> tuple[int, int, object]:
     dev = torch.cuda.current_device()
     here = torch._C._cuda_getCurrentRawStream(dev)
     if stream is None:
@@ -630,17 +652,19 @@ def _place(t, name: str, stream) -> tuple[int, int, object]:
     return dev, handle, torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream(dev)
 
 
-def _scratch(like: torch.Tensor, shape, dtype, side) -> torch.Tensor:
-    """A new tensor for a call on the current stream or on another one (side).
+def _scratch(like, shape, dtype, side) -> torch.Tensor:
+    """A new tensor (on the device of the tensor `like`, or on device `like`) for
+    a call on the current stream or on another one (side).
     Memory comes from the stream that writes it first, so that whatever used
     it before is over by then; the caller may go on to read it on the current
     one, which is why that one is recorded. (Tensor.new_empty between kernel
     launches takes twice torch.empty's time.)"""
+    device = like.device if isinstance(like, torch.Tensor) else like
     if side is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
     here = torch.cuda.current_stream()
     with torch.cuda.stream(side):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(here)
     return t
 
@@ -827,3 +851,257 @@ def _compact_tree(sym, k_caches, v_caches, kv_scales, block_tables, ctx_lens, pa
         _arg(path_lens, "path_lens", i32, dev, (n,)), n, width, P, B, hkv, D, *code, handle)
     if rc:
         raise PagedAttnError(rc, sym)
+
+
+# ---------------------------------------------------------------------------
+# Long contexts: rotary positions with the cache write, block summaries, the
+# choice of blocks, attention over them.
+# ---------------------------------------------------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def pa_rope_table(num_positions: int, rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                  factor: float = 1.0, original_len: int = 0, low: float = 1.0, high: float | None = None,
+                  amplitude: float = 1.0, first_position: int = 0, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Cosines and sines of positions: float32 [num_positions, rot_dim] on the
+    current device. scaling: "none", "linear", "base", "bands" (high defaults
+    to 4 turns) or "ramp" (to 32)."""
+    kind = ROPE_SCALINGS.get(scaling)
+    if kind is None:
+        raise ValueError(f"scaling {scaling!r}: one of {', '.join(ROPE_SCALINGS)}")
+    if high is None:
+        high = 32.0 if scaling == "ramp" else 4.0
+    dev, handle, side = _here(stream)
+    if out is None:
+        if num_positions < 0 or rot_dim < 0:
+            raise PagedAttnError(-1, "pa_rope_table")
+        out = _scratch(dev, (num_positions, rot_dim), torch.float32, side)
+    rc = load().pa_rope_table(_arg(out, "out", torch.float32, dev, (num_positions, rot_dim)), first_position,
+                              num_positions, rot_dim, base, kind, factor, original_len, low, high, amplitude, handle)
+    if rc:
+        raise PagedAttnError(rc, "pa_rope_table")
+    return out
+
+
+def pa_rope_and_cache(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                      slot_mapping: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor | None:
+    """Rotate new tokens' q and k by their positions and cache k and v: q_out.
+    q, k, v: [T, heads, D], rows of tokens may be apart (parts of one product).
+    q None: cache alone."""
+    return _rope_and_cache("pa_rope_and_cache", q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, None,
+                           interleaved, q_out, stream)
+
+
+def pa_rope_and_cache_fp8(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                          slot_mapping: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                          v_cache: torch.Tensor, kv_scales: torch.Tensor, interleaved: bool = False,
+                          q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """pa_rope_and_cache into e4m3 pools."""
+    return _rope_and_cache("pa_rope_and_cache_fp8", q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache,
+                           kv_scales, interleaved, q_out, stream)
+
+
+def pa_rope_and_cache_e5m2(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                           slot_mapping: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, kv_scales: torch.Tensor, interleaved: bool = False,
+                           q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """pa_rope_and_cache into e5m2 pools."""
+    return _rope_and_cache("pa_rope_and_cache_e5m2", q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache,
+                           kv_scales, interleaved, q_out, stream)
+
+
+def _heads(t, name: str, dtype, dev: int, shape) -> tuple[int, int]:
+    """Pointer and token stride (elements) of a tensor [tokens, heads, D] whose
+    tokens' rows are contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _refuse(t, name, dtype, dev, shape)
+    T, H, D = shape
+    step, per, one = t.stride()
+    if D > 1 and one != 1 or H > 1 and per != D or T > 1 and step < H * D:
+        raise ValueError(f"{name}'s tokens must be contiguous rows that do not overlap")
+    return t.data_ptr(), step if T > 1 else H * D
+
+
+def _rope_and_cache(sym, q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, kv_scales, interleaved, q_out,
+                    stream):
+    lib = load()
+    dev, handle, side = _place(k, "k", stream)
+    P, hkv, B, D = pool = k_cache.shape
+    dt = k.dtype
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"k must be float32, float16 or bfloat16, got {dt}")
+    T = k.shape[0]
+    shape = (T, hkv, D)
+    kp, ks = _heads(k, "k", dt, dev, shape)
+    vp, vs = _heads(v, "v", dt, dev, shape)
+    hq, qp, qs, op = 0, None, 0, None
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected [tokens, heads, {D}]")
+        hq = q.shape[1]
+        shape = (T, hq, D)
+        qp, qs = _heads(q, "q", dt, dev, shape)
+        if q_out is None:
+            q_out = _scratch(q, shape, dt, side)
+        op = _arg(q_out, "q_out", dt, dev, shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kv = dt if kv_scales is None else torch.uint8
+    pools = (_arg(k_cache, "k_cache", kv, dev, pool), _arg(v_cache, "v_cache", kv, dev, pool))
+    if kv_scales is not None:
+        pools += (_arg(kv_scales, "kv_scales", torch.float32, dev, (P, hkv, 2)),)
+    np_, rot = cos_sin.shape
+    rc = getattr(lib, sym)(
+        qp, qs, kp, ks, vp, vs, _arg(positions, "positions", torch.int32, dev, (T,)),
+        _arg(slot_mapping, "slot_mapping", torch.int64, dev, (T,)),
+        _arg(cos_sin, "cos_sin", torch.float32, dev, (np_, rot)), np_, rot, 1 if interleaved else 0, T, op, *pools, P,
+        B, hq, hkv, D, code, handle)
+    if rc:
+        raise PagedAttnError(rc, sym)
+    return q_out
+
+
+def pa_block_summaries(k_cache: torch.Tensor, block_tables: torch.Tensor, first_tokens: torch.Tensor,
+                       seq_lens: torch.Tensor, max_new_tokens: int, summaries: torch.Tensor,
+                       summary_scales: torch.Tensor, stream=None) -> None:
+    """Summaries of the blocks that hold tokens first_tokens[i] .. seq_lens[i] - 1
+    of each sequence. summaries: int8 [blocks, Hkv, 2, D]; summary_scales:
+    float32 [blocks, Hkv]; both updated."""
+    _block_summaries("pa_block_summaries", k_cache, None, block_tables, first_tokens, seq_lens, max_new_tokens,
+                     summaries, summary_scales, stream)
+
+
+def pa_block_summaries_fp8(k_cache: torch.Tensor, kv_scales: torch.Tensor, block_tables: torch.Tensor,
+                           first_tokens: torch.Tensor, seq_lens: torch.Tensor, max_new_tokens: int,
+                           summaries: torch.Tensor, summary_scales: torch.Tensor, stream=None) -> None:
+    """pa_block_summaries of an e4m3 pool."""
+    _block_summaries("pa_block_summaries_fp8", k_cache, kv_scales, block_tables, first_tokens, seq_lens,
+                     max_new_tokens, summaries, summary_scales, stream)
+
+
+def pa_block_summaries_e5m2(k_cache: torch.Tensor, kv_scales: torch.Tensor, block_tables: torch.Tensor,
+                            first_tokens: torch.Tensor, seq_lens: torch.Tensor, max_new_tokens: int,
+                            summaries: torch.Tensor, summary_scales: torch.Tensor, stream=None) -> None:
+    """pa_block_summaries of an e5m2 pool."""
+    _block_summaries("pa_block_summaries_e5m2", k_cache, kv_scales, block_tables, first_tokens, seq_lens,
+                     max_new_tokens, summaries, summary_scales, stream)
+
+
+def _block_summaries(sym, k_cache, kv_scales, block_tables, first_tokens, seq_lens, max_new_tokens, summaries,
+                     summary_scales, stream) -> None:
+    lib = load()
+    dev, handle, _ = _place(k_cache, "k_cache", stream)
+    P, hkv, B, D = pool = k_cache.shape
+    n, mb = block_tables.shape
+    i32, f32 = torch.int32, torch.float32
+    if kv_scales is None:
+        dt = k_cache.dtype
+        code = (_DT.get(dt),)
+        if code[0] is None:
+            raise TypeError(f"k_cache must be float32, float16 or bfloat16, got {dt}")
+        pools = (_arg(k_cache, "k_cache", dt, dev, pool),)
+    else:
+        code = ()
+        pools = (_arg(k_cache, "k_cache", torch.uint8, dev, pool), _arg(kv_scales, "kv_scales", f32, dev, (P, hkv, 2)))
+    rc = getattr(lib, sym)(
+        *pools, _arg(block_tables, "block_tables", i32, dev, (n, mb)), mb,
+        _arg(first_tokens, "first_tokens", i32, dev, (n,)), _arg(seq_lens, "seq_lens", i32, dev, (n,)), n,
+        max_new_tokens, P, B, hkv, D, _arg(summaries, "summaries", torch.int8, dev, (P, hkv, 2, D)),
+        _arg(summary_scales, "summary_scales", f32, dev, (P, hkv)), *code, handle)
+    if rc:
+        raise PagedAttnError(rc, sym)
+
+
+def pa_select_blocks(q: torch.Tensor, summaries: torch.Tensor, summary_scales: torch.Tensor,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, block_size: int,
+                     max_list_len: int, num_sink: int = 1, num_recent: int = 1,
+                     block_lists: torch.Tensor | None = None, list_lens: torch.Tensor | None = None,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The logical blocks that each (sequence, KV head) attends to:
+    (block_lists int32 [N, Hkv, max_list_len], list_lens int32 [N, Hkv])."""
+    lib = load()
+    dev, handle, side = _place(q, "q", stream)
+    n, hq, D = shape = q.shape
+    P, hkv = summaries.shape[:2]
+    mb = block_tables.shape[1]
+    dt, i32 = q.dtype, torch.int32
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"q must be float32, float16 or bfloat16, got {dt}")
+    if max_list_len < 1:
+        raise PagedAttnError(-1, "pa_select_blocks")
+    if block_lists is None:
+        block_lists = _scratch(q, (n, hkv, max_list_len), i32, side)
+    if list_lens is None:
+        list_lens = _scratch(q, (n, hkv), i32, side)
+    rc = lib.pa_select_blocks(
+        _arg(q, "q", dt, dev, shape), _arg(summaries, "summaries", torch.int8, dev, (P, hkv, 2, D)),
+        _arg(summary_scales, "summary_scales", torch.float32, dev, (P, hkv)),
+        _arg(block_tables, "block_tables", i32, dev, (n, mb)), mb, _arg(seq_lens, "seq_lens", i32, dev, (n,)), n,
+        max_seq_len, hq, hkv, D, block_size, P, max_list_len, num_sink, num_recent,
+        _arg(block_lists, "block_lists", i32, dev, (n, hkv, max_list_len)),
+        _arg(list_lens, "list_lens", i32, dev, (n, hkv)), code, handle)
+    if rc:
+        raise PagedAttnError(rc, "pa_select_blocks")
+    return block_lists, list_lens
+
+
+def pa_decode_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, block_lists: torch.Tensor, list_lens: torch.Tensor, scale: float,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Decode attention over the listed blocks of every (sequence, KV head)."""
+    return _decode_sparse("pa_decode_sparse", q, k_cache, v_cache, None, block_tables, seq_lens, block_lists,
+                          list_lens, scale, out, stream)
+
+
+def pa_decode_sparse_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
+                         block_tables: torch.Tensor, seq_lens: torch.Tensor, block_lists: torch.Tensor,
+                         list_lens: torch.Tensor, scale: float, out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """pa_decode_sparse over e4m3 pools."""
+    return _decode_sparse("pa_decode_sparse_fp8", q, k_cache, v_cache, kv_scales, block_tables, seq_lens,
+                          block_lists, list_lens, scale, out, stream)
+
+
+def pa_decode_sparse_e5m2(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_scales: torch.Tensor,
+                          block_tables: torch.Tensor, seq_lens: torch.Tensor, block_lists: torch.Tensor,
+                          list_lens: torch.Tensor, scale: float, out: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """pa_decode_sparse over e5m2 pools."""
+    return _decode_sparse("pa_decode_sparse_e5m2", q, k_cache, v_cache, kv_scales, block_tables, seq_lens,
+                          block_lists, list_lens, scale, out, stream)
+
+
+def _decode_sparse(sym, q, k_cache, v_cache, kv_scales, block_tables, seq_lens, block_lists, list_lens, scale, out,
+                   stream) -> torch.Tensor:
+    lib = load()
+    dev, handle, side = _place(q, "q", stream)
+    n, hq, D = shape = q.shape
+    P, hkv, B, _ = pool = k_cache.shape
+    mb, width = block_tables.shape[1], block_lists.shape[2]
+    dt, i32 = q.dtype, torch.int32
+    code = _DT.get(dt)
+    if code is None:
+        raise TypeError(f"q must be float32, float16 or bfloat16, got {dt}")
+    if pool[3] != D:
+        raise ValueError(f"k_cache has shape {tuple(pool)}, q's head_dim is {D}")
+    kv = dt if kv_scales is None else torch.uint8
+    qp = _arg(q, "q", dt, dev, shape)
+    if out is None:
+        out = _scratch(q, shape, dt, side)
+    pools = (_arg(k_cache, "k_cache", kv, dev, pool), _arg(v_cache, "v_cache", kv, dev, pool))
+    if kv_scales is not None:
+        pools += (_arg(kv_scales, "kv_scales", torch.float32, dev, (P, hkv, 2)),)
+    rc = getattr(lib, sym)(
+        qp, *pools, _arg(block_tables, "block_tables", i32, dev, (n, mb)), mb,
+        _arg(seq_lens, "seq_lens", i32, dev, (n,)), _arg(block_lists, "block_lists", i32, dev, (n, hkv, width)),
+        _arg(list_lens, "list_lens", i32, dev, (n, hkv)), width, n, hq, hkv, D, B, P, scale,
+        _arg(out, "out", dt, dev, shape), code, handle)
+    if rc:
+        raise PagedAttnError(rc, sym)
+    return out

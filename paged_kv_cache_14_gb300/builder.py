@@ -18,7 +18,7 @@ LIB_NAME = "libpagedattn.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_prefill.cu", "pa_cascade.cu", "pa_noalloc.cu",
            "pa_selftest.cu", "pa_tree.cu", "pa_tree_tc.cu",
-           "pa_verify.cu", "pa_compact.cu"]
+           "pa_verify.cu", "pa_compact.cu", "pa_rope.cu", "pa_select.cu", "pa_sparse.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-Xptxas", "-v"]

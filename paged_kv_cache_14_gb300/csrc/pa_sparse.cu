@@ -1,0 +1,692 @@
+// Decode attention over listed blocks: softmax(q K^T scale) V over the tokens
+// of the blocks that each (sequence, KV head) lists.
+//
+// The bytes of the listed K and V rows bound it: a block's keys meet the
+// query heads of one group only (4 G operations for 2 x 2 bytes). One cluster
+// works on a (sequence, KV head), its warps on 16 tokens at a time. A warp
+// loads them straight into the fragments of its matrix products, 16 bytes a
+// lane, which the products' free order of k (the head's dimensions) and of m
+// (the output's) allows:
+//   scores S[16 tokens][8 heads] = K q^T, lane (r, c) holding 8 dimensions
+//     from 32 j + 8 c on of tokens r and r + 8;
+//   output O^T[D][8 heads] += V^T P^T, lane (r, c) holding 8 dimensions from
+//     8 r on (and 64 + 8 r) of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9, paired
+//     by byte permutes; P goes from one layout to the other by a transpose of
+//     8 x 8 matrices.
+// Each warp keeps a running reference m and a sum l of each head. The
+// reference moves only when a score passes it by 2^8 (weights stay below 2^8,
+// far from the largest fp16), so that most tiles need no maximum over the
+// warp. Warps, then the cluster's CTAs, are joined in a fixed order.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <type_traits>
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+struct SparseParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* kv_scales;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* lists;
+  const int32_t* list_lens;
+  void* out;
+  int32_t max_blocks_per_seq, max_list_len, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int32_t group, row_groups;
+  float scale_log2;
+  int* status;
+};
+
+constexpr int kSparseWarps = 4;
+constexpr int kSparseThreads = kSparseWarps * 32;
+constexpr int kSparseMaxCluster = 8;
+constexpr float kMoveAt = 8.f;  // log2 of the weight that moves the reference
+
+namespace {
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* local, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float remote_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 remote_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// The cluster's row: its sequence, KV head and query heads, and its list.
+struct SparseRow {
+  int ranks, rank, seq, head, first_head, heads, len, entries;
+  const int32_t* list;
+  const int32_t* table;
+};
+__device__ __forceinline__ SparseRow sparse_row(const SparseParams& p, int heads_per_row) {
+  SparseRow w;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(w.ranks));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(w.rank));
+  int row = blockIdx.x / w.ranks;
+  const int rg = row % p.row_groups;
+  row /= p.row_groups;
+  w.seq = row / p.num_kv_heads;
+  w.head = row - w.seq * p.num_kv_heads;
+  w.first_head = w.head * p.group + rg * heads_per_row;
+  w.heads = min(heads_per_row, p.group - rg * heads_per_row);
+  w.len = p.seq_lens[w.seq];
+  w.entries = p.list_lens[row];
+  w.list = p.lists + (int64_t)row * p.max_list_len;
+  w.table = p.block_tables + (int64_t)w.seq * p.max_blocks_per_seq;
+  if (w.entries < 0 || w.entries > p.max_list_len || w.len < 0 ||
+      (w.len > 0 && (w.len - 1) / p.block_size >= p.max_blocks_per_seq)) {
+    if (threadIdx.x == 0) record_error(p.status, PA_ERR_SEQLEN);
+    w.entries = 0;
+  }
+  return w;
+}
+
+// Tokens `16 sub ..` of list entry i: (block, tokens there); no tokens for an
+// entry that is refused.
+__device__ __forceinline__ int2 sparse_item(const SparseParams& p, const SparseRow& w, int i, int sub) {
+  const int lb = w.list[i], before = i > 0 ? w.list[i - 1] : -1;
+  if (lb <= before || lb < 0 || w.len <= 0 || lb > (w.len - 1) / p.block_size) {
+    record_error(p.status, lb <= before || lb < 0 ? PA_ERR_ARG : PA_ERR_SEQLEN);
+    return make_int2(0, 0);
+  }
+  const int blk = w.table[lb];
+  if (blk < 0 || blk >= p.num_blocks) {
+    record_error(p.status, PA_ERR_BLOCK_OOB);
+    return make_int2(0, 0);
+  }
+  return make_int2(blk, min(16, max(0, w.len - lb * p.block_size - 16 * sub)));
+}
+
+// Joins a cluster's CTAs: o [heads][D], m and l in every CTA's shared memory
+// (o relative to m); each CTA writes its share of the output. Ends with a
+// cluster barrier, after which shared memory may go.
+template <typename T, int D>
+__device__ __forceinline__ void sparse_join(const SparseParams& p, const SparseRow& w, const float* o, const float* m,
+                                            const float* l) {
+  cluster_sync();
+  const int quads = w.heads * (D / 4);
+  for (int x = w.rank * kSparseThreads + threadIdx.x; x < quads; x += w.ranks * kSparseThreads) {
+    const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
+    float top = neg_inf(), sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < w.ranks; ++i) top = fmaxf(top, remote_f32(remote(m + h, i)));
+    for (int i = 0; i < w.ranks; ++i) {
+      const float mi = remote_f32(remote(m + h, i));
+      const float f = mi == neg_inf() ? 1.f : exp2f(mi - top);  // (without tokens: zeros, or a NaN to keep)
+      const float4 v = remote_f32x4(remote(o + h * D + d, i));
+      sum += f * remote_f32(remote(l + h, i));
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+    const float inv = w.entries > 0 ? 1.f / sum : 0.f;  // a row without blocks: zeros
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    store4(static_cast<T*>(p.out) + ((int64_t)w.seq * p.num_q_heads + w.first_head + h) * D + d, acc);
+  }
+  cluster_sync();
+}
+
+}  // namespace
+
+// KV8: 0 (the pools hold T), 1 e4m3, 2 e5m2 (codes widened to fp16 exactly;
+// a bf16 query row goes into fp16 by a power of two that its scores take
+// back; a block's V scale multiplies the block's product, so that no weight
+// carries it). NT: tiles of 8 query heads.
+template <typename T, int KV8, int D, int NT>
+__global__ void __launch_bounds__(kSparseThreads) sparse_kernel(const __grid_constant__ SparseParams p) {
+  using M = typename std::conditional<KV8 != 0, __half, T>::type;  // the products' type
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int H = 8 * NT;
+  constexpr int KP = KV8 ? D / 64 : D / 32;  // 16-byte pieces of a K row for a lane
+  constexpr int VP = KV8 ? D / 128 : D / 64; // 16-byte pieces of a V row for a lane
+  constexpr int MT = D / 16;                 // tiles of 16 output dimensions
+  constexpr int KS = D / 16;                 // steps of the score product
+  __shared__ __align__(16) float so[kSparseWarps][H][D];
+  __shared__ float sm[kSparseWarps][H], sl[kSparseWarps][H];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+  const SparseRow w = sparse_row(p, H);
+  const int halves = p.block_size >> 4;  // items of a block
+
+  // The queries' fragments: head r (and r + 8), 16 bytes as the keys lie.
+  uint32_t qf[NT][KS][2];
+  float mul[NT][2];  // of the scores of heads 2 c, 2 c + 1
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = n * 8 + r;
+    const T* q = static_cast<const T*>(p.q) + ((int64_t)w.seq * p.num_q_heads + w.first_head + (h < w.heads ? h : 0)) * D;
+    if constexpr (KV8 == 0) {
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4*>(q + 32 * j + 8 * c);
+        qf[n][2 * j][0] = x.x;
+        qf[n][2 * j][1] = x.y;
+        qf[n][2 * j + 1][0] = x.z;
+        qf[n][2 * j + 1][1] = x.w;
+      }
+      mul[n][0] = mul[n][1] = p.scale_log2;
+    } else {
+      float f = 1.f;
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * c);
+        const uint4 y = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * c + 8);
+        const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qf[n][4 * j + i / 2][i & 1] = v[i];
+      }
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[n][k][i]));
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        // The row's largest value goes to [2^14, 2^15): what that puts below
+        // fp16's normal numbers is 2^28 times smaller.
+        const int e = top > 0.f ? min(max((__float_as_int(top) >> 23) - 127 - 14, -126), 113) : 0;
+        const float down = __int_as_float((127 - e) << 23);
+        f = __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[n][k][i]));
+            qf[n][k][i] = MmaOp<__half>::pack(v.x * down, v.y * down);
+          }
+      }
+      mul[n][0] = p.scale_log2 * __shfl_sync(kAll, f, 8 * c);
+      mul[n][1] = p.scale_log2 * __shfl_sync(kAll, f, 8 * c + 4);
+    }
+  }
+
+  float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+    m[n][0] = m[n][1] = neg_inf();
+    l[n][0] = l[n][1] = 0.f;
+  }
+
+  const int warps = w.ranks * kSparseWarps, me = w.rank * kSparseWarps + warp, items = w.entries * halves;
+  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
+  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
+  constexpr int RB = KV8 ? D : 2 * D;  // bytes of a row
+  for (int base = me; base < items; base += 32 * warps) {
+    // 32 items ahead, one a lane.
+    const int mine = base + lane * warps;
+    int2 it = make_int2(0, 0);
+    float ks = 1.f, vs = 1.f;
+    if (mine < items) {
+      const int i = halves == 2 ? mine >> 1 : mine, sub = halves == 2 ? mine & 1 : 0;
+      it = sparse_item(p, w, i, sub);
+      if constexpr (KV8 != 0) {
+        const float2 s = *reinterpret_cast<const float2*>(p.kv_scales + ((int64_t)it.x * p.num_kv_heads + w.head) * 2);
+        ks = s.x;
+        vs = s.y;
+      }
+    }
+    const int count = min(32, (items - base + warps - 1) / warps);
+    for (int x = 0; x < count; ++x) {
+      const int blk = __shfl_sync(kAll, it.x, x), n_tok = __shfl_sync(kAll, it.y, x);
+      const float k_scale = KV8 ? __shfl_sync(kAll, ks, x) : 1.f, v_scale = KV8 ? __shfl_sync(kAll, vs, x) : 1.f;
+      if (n_tok == 0) continue;
+      const int sub = halves == 2 ? (base + x * warps) & 1 : 0;
+      const int64_t at = (((int64_t)blk * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * RB;
+      const int last = n_tok - 1;
+      uint4 kr[2][KP], vr[4][VP];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < KP; ++j)
+          kr[i][j] = *reinterpret_cast<const uint4*>(kc + at + min(r + 8 * i, last) * RB + 64 * j + 16 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < VP; ++j)
+          vr[i][j] = *reinterpret_cast<const uint4*>(vc + at + min(2 * c + (i & 1) + 8 * (i >> 1), last) * RB +
+                                                     128 * j + 16 * r);
+      // Scores.
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KP; ++j) {
+        const uint32_t a0[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
+        const uint32_t a1[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
+        if constexpr (KV8 == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t a[4] = {a0[2 * k], a1[2 * k], a0[2 * k + 1], a1[2 * k + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) MmaOp<M>::run(s[n], a, qf[n][2 * j + k][0], qf[n][2 * j + k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t a[4];
+            fp8x4_to_f16x4<KV8 == 2>(a0[k], a[0], a[2]);
+            fp8x4_to_f16x4<KV8 == 2>(a1[k], a[1], a[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) MmaOp<M>::run(s[n], a, qf[n][4 * j + k][0], qf[n][4 * j + k][1]);
+          }
+        }
+      }
+      bool move = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[n][i] = r + 8 * (i >> 1) < n_tok ? s[n][i] * (KV8 ? mul[n][i & 1] * k_scale : mul[n][i & 1]) : neg_inf();
+          move |= s[n][i] > m[n][i & 1] + kMoveAt;
+        }
+      }
+      if (__any_sync(kAll, move)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = fmaxf(s[n][i], s[n][2 + i]);
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+            top = fmaxf(top, m[n][i]);
+            if (top > m[n][i]) {
+              const float f = fast_exp2(m[n][i] - top);
+              m[n][i] = top;
+              l[n][i] *= f;
+#pragma unroll
+              for (int t = 0; t < MT; ++t) {
+                o[n][t][i] *= f;
+                o[n][t][2 + i] *= f;
+              }
+            }
+          }
+        }
+      }
+      // Weights, rounded to the products' type (their sums are taken before).
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float ref = m[n][i & 1];
+          e[i] = fast_exp2(s[n][i] - (ref == neg_inf() ? 0.f : ref));
+          l[n][i & 1] += e[i];
+        }
+        pf[n][0] = transposed(MmaOp<M>::pack(e[0], e[1]));
+        pf[n][1] = transposed(MmaOp<M>::pack(e[2], e[3]));
+      }
+      // Lane elements: word 2 i, 2 i + 1 of token i's dimensions.
+      uint32_t v[4][MT];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool there = 2 * c + (i & 1) + 8 * (i >> 1) < n_tok;
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+          const uint32_t x4[4] = {vr[i][j].x, vr[i][j].y, vr[i][j].z, vr[i][j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t word = there ? x4[k] : 0u;
+            if constexpr (KV8 == 0) v[i][4 * j + k] = word;
+            else fp8x4_to_f16x4<KV8 == 2>(word, v[i][8 * j + 2 * k], v[i][8 * j + 2 * k + 1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        // Elements t and t + MT of every token's list.
+        const int e0 = t, e1 = t + MT;
+        const uint32_t a[4] = {__byte_perm(v[0][e0 / 2], v[1][e0 / 2], e0 & 1 ? 0x7632 : 0x5410),
+                               __byte_perm(v[0][e1 / 2], v[1][e1 / 2], e1 & 1 ? 0x7632 : 0x5410),
+                               __byte_perm(v[2][e0 / 2], v[3][e0 / 2], e0 & 1 ? 0x7632 : 0x5410),
+                               __byte_perm(v[2][e1 / 2], v[3][e1 / 2], e1 & 1 ? 0x7632 : 0x5410)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (KV8 == 0) {
+            MmaOp<M>::run(o[n][t], a, pf[n][0], pf[n][1]);
+          } else {
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            MmaOp<M>::run(part, a, pf[n][0], pf[n][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][t][i] = fmaf(v_scale, part[i], o[n][t][i]);
+          }
+        }
+      }
+    }
+  }
+
+  // Join the warps. Element e of a lane's list is dimension e of 16-byte
+  // piece e / per, `per` elements each, its pieces 8 lanes apart.
+  constexpr int PER = KV8 ? 16 : 8;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = n * 8 + 2 * c + i;
+      float sum = l[n][i];
+      sum += __shfl_xor_sync(kAll, sum, 4);
+      sum += __shfl_xor_sync(kAll, sum, 8);
+      sum += __shfl_xor_sync(kAll, sum, 16);
+      if (r == 0) {
+        sm[warp][h] = m[n][i];
+        sl[warp][h] = sum;
+      }
+#pragma unroll
+      for (int e = 0; e < 2 * MT; ++e) {
+        const int d = e / PER * (8 * PER) + r * PER + e % PER;
+        so[warp][h][d] = o[n][e % MT][i + 2 * (e / MT)];
+      }
+    }
+  }
+  __syncthreads();
+  for (int x = tid; x < H * D; x += kSparseThreads) {
+    const int h = x / D, d = x - h * D;
+    float top = sm[0][h], acc = 0.f;
+#pragma unroll
+    for (int i = 1; i < kSparseWarps; ++i) top = fmaxf(top, sm[i][h]);
+#pragma unroll
+    for (int i = 0; i < kSparseWarps; ++i)
+      acc += (sm[i][h] == neg_inf() ? 1.f : exp2f(sm[i][h] - top)) * so[i][h][d];
+    so[0][h][d] = acc;
+  }
+  __syncthreads();
+  if (tid < H) {
+    float top = sm[0][tid], sum = 0.f;
+#pragma unroll
+    for (int i = 1; i < kSparseWarps; ++i) top = fmaxf(top, sm[i][tid]);
+#pragma unroll
+    for (int i = 0; i < kSparseWarps; ++i)
+      sum += (sm[i][tid] == neg_inf() ? 1.f : exp2f(sm[i][tid] - top)) * sl[i][tid];
+    sm[0][tid] = top;
+    sl[0][tid] = sum;
+  }
+  sparse_join<T, D>(p, w, &so[0][0][0], sm[0], sl[0]);
+}
+
+// fp32 on CUDA cores, exact fp32 arithmetic: a CTA takes 16 tokens at a time,
+// scores them pair by pair of (head, token) and adds their values, a thread to
+// each dimension, for 8 query heads.
+template <int D>
+__global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid_constant__ SparseParams p) {
+  constexpr int H = 8, TOK = 16, ST = D + 4;
+  constexpr int DT = (D + kSparseThreads - 1) / kSparseThreads;  // dimensions of a thread
+  extern __shared__ __align__(16) float sh[];
+  float* so = sh;                  // [H][D]
+  float* sq = so + H * D;          // [H][ST]
+  float* sk = sq + H * ST;         // [TOK][ST]
+  float* sv = sk + TOK * ST;       // [TOK][D]
+  __shared__ float ss[H][TOK], sm[H], sl[H], sf[H];
+  const int tid = threadIdx.x;
+  const SparseRow w = sparse_row(p, H);
+  const int halves = p.block_size >> 4, items = w.entries * halves;
+  const float* q = static_cast<const float*>(p.q) + ((int64_t)w.seq * p.num_q_heads + w.first_head) * D;
+  for (int x = tid; x < w.heads * D; x += kSparseThreads) sq[x / D * ST + x % D] = q[x];
+  if (tid < H) {
+    sm[tid] = neg_inf();
+    sl[tid] = 0.f;
+  }
+  float acc[H][DT];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int i = 0; i < DT; ++i) acc[h][i] = 0.f;
+  for (int x = w.rank; x < items; x += w.ranks) {
+    const int sub = halves == 2 ? x & 1 : 0;
+    // (Every thread asks: the answer is the same.)
+    const int2 it = sparse_item(p, w, halves == 2 ? x >> 1 : x, sub);
+    if (it.y == 0) continue;
+    const int64_t at = (((int64_t)it.x * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * D;
+    __syncthreads();
+    for (int y = tid; y < it.y * (D / 4); y += kSparseThreads) {
+      const int t = y / (D / 4), d = (y - t * (D / 4)) * 4;
+      *reinterpret_cast<float4*>(sk + t * ST + d) =
+          *reinterpret_cast<const float4*>(static_cast<const float*>(p.k_cache) + at + t * D + d);
+      *reinterpret_cast<float4*>(sv + t * D + d) =
+          *reinterpret_cast<const float4*>(static_cast<const float*>(p.v_cache) + at + t * D + d);
+    }
+    __syncthreads();
+    {
+      const int t = tid % TOK, h = tid / TOK;  // 16 tokens x 8 heads
+      float s = neg_inf();
+      if (t < it.y && h < w.heads) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int d = 0; d < D; d += 4) {
+          const float4 x4 = *reinterpret_cast<const float4*>(sk + t * ST + d);
+          const float4 y4 = *reinterpret_cast<const float4*>(sq + h * ST + d);
+          a.x = fmaf(x4.x, y4.x, a.x);
+          a.y = fmaf(x4.y, y4.y, a.y);
+          a.z = fmaf(x4.z, y4.z, a.z);
+          a.w = fmaf(x4.w, y4.w, a.w);
+        }
+        s = ((a.x + a.y) + (a.z + a.w)) * p.scale_log2;
+      }
+      float top = s;
+#pragma unroll
+      for (int i = 1; i < TOK; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      const float old = sm[h], now = fmaxf(old, top);
+      const float ref = now == neg_inf() ? 0.f : now;
+      const float e = exp2f(s - ref);
+      float sum = e;
+#pragma unroll
+      for (int i = 1; i < TOK; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+      ss[h][t] = e;
+      __syncwarp();
+      if (t == 0) {
+        const float f = old == neg_inf() ? 1.f : exp2f(old - ref);
+        sf[h] = f;
+        sl[h] = sl[h] * f + sum;
+        sm[h] = now;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const float f = sf[h];
+#pragma unroll
+      for (int i = 0; i < DT; ++i) acc[h][i] *= f;
+      for (int t = 0; t < it.y; ++t) {
+        const float e = ss[h][t];
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          const int d = tid + i * kSparseThreads;
+          if (d < D) acc[h][i] = fmaf(e, sv[t * D + d], acc[h][i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+      if (tid + i * kSparseThreads < D) so[h * D + tid + i * kSparseThreads] = acc[h][i];
+  sparse_join<float, D>(p, w, so, sm, sl);
+}
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int launch_sparse(void (*kernel)(SparseParams), const SparseParams& p, int smem, int items_per_cta,
+                  cudaStream_t stream) {
+  const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
+  const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
+  // CTAs of a row: as many as keep the batch within three per SM and leave
+  // each enough items.
+  int ranks = 1;
+  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 3 * num_sms_current_device() &&
+         items >= (int64_t)ranks * 2 * items_per_cta)
+    ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * ranks));
+  cfg.blockDim = dim3(kSparseThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <int D>
+int launch_sparse_f32(const SparseParams& p, cudaStream_t stream) {
+  constexpr int smem = (8 * D + 24 * (D + 4) + 16 * D) * 4;
+  if (smem > 40 * 1024 &&
+      set_max_dynamic_smem(reinterpret_cast<const void*>(sparse_f32_kernel<D>), smem) != PA_OK)
+    return PA_ERR_CUDA;
+  return launch_sparse(sparse_f32_kernel<D>, p, smem, 4, stream);
+}
+
+template <typename T, int KV8, int D>
+int launch_sparse_tc(const SparseParams& p, cudaStream_t stream) {
+  return p.group <= 8 ? launch_sparse(sparse_kernel<T, KV8, D, 1>, p, 0, 2 * kSparseWarps, stream)
+                      : launch_sparse(sparse_kernel<T, KV8, D, 2>, p, 0, 2 * kSparseWarps, stream);
+}
+
+// kv8: 0, or 1 + the format of an 8-bit cache.
+int decode_sparse(const void* q, const void* k_cache, const void* v_cache, const float* kv_scales,
+                  const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                  const int32_t* block_lists, const int32_t* list_lens, int32_t max_list_len, int32_t num_seqs,
+                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                  int32_t num_blocks, float scale, void* out, pa_dtype dtype, int kv8, cudaStream_t stream) {
+  if (num_seqs < 0 || max_blocks_per_seq < 1 || max_list_len < 1 || num_q_heads < 1 || num_kv_heads < 1 ||
+      num_blocks < 1 || !std::isfinite(scale))
+    return PA_ERR_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16 && (kv8 || dtype != PA_F32)) return PA_ERR_DTYPE;
+  if (num_q_heads % num_kv_heads) return PA_ERR_HEADS;
+  if (block_size != 16 && block_size != 32) return PA_ERR_BLOCKSIZE;
+  const int group = num_q_heads / num_kv_heads;
+  if (kv8 ? head_dim != 128
+          : dtype == PA_F32 ? head_dim < 32 || head_dim > 256 || head_dim % 32 : head_dim != 64 && head_dim != 128)
+    return PA_ERR_UNSUPPORTED;
+  if (group > 128 || num_seqs > 65535 || max_list_len > (1 << 26)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !block_lists || !list_lens || !out ||
+      (kv8 && !kv_scales))
+    return PA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || (kv8 && !aligned16(kv_scales)))
+    return PA_ERR_ALIGN;
+  SparseParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.kv_scales = kv_scales;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.lists = block_lists;
+  p.list_lens = list_lens;
+  p.out = out;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_list_len = max_list_len;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.head_dim = head_dim;
+  p.block_size = block_size;
+  p.num_blocks = num_blocks;
+  p.group = group;
+  const int per_row = dtype == PA_F32 || group <= 8 ? 8 : 16;
+  p.row_groups = (group + per_row - 1) / per_row;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  if ((int64_t)num_seqs * num_kv_heads * p.row_groups > (1 << 27)) return PA_ERR_UNSUPPORTED;
+  if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
+  if (dtype == PA_F32) {
+    switch (head_dim / 32) {
+      case 1: return launch_sparse_f32<32>(p, stream);
+      case 2: return launch_sparse_f32<64>(p, stream);
+      case 3: return launch_sparse_f32<96>(p, stream);
+      case 4: return launch_sparse_f32<128>(p, stream);
+      case 5: return launch_sparse_f32<160>(p, stream);
+      case 6: return launch_sparse_f32<192>(p, stream);
+      case 7: return launch_sparse_f32<224>(p, stream);
+      default: return launch_sparse_f32<256>(p, stream);
+    }
+  }
+  const bool half = dtype == PA_F16;
+  if (kv8 == 1 + PA_KV_E4M3)
+    return half ? launch_sparse_tc<__half, 1, 128>(p, stream) : launch_sparse_tc<__nv_bfloat16, 1, 128>(p, stream);
+  if (kv8)
+    return half ? launch_sparse_tc<__half, 2, 128>(p, stream) : launch_sparse_tc<__nv_bfloat16, 2, 128>(p, stream);
+  if (head_dim == 64)
+    return half ? launch_sparse_tc<__half, 0, 64>(p, stream) : launch_sparse_tc<__nv_bfloat16, 0, 64>(p, stream);
+  return half ? launch_sparse_tc<__half, 0, 128>(p, stream) : launch_sparse_tc<__nv_bfloat16, 0, 128>(p, stream);
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+int pa_decode_sparse(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                     int32_t max_blocks_per_seq, const int32_t* seq_lens, const int32_t* block_lists,
+                     const int32_t* list_lens, int32_t max_list_len, int32_t num_seqs, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
+                     void* out, pa_dtype dtype, void* stream) {
+  return pa::decode_sparse(q, k_cache, v_cache, nullptr, block_tables, max_blocks_per_seq, seq_lens, block_lists,
+                           list_lens, max_list_len, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                           num_blocks, scale, out, dtype, 0, static_cast<cudaStream_t>(stream));
+}
+
+int pa_decode_sparse_fp8(const void* q, const void* k_cache, const void* v_cache, const float* kv_scales,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                         const int32_t* block_lists, const int32_t* list_lens, int32_t max_list_len,
+                         int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int32_t num_blocks, float scale, void* out, pa_dtype dtype,
+                         void* stream) {
+  return pa::decode_sparse(q, k_cache, v_cache, kv_scales, block_tables, max_blocks_per_seq, seq_lens, block_lists,
+                           list_lens, max_list_len, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                           num_blocks, scale, out, dtype, 1 + pa::PA_KV_E4M3, static_cast<cudaStream_t>(stream));
+}
+
+int pa_decode_sparse_e5m2(const void* q, const void* k_cache, const void* v_cache, const float* kv_scales,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                          const int32_t* block_lists, const int32_t* list_lens, int32_t max_list_len,
+                          int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t block_size, int32_t num_blocks, float scale, void* out, pa_dtype dtype,
+                          void* stream) {
+  return pa::decode_sparse(q, k_cache, v_cache, kv_scales, block_tables, max_blocks_per_seq, seq_lens, block_lists,
+                           list_lens, max_list_len, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                           num_blocks, scale, out, dtype, 1 + pa::PA_KV_E5M2, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -16,6 +16,10 @@ TreeStep is the step of a serving engine that drafts: the nodes of a draft
 tree instead of one new token, their attention in every layer
 (pa_decode_tree), then the choice (pa_verify_tree) and the kept rows' move
 (pa_compact_tree).
+SparseStep is a decode step over long contexts: queries and keys are rotated
+on the way into the cache (pa_rope_and_cache), every layer keeps summaries of
+its blocks (pa_block_summaries), and the attention reads the blocks that a
+query's scores choose (pa_select_blocks, pa_decode_sparse).
 This module only sequences library calls on one stream and owns the device
 buffers the calls need (slot mapping, output, split-KV workspace), allocated
 once with PyTorch.
@@ -338,6 +342,87 @@ class TreeStep:
         else:
             self.call_8bit("pa_compact_tree")(self.k_caches, self.v_caches, self.kv_scales, *tail, stream=stream)
         return self.path, self.path_lens, self.next_tokens
+
+
+class SparseStep:
+    """Steps over long contexts on the KV pools of a model's layers.
+
+    The engine fills the step's inputs (device tensors of fixed size, so that
+    a step can be captured once and replayed): ctx_lens (cached tokens of each
+    sequence before the step), seq_lens (with the step's), and for every new
+    token new_seq_ids and new_positions (rows behind the last sequence's are
+    padding and name a sequence outside the batch: pa_slot_mapping gives them
+    slot -1 and reports them; or fill slot_mapping instead of calling slots()).
+    Then slots(), and for every layer write(), which rotates, caches and
+    summarises, and attend(), one query token a sequence. A prompt's chunks go
+    through slots() and write() in the same way, with pa_chunked_prefill for
+    their attention. Where a sequence's blocks change by other means (a copy on
+    write, a swap, a compacted draft tree), summarize() makes their summaries
+    again.
+    """
+
+    def __init__(self, *, k_caches, v_caches, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
+                 seq_lens: torch.Tensor, new_seq_ids: torch.Tensor, new_positions: torch.Tensor,
+                 cos_sin: torch.Tensor, num_q_heads: int, dtype: torch.dtype, max_seq_len: int, max_new_tokens: int,
+                 max_list_len: int, scale: float, num_sink: int = 1, num_recent: int = 1, interleaved: bool = False,
+                 kv_scales=None, kv_format: str = "e4m3"):
+        if kv_format not in ("e4m3", "e5m2"):
+            raise ValueError(f"kv_format {kv_format!r}: e4m3 or e5m2")
+        self.k_caches, self.v_caches, self.kv_scales = list(k_caches), list(v_caches), kv_scales
+        self.suffix = "" if kv_scales is None else "_fp8" if kv_format == "e4m3" else "_e5m2"
+        self.block_tables, self.ctx_lens, self.seq_lens = block_tables, ctx_lens, seq_lens
+        self.new_seq_ids, self.new_positions, self.cos_sin = new_seq_ids, new_positions, cos_sin
+        self.max_seq_len, self.max_new_tokens = int(max_seq_len), int(max_new_tokens)
+        self.max_list_len, self.num_sink, self.num_recent = int(max_list_len), int(num_sink), int(num_recent)
+        self.scale, self.interleaved = float(scale), bool(interleaved)
+        self.num_blocks, hkv, self.block_size, d = self.k_caches[0].shape
+        total, n, dev = new_positions.shape[0], seq_lens.shape[0], seq_lens.device
+        self.slot_mapping = torch.empty(total, dtype=torch.int64, device=dev)
+        self.q = torch.zeros(total, num_q_heads, d, dtype=dtype, device=dev)
+        self.out = torch.empty(n, num_q_heads, d, dtype=dtype, device=dev)
+        self.block_lists = torch.empty(n, hkv, self.max_list_len, dtype=torch.int32, device=dev)
+        self.list_lens = torch.empty(n, hkv, dtype=torch.int32, device=dev)
+        self.summaries = [torch.zeros(self.num_blocks, hkv, 2, d, dtype=torch.int8, device=dev)
+                          for _ in self.k_caches]
+        self.summary_scales = [torch.zeros(self.num_blocks, hkv, device=dev) for _ in self.k_caches]
+
+    def pools(self, layer: int):
+        k, v = self.k_caches[layer], self.v_caches[layer]
+        return (k, v) if self.kv_scales is None else (k, v, self.kv_scales[layer])
+
+    def slots(self, stream=None) -> torch.Tensor:
+        """The new tokens' cache slots: once a step, before the first write()."""
+        return pa.pa_slot_mapping(self.block_tables, self.new_seq_ids, self.new_positions, self.block_size,
+                                  self.num_blocks, slot_mapping=self.slot_mapping, stream=stream)
+
+    def write(self, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+              stream=None) -> torch.Tensor:
+        """Rotate and cache one layer's new tokens and summarise their blocks:
+        the rotated queries (a buffer that the next layer reuses)."""
+        getattr(pa, "pa_rope_and_cache" + self.suffix)(
+            q, k_new, v_new, self.new_positions, self.slot_mapping, self.cos_sin, *self.pools(layer),
+            interleaved=self.interleaved, q_out=self.q, stream=stream)
+        self.summarize(layer, self.ctx_lens, self.max_new_tokens, stream=stream)
+        return self.q
+
+    def summarize(self, layer: int, first_tokens: torch.Tensor, max_new_tokens: int, stream=None) -> None:
+        """Summaries of one layer's blocks from first_tokens on."""
+        pools = self.pools(layer)
+        getattr(pa, "pa_block_summaries" + self.suffix)(
+            pools[0], *pools[2:], self.block_tables, first_tokens, self.seq_lens, max_new_tokens,
+            self.summaries[layer], self.summary_scales[layer], stream=stream)
+
+    def attend(self, layer: int, q: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Choose blocks for one rotated query token a sequence (what write()
+        returned, unless q is given) and attend to them (out is reused by the
+        next layer)."""
+        q = self.q[:self.seq_lens.shape[0]] if q is None else q
+        pa.pa_select_blocks(q, self.summaries[layer], self.summary_scales[layer], self.block_tables, self.seq_lens,
+                            self.max_seq_len, self.block_size, self.max_list_len, self.num_sink, self.num_recent,
+                            block_lists=self.block_lists, list_lens=self.list_lens, stream=stream)
+        return getattr(pa, "pa_decode_sparse" + self.suffix)(
+            q, *self.pools(layer), self.block_tables, self.seq_lens, self.block_lists, self.list_lens, self.scale,
+            out=self.out, stream=stream)
 
 
 class HostPipeline:
