@@ -800,10 +800,9 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
  * it is written. A slot outside the pool records PA_ERR_BLOCK_OOB, a position
  * outside [0, num_positions) PA_ERR_SEQLEN; such a token is skipped too.
  * num_q_heads 0 caches alone (q and q_out may be NULL). rot_dim is even, 2 to
- * min(head_dim, 256); head_dim * sizeof(dtype) a multiple of 16, head_dim at
- * most 1024; num_tokens * num_kv_heads at most 2^30, and a grid of
- * ceil(units / 128) CTAs a token below 2^31 (PA_ERR_UNSUPPORTED). Two tokens
- * with the same slot race.
+ * min(head_dim, 256); head_dim * sizeof(dtype) is a multiple of 16, head_dim
+ * at most 1024, head counts at most 2^20, num_tokens * num_kv_heads at most 2^30
+ * (PA_ERR_UNSUPPORTED). Two tokens with the same slot race.
  */
 int pa_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, const float* cos_sin,

@@ -313,6 +313,40 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Asynchronous copies of 16 (past L1) or 4 bytes into shared memory, in groups
+// that a thread waits for in order.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {  // for all groups but the last N
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Quotients by one divisor, each correctly rounded: with a correctly rounded
+// reciprocal, a quotient and its exact remainder give the rounded quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) as long as nothing overflows or loses bits below the
+// normal numbers, which a divisor from 2^-80 to 1 sees to for the uses here
+// (quotients of at most 2^16 in size, of which those below 2^-40 matter by
+// their sign alone). Other divisors go through the division itself.
+struct Divisor {
+  float by, inv;
+  bool quick;
+};
+__device__ __forceinline__ Divisor divisor(float s) {
+  return Divisor{s, __fdiv_rn(1.f, s), s >= 8.27180613e-25f && s <= 1.f};
+}
+__device__ __forceinline__ float quotient(float x, const Divisor& d) {
+  if (!d.quick) return __fdiv_rn(x, d.by);
+  const float y = __fmul_rn(x, d.inv);
+  return __fmaf_rn(__fmaf_rn(-y, d.by, x), d.inv, y);
+}
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }

@@ -7,6 +7,7 @@
 // multiply-add), so results can be reproduced bit for bit from the table.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_fp8.cuh"
@@ -44,19 +45,34 @@ __device__ __forceinline__ void turn(unsigned long long t, float& c, float& s) {
   s = quarter & 2 ? -b : b;
 }
 
+// A thread keeps N pairs (4 where the halves are whole float4) and goes from
+// position to position.
+template <int N>
 __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(float* __restrict__ out, uint32_t first,
-                                                                   int64_t positions, int32_t half, float amplitude,
+                                                                   uint32_t positions, int32_t half, float amplitude,
                                                                    const __grid_constant__ RopeSteps steps) {
-  const int64_t total = positions * half;
-  for (int64_t x = blockIdx.x * (int64_t)kRopeThreads + threadIdx.x; x < total;
-       x += (int64_t)gridDim.x * kRopeThreads) {
-    const int64_t p = x / half;
-    const int i = (int)(x - p * half);
-    float c, s;
-    turn((first + (unsigned long long)p) * steps.step[i], c, s);
-    float* row = out + p * 2 * half;
-    row[i] = c * amplitude;
-    row[half + i] = s * amplitude;
+  const int groups = half / N, rows = kRopeThreads / groups;  // positions that a CTA does at a time
+  const int row = threadIdx.x / groups, i = (threadIdx.x - row * groups) * N;
+  if (row >= rows) return;
+  unsigned long long step[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) step[k] = steps.step[i + k];
+  for (int64_t p = (int64_t)blockIdx.x * rows + row; p < positions; p += (int64_t)gridDim.x * rows) {
+    float c[N], s[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      turn((first + (unsigned long long)p) * step[k], c[k], s[k]);
+      c[k] *= amplitude;
+      s[k] *= amplitude;
+    }
+    float* dst = out + p * 2 * half + i;
+    if constexpr (N == 4) {
+      *reinterpret_cast<float4*>(dst) = make_float4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<float4*>(dst + half) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+      dst[0] = c[0];
+      dst[half] = s[0];
+    }
   }
 }
 
@@ -79,10 +95,12 @@ struct RopeParams {
   void* v_cache;
   float* kv_scales;
   int32_t num_blocks, block_size, num_q_heads, num_kv_heads, head_dim;
-  int32_t row_units;    // work units of a rotated row
-  int32_t token_units;  // work units of a token
-  int32_t chunks;       // CTAs of a token
-  int64_t q_ctas;       // 8-bit caches: CTAs that rotate queries
+  int32_t row_units;  // work units of a row
+  int32_t rows;       // rows of a token: queries, and keys and values of a 16- or 32-bit cache
+  int32_t pass_rows;  // rows that a CTA does at a time
+  int32_t chunks;     // CTAs of a token
+  int64_t q_ctas;     // 8-bit caches: CTAs that rotate queries
+  int32_t group;      // 8-bit caches: tokens of a warp
   int* status;
 };
 
@@ -129,109 +147,131 @@ struct Vec16 {
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<int4*>(p) = raw; }
 };
 
+// One element.
+template <typename T>
+struct Vec1 {
+  T e[1];
+  __device__ __forceinline__ void load(const T* p) { e[0] = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = e[0]; }
+};
+
 enum RopeLayout { kRopePairs, kRopeHalves, kRopeHalvesOdd };
 
-// Source and destination of row `row` of a token: queries first, then keys
+// Where row `row` of a token lies, and where it goes: queries first, then keys
 // and values.
 template <typename T>
-__device__ __forceinline__ void rope_ends(const RopeParams& p, int64_t t, int64_t slot, int row, const T*& src,
-                                          T*& dst) {
-  const int d = p.head_dim;
-  if (row < p.num_q_heads) {
-    src = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)row * d;
-    dst = static_cast<T*>(p.q_out) + (t * p.num_q_heads + row) * d;
-    return;
-  }
-  const bool is_v = row >= p.num_q_heads + p.num_kv_heads;
-  const int h = row - p.num_q_heads - (is_v ? p.num_kv_heads : 0);
-  const int64_t blk = slot / p.block_size;
-  const int off = (int)(slot - blk * p.block_size);
-  const int64_t to = ((blk * p.num_kv_heads + h) * p.block_size + off) * d;
-  src = static_cast<const T*>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) + (int64_t)h * d;
-  dst = static_cast<T*>(is_v ? p.v_cache : p.k_cache) + to;
+__device__ __forceinline__ const T* rope_source(const RopeParams& p, int64_t t, int row) {
+  const int h = row - p.num_q_heads;
+  return h < 0 ? static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)row * p.head_dim
+         : h < p.num_kv_heads
+             ? static_cast<const T*>(p.k) + t * p.k_stride + (int64_t)h * p.head_dim
+             : static_cast<const T*>(p.v) + t * p.v_stride + (int64_t)(h - p.num_kv_heads) * p.head_dim;
+}
+template <typename T>
+__device__ __forceinline__ T* rope_target(const RopeParams& p, int64_t t, int64_t blk, int off, int row) {
+  const int h = row - p.num_q_heads;
+  if (h < 0) return static_cast<T*>(p.q_out) + (t * p.num_q_heads + row) * p.head_dim;
+  const bool is_v = h >= p.num_kv_heads;
+  return static_cast<T*>(is_v ? p.v_cache : p.k_cache) +
+         ((blk * p.num_kv_heads + (is_v ? h - p.num_kv_heads : h)) * p.block_size + off) * p.head_dim;
 }
 
-// One thread per unit of a token: with halves a vector of each half or a
-// vector that stays, with pairs a vector of pairs; a vector of a value row.
-// (kRopeHalvesOdd, a half that is no whole number of vectors: an element of
-// each half, or one that stays.) Rows are read once and written once; a
-// query may be rotated in place, because the thread that writes an element is
-// the one that reads it.
+// A CTA takes a token's rows, or a part of them, `pass_rows` at a time; a
+// thread keeps its place in the row and with it its cosines and sines. Its
+// place is a vector of each half, or a vector that stays (kRopeHalves); a
+// vector of pairs (kRopePairs); an element of each half, or one that stays
+// (kRopeHalvesOdd: a half that is no whole number of vectors). Rows are read
+// once and written once, kRopeBatch of them in flight; a query may be rotated
+// in place, because the thread that writes an element is the one that reads it.
+constexpr int kRopeBatch = 4;
+
 template <typename T, int LAYOUT>
-__device__ __forceinline__ void rope_unit(const RopeParams& p, int64_t t, int unit) {
-  constexpr int N = Vec16<T>::N;
+__device__ __forceinline__ void rope_token(const RopeParams& p, int64_t t, int chunk) {
+  constexpr int N = LAYOUT == kRopeHalvesOdd ? 1 : Vec16<T>::N;
+  constexpr int PAIRS = LAYOUT == kRopePairs ? N / 2 : N;
+  using V = typename std::conditional<LAYOUT == kRopeHalvesOdd, Vec1<T>, Vec16<T>>::type;
+  const int places = min(p.row_units, kRopeThreads), row0 = threadIdx.x / places;
+  const int half = p.rot >> 1, rotated = p.num_q_heads + p.num_kv_heads, step = p.chunks * p.pass_rows;
   const int64_t slot = p.slots[t];
-  const float* cs = rope_row(p, t, slot, unit == 0);
-  if (!cs) return;
-  const int half = p.rot >> 1, rotated = (p.num_q_heads + p.num_kv_heads) * p.row_units;
-  const T* src;
-  T* dst;
-  if (unit >= rotated) {
-    const int u = unit - rotated, per = p.head_dim / N, row = u / per;
-    rope_ends(p, t, slot, p.num_q_heads + p.num_kv_heads + row, src, dst);
-    Vec16<T> x;
-    x.load(src + (u - row * per) * N);
-    x.store(dst + (u - row * per) * N);
-    return;
-  }
-  const int row = unit / p.row_units, u = unit - row * p.row_units;
-  rope_ends(p, t, slot, row, src, dst);
-  if constexpr (LAYOUT == kRopePairs) {
+  if (row0 >= p.pass_rows) return;
+  for (int u = threadIdx.x - row0 * places; u < p.row_units; u += places) {
     const int d = u * N;
-    Vec16<T> x;
-    x.load(src + d);
+    // Pairs of this place: all of them turn, or (pairs) those below rot.
+    const bool two = LAYOUT != kRopePairs && d < half;
+    const int at = LAYOUT == kRopePairs || two ? d : half + d;  // a place behind the halves
+    const int turning = LAYOUT == kRopePairs ? max(0, min(PAIRS, (p.rot - d) >> 1)) : two ? PAIRS : 0;
+    int r0 = chunk * p.pass_rows + row0;
+    V x[kRopeBatch], y[kRopeBatch];
+    auto load = [&] {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      if (d + i < p.rot) {
-        float a = to_f32(x.e[i]), b = to_f32(x.e[i + 1]);
-        rotate(a, b, cs[(d + i) >> 1], cs[half + ((d + i) >> 1)]);
-        x.e[i] = from_f32<T>(a);
-        x.e[i + 1] = from_f32<T>(b);
+      for (int k = 0; k < kRopeBatch; ++k) {
+        if (r0 + k * step >= p.rows) break;
+        const T* src = rope_source<T>(p, t, r0 + k * step);
+        x[k].load(src + at);
+        if (two) y[k].load(src + half + d);
+      }
+    };
+    load();  // (before the token's place is known: its rows are there in any case)
+    const float* cs = rope_row(p, t, slot, chunk == 0 && threadIdx.x == 0);
+    if (!cs) return;
+    const int64_t blk = slot / p.block_size;
+    const int off = (int)(slot - blk * p.block_size);
+    float c[PAIRS], s[PAIRS];
+    const float* from = cs + (LAYOUT == kRopePairs ? d >> 1 : d);
+    if (turning == PAIRS && PAIRS % 4 == 0 && (half & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < PAIRS / 4; ++i) {
+        reinterpret_cast<float4*>(c)[i] = reinterpret_cast<const float4*>(from)[i];
+        reinterpret_cast<float4*>(s)[i] = reinterpret_cast<const float4*>(from + half)[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) {
+        c[i] = i < turning ? from[i] : 1.f;
+        s[i] = i < turning ? from[half + i] : 0.f;
       }
     }
-    x.store(dst + d);
-  } else if constexpr (LAYOUT == kRopeHalves) {
-    const int d = u * N;
-    Vec16<T> x, y;
-    if (d >= half) {  // behind the rotated part
-      x.load(src + half + d);
-      x.store(dst + half + d);
-      return;
-    }
-    x.load(src + d);
-    y.load(src + half + d);
-    float c[N], s[N];
+    while (true) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + d + i);
-      *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(cs + half + d + i);
-    }
+      for (int k = 0; k < kRopeBatch; ++k) {
+        const int row = r0 + k * step;
+        if (row >= p.rows) break;
+        if (row < rotated) {
+          if constexpr (LAYOUT == kRopePairs) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float a = to_f32(x.e[i]), b = to_f32(y.e[i]);
-      rotate(a, b, c[i], s[i]);
-      x.e[i] = from_f32<T>(a);
-      y.e[i] = from_f32<T>(b);
+            for (int i = 0; i < PAIRS; ++i) {
+              if (i < turning) {
+                float a = to_f32(x[k].e[2 * i]), b = to_f32(x[k].e[2 * i + 1]);
+                rotate(a, b, c[i], s[i]);
+                x[k].e[2 * i] = from_f32<T>(a);
+                x[k].e[2 * i + 1] = from_f32<T>(b);
+              }
+            }
+          } else if (two) {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+              float a = to_f32(x[k].e[i]), b = to_f32(y[k].e[i]);
+              rotate(a, b, c[i], s[i]);
+              x[k].e[i] = from_f32<T>(a);
+              y[k].e[i] = from_f32<T>(b);
+            }
+          }
+        }
+        T* dst = rope_target<T>(p, t, blk, off, row);
+        x[k].store(dst + at);
+        if (two) y[k].store(dst + half + d);
+      }
+      r0 += kRopeBatch * step;
+      if (r0 >= p.rows) break;
+      load();
     }
-    x.store(dst + d);
-    y.store(dst + half + d);
-  } else {
-    if (u >= half) {
-      dst[half + u] = src[half + u];
-      return;
-    }
-    float a = to_f32(src[u]), b = to_f32(src[half + u]);
-    rotate(a, b, cs[u], cs[half + u]);
-    dst[u] = from_f32<T>(a);
-    dst[half + u] = from_f32<T>(b);
   }
 }
 
 template <typename T, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  const int64_t t = blockIdx.x / p.chunks;
-  const int unit = (int)(blockIdx.x - t * p.chunks) * kRopeThreads + threadIdx.x;
-  if (unit < p.token_units) rope_unit<T, LAYOUT>(p, t, unit);
+  const unsigned t = blockIdx.x / p.chunks;
+  rope_token<T, LAYOUT>(p, t, blockIdx.x - t * p.chunks);
 }
 
 // ---------------------------------------------------------------------------
@@ -241,13 +281,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 // rounding, not two).
 // ---------------------------------------------------------------------------
 
-// Elements d .. d + VEC - 1 of a row, rotated if cs is given. `whole`: the
-// halves are whole numbers of vectors.
+// Elements d .. d + VEC - 1 of a row as they lie.
+template <typename T, int VEC>
+__device__ __forceinline__ void row_values(const T* row, int d, float (&x)[VEC]) {
+  struct alignas(VEC * sizeof(T)) Part {
+    T e[VEC];
+  };
+  const Part v = *reinterpret_cast<const Part*>(row + d);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) x[i] = to_f32(v.e[i]);
+}
+
+// The same, rotated if cs is given. `whole`: the halves are whole numbers of
+// VEC.
 template <typename T, int VEC>
 __device__ __forceinline__ void rope_values(const T* row, const float* cs, int d, int rot, bool inter, bool whole,
                                             float (&x)[VEC]) {
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) x[i] = to_f32(row[d + i]);
+  row_values<T, VEC>(row, d, x);
   if (!cs || d >= rot) return;
   const int half = rot >> 1;
   if (inter) {
@@ -258,16 +308,14 @@ __device__ __forceinline__ void rope_values(const T* row, const float* cs, int d
   }
   if (whole) {
     const bool upper = d >= half;
-    const int lo = upper ? d - half : d, other = upper ? d - half : d + half;
+    const int lo = upper ? d - half : d;
+    float y[VEC];
+    row_values<T, VEC>(row, upper ? lo : d + half, y);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      float a = x[i], b = to_f32(row[other + i]);
-      if (upper) {
-        rotate(b, a, cs[lo + i], cs[half + lo + i]);
-      } else {
-        rotate(a, b, cs[lo + i], cs[half + lo + i]);
-      }
-      x[i] = a;
+      float a = upper ? y[i] : x[i], b = upper ? x[i] : y[i];
+      rotate(a, b, cs[lo + i], cs[half + lo + i]);
+      x[i] = upper ? b : a;
     }
     return;
   }
@@ -283,67 +331,66 @@ __device__ __forceinline__ void rope_values(const T* row, const float* cs, int d
   }
 }
 
+// A token's place, or -1 if it is skipped.
+__device__ __forceinline__ int64_t rope_place(const RopeParams& p, int64_t j) {
+  if (j < 0 || j >= p.num_tokens) return -1;
+  const int64_t s = p.slots[j];
+  if (s < 0 || s >= (int64_t)p.num_blocks * p.block_size) return -1;
+  const int32_t pos = p.positions[j];
+  return pos >= 0 && pos < p.num_positions ? s : -1;
+}
+
+// The run of tokens that starts with token t (its place: slot): one KV head of
+// one pool. Rows are loaded kRopeBatch at a time; the rows of a run that is no
+// longer are kept from the search for the largest value to their encoding.
 template <typename T, int VEC, bool E5>
-__device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter, int64_t w) {
+__device__ __forceinline__ void rope_run_8bit(const RopeParams& p, bool inter, int64_t t, int64_t slot, int h,
+                                              int pool) {
   constexpr int D = VEC * 32;
   constexpr unsigned kFull = 0xffffffffu;
-  const int lane = threadIdx.x & 31, hkv = p.num_kv_heads, bs = p.block_size;
-  const int64_t cap = (int64_t)p.num_blocks * bs;
-  const int64_t t = w / (hkv * 2);
-  const int rem = (int)(w - t * hkv * 2), h = rem >> 1, pool = rem & 1;
-  // A token counts if it has a place and a position (those that have not are
-  // skipped as padding is).
-  auto place = [&](int64_t j) -> int64_t {
-    if (j < 0 || j >= p.num_tokens) return -1;
-    const int64_t s = p.slots[j];
-    if (s < 0 || s >= cap) return -1;
-    const int32_t pos = p.positions[j];
-    return pos >= 0 && pos < p.num_positions ? s : -1;
-  };
-  const int64_t slot = place(t);
-  if (slot < 0) {
-    if (lane == 0 && rem == 0) rope_row(p, t, p.slots[t], true);
-    return;
-  }
-  const int64_t blk = slot / bs;
-  // The first token of a run leads: the nearest one before it that counts
-  // lies in another block.
-  for (int64_t base = t - 1; base >= 0; base -= 32) {
-    const int64_t sj = place(base - lane);
-    const unsigned ok = __ballot_sync(kFull, sj >= 0);
-    if (ok) {
-      const int64_t near = __shfl_sync(kFull, sj, __ffs(ok) - 1);  // lowest lane = latest token
-      if (near / bs == blk) return;
-      break;
-    }
-  }
+  const int lane = threadIdx.x & 31, bs = p.block_size;
+  const int64_t blk = slot / bs, at = blk * p.num_kv_heads + h;
   const T* src = static_cast<const T*>(pool == 0 ? p.k : p.v) + h * D;
   const int64_t stride = pool == 0 ? p.k_stride : p.v_stride;
   const bool whole = (p.rot >> 1) % VEC == 0;
-  uint8_t* codes =
-      static_cast<uint8_t*>(pool == 0 ? p.k_cache : p.v_cache) + (blk * hkv + h) * (int64_t)bs * D + lane * VEC;
-  auto values = [&](int64_t j, float (&x)[VEC]) {
-    const float* cs = pool == 0 ? p.table + (int64_t)p.positions[j] * p.rot : nullptr;
-    rope_values<T, VEC>(src + j * stride, cs, lane * VEC, p.rot, inter, whole, x);
+  uint8_t* codes = static_cast<uint8_t*>(pool == 0 ? p.k_cache : p.v_cache) + at * bs * D + lane * VEC;
+  float* sp = p.kv_scales + at * 2 + pool;
+  const float stored = *sp;
+  float x[kRopeBatch][VEC];
+  int off[kRopeBatch];
+  // The next rows of `mem` (tokens base + its bits, in blocks' offsets sj).
+  auto take = [&](int64_t base, int64_t sj, unsigned& mem) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      if (!mem) break;
+      const int ln = __ffs(mem) - 1;
+      mem &= mem - 1;
+      off[k] = (int)(__shfl_sync(kFull, sj, ln) - blk * bs);
+      const float* cs = pool == 0 ? p.table + (int64_t)p.positions[base + ln] * p.rot : nullptr;
+      rope_values<T, VEC>(src + (base + ln) * stride, cs, lane * VEC, p.rot, inter, whole, x[k]);
+      n = k + 1;
+    }
+    return n;
   };
-  // The run's rows: their largest value, the lowest offset, one past the end.
   float amax = 0.f;
-  int omin = bs;
+  int omin = bs, rows = 0, kept = 0;
   int64_t end = p.num_tokens;
   for (int64_t base = t; base < p.num_tokens; base += 32) {
-    const int64_t sj = place(base + lane);
+    const int64_t sj = rope_place(p, base + lane);
     const unsigned other = __ballot_sync(kFull, sj >= 0 && sj / bs != blk);
     const int lim = other ? __ffs(other) - 1 : 32;
     unsigned mem = __ballot_sync(kFull, sj >= 0 && lane < lim);
     while (mem) {
-      const int ln = __ffs(mem) - 1;
-      mem &= mem - 1;
-      const int64_t sm = __shfl_sync(kFull, sj, ln);
-      omin = min(omin, (int)(sm - blk * bs));
-      float x[VEC];
-      values(base + ln, x);
+      kept = take(base, sj, mem);
+      rows += kept;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) amax = fmaxf(amax, fabsf(x[i]));
+      for (int k = 0; k < kRopeBatch; ++k) {
+        if (k >= kept) break;
+        omin = min(omin, off[k]);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) amax = fmaxf(amax, fabsf(x[k][i]));
+      }
     }
     if (other) {
       end = base + lim;
@@ -351,50 +398,100 @@ __device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter,
     }
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, off));
-  float* sp = p.kv_scales + (blk * hkv + h) * 2 + pool;
-  const float s_old = omin == 0 ? 0.f : *sp;
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+  const float s_old = omin == 0 ? 0.f : stored;
   const float s_new = fmaxf(s_old, __fdiv_rn(amax, E5 ? 57344.f : 448.f));
   if (s_new > s_old && s_old > 0.f) {
     const float r = __fdiv_rn(s_old, s_new);
-    for (int o = 0; o < omin; ++o) {
-      float x[VEC];
-      load_codes<VEC, E5>(codes + o * D, x);
-      uint32_t c[VEC / 2];
+    constexpr int kAgain = 8;  // rows in flight
+    for (int o0 = 0; o0 < omin; o0 += kAgain) {
+      float y[kAgain][VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; i += 2) c[i / 2] = f32x2_to_fp8x2<E5>(__fmul_rn(x[i], r), __fmul_rn(x[i + 1], r));
-      store_codes<VEC>(codes + o * D, c);
+      for (int k = 0; k < kAgain; ++k) load_codes<VEC, E5>(codes + min(o0 + k, omin - 1) * D, y[k]);
+#pragma unroll
+      for (int k = 0; k < kAgain; ++k) {
+        uint32_t c[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+          c[i / 2] = f32x2_to_fp8x2<E5>(__fmul_rn(y[k][i], r), __fmul_rn(y[k][i + 1], r));
+        if (o0 + k < omin) store_codes<VEC>(codes + (o0 + k) * D, c);
+      }
     }
   }
-  for (int64_t base = t; base < end; base += 32) {
-    const int64_t sj = base + lane < end ? place(base + lane) : -1;
-    unsigned mem = __ballot_sync(kFull, sj >= 0);
-    while (mem) {
-      const int ln = __ffs(mem) - 1;
-      mem &= mem - 1;
-      const int64_t sm = __shfl_sync(kFull, sj, ln);
-      float x[VEC];
-      values(base + ln, x);
+  const Divisor div = divisor(s_new);
+  auto encode = [&](int n) {
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      if (k >= n) break;
       uint32_t c[VEC / 2];
 #pragma unroll
       for (int i = 0; i < VEC; i += 2)
-        c[i / 2] = s_new > 0.f ? f32x2_to_fp8x2<E5>(__fdiv_rn(x[i], s_new), __fdiv_rn(x[i + 1], s_new)) : 0u;
-      store_codes<VEC>(codes + (sm - blk * bs) * D, c);
+        c[i / 2] = s_new > 0.f ? f32x2_to_fp8x2<E5>(quotient(x[k][i], div), quotient(x[k][i + 1], div)) : 0u;
+      store_codes<VEC>(codes + off[k] * D, c);
+    }
+  };
+  if (rows == kept) {
+    encode(kept);
+  } else {
+    for (int64_t base = t; base < end; base += 32) {
+      const int64_t sj = base + lane < end ? rope_place(p, base + lane) : -1;
+      unsigned mem = __ballot_sync(kFull, sj >= 0);
+      while (mem) encode(take(base, sj, mem));
     }
   }
   if (lane == 0) *sp = s_new;
+}
+
+// A warp per (group of tokens, KV head, pool): the runs that start in the
+// group. A token starts a run if the nearest one before it that counts lies in
+// another block; lanes look at the 16 tokens before the group and at the
+// group's.
+template <typename T, int VEC, bool E5>
+__device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter, int64_t w) {
+  constexpr unsigned kFull = 0xffffffffu;
+  const int lane = threadIdx.x & 31, hkv = p.num_kv_heads, bs = p.block_size;
+  const int64_t g = w / (hkv * 2), t0 = g * p.group;
+  const int rem = (int)(w - g * hkv * 2), h = rem >> 1, pool = rem & 1;
+  const int64_t t = t0 - 16 + lane;
+  const bool mine = lane >= 16 && lane < 16 + p.group && t < p.num_tokens;
+  const int64_t slot = rope_place(p, t);
+  if (mine && slot < 0 && rem == 0) rope_row(p, t, p.slots[t], true);
+  const unsigned ok = __ballot_sync(kFull, slot >= 0);
+  const unsigned below = ok & ((1u << lane) - 1u);
+  const int64_t before = __shfl_sync(kFull, slot, below ? 31 - __clz(below) : 0);
+  unsigned starts = __ballot_sync(kFull, mine && slot >= 0 && (!below || before / bs != slot / bs));
+  const unsigned unsure = __ballot_sync(kFull, mine && slot >= 0 && !below && t0 > 16);
+  if (unsure) {
+    // Nothing but padding in the window: look further back.
+    const int ln = __ffs(unsure) - 1;
+    const int64_t blk = __shfl_sync(kFull, slot, ln) / bs;
+    for (int64_t base = t0 - 17; base >= 0; base -= 32) {
+      const int64_t sj = rope_place(p, base - lane);
+      const unsigned found = __ballot_sync(kFull, sj >= 0);
+      if (found) {
+        const int64_t near = __shfl_sync(kFull, sj, __ffs(found) - 1);  // lowest lane = latest token
+        if (near / bs == blk) starts &= ~(1u << ln);
+        break;
+      }
+    }
+  }
+  while (starts) {
+    const int ln = __ffs(starts) - 1;
+    starts &= starts - 1;
+    rope_run_8bit<T, VEC, E5>(p, inter, t0 - 16 + ln, __shfl_sync(kFull, slot, ln), h, pool);
+  }
 }
 
 template <typename T, int VEC, bool E5, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads) rope_8bit_kernel(const __grid_constant__ RopeParams p) {
   if (blockIdx.x >= p.q_ctas) {
     const int64_t w = (blockIdx.x - p.q_ctas) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    if (w < p.num_tokens * p.num_kv_heads * 2) rope_cache_8bit<T, VEC, E5>(p, LAYOUT == kRopePairs, w);
+    if (w < (p.num_tokens + p.group - 1) / p.group * p.num_kv_heads * 2)
+      rope_cache_8bit<T, VEC, E5>(p, LAYOUT == kRopePairs, w);
     return;
   }
-  const int64_t t = blockIdx.x / p.chunks;
-  const int unit = (int)(blockIdx.x - t * p.chunks) * kRopeThreads + threadIdx.x;
-  if (unit < p.num_q_heads * p.row_units) rope_unit<T, LAYOUT>(p, t, unit);
+  const unsigned t = blockIdx.x / p.chunks;
+  rope_token<T, LAYOUT>(p, t, blockIdx.x - t * p.chunks);
 }
 
 namespace {
@@ -406,7 +503,7 @@ int launch_rope(const RopeParams& p, int kv8, cudaStream_t stream) {
   if (!kv8) {
     rope_kernel<T, LAYOUT><<<(unsigned)(p.num_tokens * p.chunks), kRopeThreads, 0, stream>>>(p);
   } else {
-    const int64_t warps = p.num_tokens * p.num_kv_heads * 2;
+    const int64_t warps = (p.num_tokens + p.group - 1) / p.group * p.num_kv_heads * 2;
     const unsigned ctas = (unsigned)(p.q_ctas + (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
     const bool e5 = kv8 == 1 + PA_KV_E5M2;
     if (p.head_dim == 64 && e5) rope_8bit_kernel<T, 2, true, LAYOUT><<<ctas, kRopeThreads, 0, stream>>>(p);
@@ -468,16 +565,22 @@ int rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_str
   p.head_dim = head_dim;
   const int vec = 16 / size, half = rot_dim / 2;
   const int layout = interleaved ? kRopePairs : half % vec == 0 ? kRopeHalves : kRopeHalvesOdd;
-  p.row_units = layout == kRopePairs ? head_dim / vec
+  p.row_units = layout == kRopePairs    ? head_dim / vec
                 : layout == kRopeHalves ? (head_dim - half) / vec
                                         : head_dim - half;
-  const int64_t units = kv8 ? (int64_t)num_q_heads * p.row_units
-                            : (int64_t)(num_q_heads + num_kv_heads) * p.row_units + kv_row / vec;
-  if (units > (1 << 24)) return PA_ERR_UNSUPPORTED;
-  p.token_units = (int32_t)units;
-  p.chunks = std::max<int32_t>(1, (p.token_units + kRopeThreads - 1) / kRopeThreads);
+  p.rows = kv8 ? num_q_heads : num_q_heads + 2 * num_kv_heads;
+  if (num_q_heads > (1 << 20) || num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  p.pass_rows = std::max(1, kRopeThreads / p.row_units);
+  // CTAs of a token: one for each pass over its rows, as long as the machine
+  // has room for them all at once (16 an SM); then as few as fill it.
+  const int passes = std::max(1, (p.rows + p.pass_rows - 1) / p.pass_rows);
+  const int64_t room = 16 * num_sms_current_device();
+  p.chunks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(passes, room / num_tokens));
   p.q_ctas = num_q_heads > 0 ? num_tokens * p.chunks : 0;
-  if (num_tokens > (1ll << 31) / p.chunks - 1 || num_tokens * num_kv_heads > (1ll << 30)) return PA_ERR_UNSUPPORTED;
+  // Tokens of a warp (8-bit caches): more than one when that leaves each SM 32 warps.
+  const int64_t warps = num_tokens * num_kv_heads * 2;
+  p.group = (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, warps / (32 * num_sms_current_device())));
+  if (num_tokens > (1ll << 30) || num_tokens * num_kv_heads > (1ll << 30)) return PA_ERR_UNSUPPORTED;
   if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
 #define PA_ROPE(T)                                                       \
   (layout == kRopePairs    ? launch_rope<T, kRopePairs>(p, kv8, stream)  \
@@ -530,10 +633,12 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
     turns -= std::floor(turns);
     steps.step[i] = turns >= 1.0 ? 0 : (unsigned long long)(turns * 18446744073709551616.0);
   }
-  const int64_t total = num_positions * half;
-  const int64_t ctas = std::min<int64_t>((total + kRopeThreads - 1) / kRopeThreads, 1 << 24);
-  rope_table_kernel<<<(unsigned)ctas, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-      cos_sin, (uint32_t)first_position, num_positions, half, (float)amplitude, steps);
+  const int n = half % 4 == 0 ? 4 : 1, rows = kRopeThreads / (half / n);
+  // Four positions a thread, and no more CTAs than that takes.
+  const unsigned ctas = (unsigned)((num_positions + 4 * rows - 1) / (4 * rows));
+  const auto kernel = n == 4 ? rope_table_kernel<4> : rope_table_kernel<1>;
+  kernel<<<ctas, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      cos_sin, (uint32_t)first_position, (uint32_t)num_positions, half, (float)amplitude, steps);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

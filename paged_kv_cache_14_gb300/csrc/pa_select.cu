@@ -31,21 +31,21 @@ struct SummaryParams {
   float* scales;
   int32_t max_blocks_per_seq, num_seqs, max_new_tokens, num_blocks, block_size, num_kv_heads, head_dim;
   int32_t seq_blocks;  // blocks of a sequence that a call may summarise
-  int64_t items;
+  int64_t items;       // (sequence, block, KV head)
+  int32_t stages;      // tiles that a warp has on their way
   int* status;
 };
 
-constexpr int kSummaryThreads = 256;
+constexpr int kSummaryWarps = 8;
+constexpr int kSummaryThreads = 32 * kSummaryWarps;
 
-// A warp's item: the block to summarise, its rows and KV head; false if there
-// is nothing to do.
-__device__ __forceinline__ bool summary_item(const SummaryParams& p, int64_t item, bool report, int64_t& blk,
-                                             int& rows, int& head) {
-  head = (int)(item % p.num_kv_heads);
-  const int64_t rest = item / p.num_kv_heads;
-  const int seq = (int)(rest / p.seq_blocks), j = (int)(rest - (int64_t)seq * p.seq_blocks);
+// Item x of the call, a (block, KV head): whether there is anything to do, the
+// tile's number and its rows.
+__device__ __forceinline__ bool summary_item(const SummaryParams& p, int64_t x, int64_t& at, int& rows) {
+  const int item = (int)(x / p.num_kv_heads), head = (int)(x - (int64_t)item * p.num_kv_heads);
+  const int seq = item / p.seq_blocks, j = item - seq * p.seq_blocks;
   const int first = p.first_tokens[seq], len = p.seq_lens[seq];
-  report = report && head == 0;
+  const bool report = head == 0;
   if (first < 0 || len < first || len - first > p.max_new_tokens) {
     if (report && j == 0) record_error(p.status, PA_ERR_SEQLEN);
     return false;
@@ -57,11 +57,12 @@ __device__ __forceinline__ bool summary_item(const SummaryParams& p, int64_t ite
     if (report) record_error(p.status, PA_ERR_SEQLEN);
     return false;
   }
-  blk = p.block_tables[(int64_t)seq * p.max_blocks_per_seq + lb];
+  const int blk = p.block_tables[(int64_t)seq * p.max_blocks_per_seq + lb];
   if (blk < 0 || blk >= p.num_blocks) {
     if (report) record_error(p.status, PA_ERR_BLOCK_OOB);
     return false;
   }
+  at = (int64_t)blk * p.num_kv_heads + head;
   rows = min(p.block_size, len - lb * p.block_size);
   return true;
 }
@@ -71,11 +72,10 @@ __device__ __forceinline__ bool summary_item(const SummaryParams& p, int64_t ite
 __device__ __forceinline__ float summary_scale(float top) {
   return top <= 3.402823466e38f ? __fdiv_rn(top, 127.f) : __int_as_float(0x7f800000);
 }
-__device__ __forceinline__ int code_up(float x, float scale) {
-  return scale > 0.f && scale <= 3.402823466e38f ? (int)fminf(ceilf(__fdiv_rn(x, scale)), 127.f) : 0;
-}
-__device__ __forceinline__ int code_down(float x, float scale) {
-  return scale > 0.f && scale <= 3.402823466e38f ? (int)fmaxf(floorf(__fdiv_rn(x, scale)), -127.f) : 0;
+// ceil(x / scale), at most 127. The lower ends go through it with their signs
+// changed: floor(x / s) = -ceil(-x / s).
+__device__ __forceinline__ int code_up(float x, const Divisor& scale) {
+  return scale.by > 0.f && scale.by <= 3.402823466e38f ? (int)fminf(ceilf(quotient(x, scale)), 127.f) : 0;
 }
 // Maximum and minimum that keep a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -121,25 +121,19 @@ struct Bf16Range {
   }
 };
 
-// 16-bit rows, or 8-bit codes (KV8: 1 e4m3, 2 e5m2) widened to fp16. A warp
-// per (block, KV head): a lane takes 16 bytes of a row, RPP rows at a time.
+// 16-bit rows, or 8-bit codes (KV8: 1 e4m3, 2 e5m2) widened to fp16, of one
+// tile in shared memory: a lane takes 16 bytes of a row, RPP rows at a time.
 template <typename R, int D, int KV8>
-__global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const __grid_constant__ SummaryParams p) {
-  constexpr int E = KV8 ? 16 : 8;      // elements of a lane
-  constexpr int VPR = D / E;           // lanes of a row
-  constexpr int RPP = 32 / VPR;        // rows of a pass
-  constexpr int W = E / 2;             // packed pairs of a lane
-  constexpr int NR = 16 / RPP;         // passes of 16 rows
+__device__ __forceinline__ void summary_of(const SummaryParams& p, const uint8_t* tile, int64_t at, int rows,
+                                           float mul) {
+  constexpr int E = KV8 ? 16 : 8;  // elements of a lane
+  constexpr int VPR = D / E;       // lanes of a row
+  constexpr int RPP = 32 / VPR;    // rows of a pass
+  constexpr int W = E / 2;         // packed pairs of a lane
+  constexpr int NR = 16 / RPP;     // passes of 16 rows
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x * (int64_t)(kSummaryThreads / 32) + (threadIdx.x >> 5);
-  if (item >= p.items) return;
-  int64_t blk;
-  int rows, head;
-  if (!summary_item(p, item, lane == 0, blk, rows, head)) return;
-  const int64_t at = blk * p.num_kv_heads + head;
-  const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) + at * p.block_size * D * (KV8 ? 1 : 2) +
-                       (lane % VPR) * 16;
+  const uint8_t* src = tile + (lane % VPR) * 16;
   uint32_t hi[W], lo[W];
   bool started = false;
   for (int r0 = 0; r0 < rows; r0 += 16) {
@@ -167,55 +161,56 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const __grid_c
     }
     started = true;
   }
-#pragma unroll
-  for (int o = VPR; o < 32; o <<= 1) {
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      hi[j] = R::top(hi[j], __shfl_xor_sync(kAll, hi[j], o));
-      lo[j] = R::low(lo[j], __shfl_xor_sync(kAll, lo[j], o));
-    }
-  }
-  const float mul = KV8 ? p.kv_scales[at * 2] : 1.f;
-  float top = 0.f;
+  // The RPP lanes that hold the same elements share the rest: half of them
+  // take the upper ends, the others the lower (with their signs changed, so
+  // that both are maxima), and each a part of the words. What a lane gives
+  // away goes to the lane that keeps it.
+  const bool low = lane & 16;
 #pragma unroll
   for (int j = 0; j < W; ++j) {
-    const float2 a = R::wide(hi[j]), b = R::wide(lo[j]);
-    top = max_nan(top, max_nan(max_nan(fabsf(a.x), fabsf(a.y)), max_nan(fabsf(b.x), fabsf(b.y))));
+    const uint32_t l = lo[j] ^ 0x80008000u, keep = low ? l : hi[j];
+    hi[j] = R::top(keep, __shfl_xor_sync(kAll, low ? hi[j] : l, 16));
   }
+  int part = 0;  // first of the lane's words
 #pragma unroll
-  for (int o = 1; o < VPR; o <<= 1) top = max_nan(top, __shfl_xor_sync(kAll, top, o));
-  const float scale = summary_scale(KV8 ? fabsf(__fmul_rn(top, mul)) : top);
-  // The first lanes of a row's write the upper ends, the next ones the lower.
-  const int part = lane / VPR;
-  if (part < 2) {
-    uint32_t out[E / 4];
+  for (int o = 8, n = W / 2; o >= VPR; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+    part += up ? n : 0;
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      const float2 v = R::wide(part ? lo[j] : hi[j]);
-      const float x = KV8 ? __fmul_rn(v.x, mul) : v.x, y = KV8 ? __fmul_rn(v.y, mul) : v.y;
-      const int c0 = part ? code_down(x, scale) : code_up(x, scale);
-      const int c1 = part ? code_down(y, scale) : code_up(y, scale);
-      const uint32_t two = (c0 & 255) | (c1 & 255) << 8;
-      if (j & 1) out[j / 2] |= two << 16;
-      else out[j / 2] = two;
+    for (int j = 0; j < W / 2; ++j) {
+      if (j >= n) break;
+      const uint32_t keep = up ? hi[j + n] : hi[j];
+      hi[j] = R::top(keep, __shfl_xor_sync(kAll, up ? hi[j] : hi[j + n], o));
     }
-    int8_t* dst = p.summaries + (at * 2 + part) * D + (lane % VPR) * E;
-    if constexpr (KV8 != 0) *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   }
+  constexpr int C = 2 * E / RPP;  // elements that a lane has now: 8 or 4
+  uint32_t most = hi[0];
+#pragma unroll
+  for (int j = 1; j < C / 2; ++j) most = R::top(most, hi[j]);
+  const float2 two = R::wide(most);
+  float top = max_nan(two.x, two.y);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) top = max_nan(top, __shfl_xor_sync(kAll, top, o));
+  const float scale = summary_scale(KV8 ? __fmul_rn(top, mul) : top);
+  const Divisor div = divisor(scale);
+  uint32_t out[C / 4] = {};
+#pragma unroll
+  for (int j = 0; j < C / 2; ++j) {
+    const float2 v = R::wide(hi[j]);
+    int c0 = code_up(KV8 ? __fmul_rn(v.x, mul) : v.x, div), c1 = code_up(KV8 ? __fmul_rn(v.y, mul) : v.y, div);
+    if (low) c0 = -c0, c1 = -c1;
+    out[j / 2] |= ((c0 & 255) | (c1 & 255) << 8) << (j & 1) * 16;
+  }
+  int8_t* dst = p.summaries + (at * 2 + low) * D + (lane % VPR) * E + 2 * part;
+  if constexpr (C == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = out[0];
   if (lane == 0) p.scales[at] = scale;
 }
 
 // fp32 rows of 32 N elements, a lane taking every 32nd.
 template <int N>
-__global__ void __launch_bounds__(kSummaryThreads) summary_f32_kernel(const __grid_constant__ SummaryParams p) {
+__device__ __forceinline__ void summary_of_f32(const SummaryParams& p, int64_t at, int rows) {
   const int lane = threadIdx.x & 31;
-  const int64_t item = blockIdx.x * (int64_t)(kSummaryThreads / 32) + (threadIdx.x >> 5);
-  if (item >= p.items) return;
-  int64_t blk;
-  int rows, head;
-  if (!summary_item(p, item, lane == 0, blk, rows, head)) return;
-  const int64_t at = blk * p.num_kv_heads + head;
   const float* src = static_cast<const float*>(p.k_cache) + at * p.block_size * (32 * N) + lane;
   float hi[N], lo[N], top = 0.f;
 #pragma unroll
@@ -233,13 +228,90 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_f32_kernel(const __gr
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float scale = summary_scale(top);
+  const Divisor div = divisor(scale);
   int8_t* dst = p.summaries + at * 2 * (32 * N) + lane;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    dst[32 * i] = (int8_t)code_up(hi[i], scale);
-    dst[32 * N + 32 * i] = (int8_t)code_down(lo[i], scale);
+    dst[32 * i] = (int8_t)code_up(hi[i], div);
+    dst[32 * N + 32 * i] = (int8_t)-code_up(-lo[i], div);
   }
   if (lane == 0) p.scales[at] = scale;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+constexpr int kSummaryMaxStages = 8;
+
+// Each warp for itself: it finds 32 items at a time, a lane each, keeps the
+// next tiles on their way into shared memory and takes them in order.
+template <typename R, int D, int KV8>
+__global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const __grid_constant__ SummaryParams p) {
+  constexpr unsigned kAll = 0xffffffffu;
+  constexpr int RB = D * (KV8 ? 1 : 2);
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kSummaryWarps][kSummaryMaxStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile_bytes = p.block_size * RB;
+  uint8_t* ring = smem + warp * p.stages * tile_bytes;
+  if (lane == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  const int64_t step = (int64_t)gridDim.x * kSummaryWarps;
+  int put = 0, put_turn = 0, got = 0, got_turn = 0;  // stage and round of the next tile to ask for, to take
+  for (int64_t base = (int64_t)blockIdx.x * kSummaryWarps + warp; base < p.items; base += 32 * step) {
+    int64_t at = 0;
+    int rows = 0;
+    float mul = 1.f;
+    if (base + lane * step < p.items && summary_item(p, base + lane * step, at, rows)) {
+      if constexpr (KV8 != 0) mul = p.kv_scales[at * 2];
+    }
+    unsigned ask = __ballot_sync(kAll, rows > 0), take = ask;
+    auto next = [&] {
+      if (!ask) return;
+      const int l = __ffs(ask) - 1;
+      ask &= ask - 1;
+      if (lane == l) {
+        const uint32_t bar = smem_u32(&bars[warp][put]);
+        mbar_arrive_expect_tx(bar, rows * RB);
+        bulk_load(smem_u32(ring + put * tile_bytes), static_cast<const uint8_t*>(p.k_cache) + at * tile_bytes,
+                  rows * RB, bar);
+      }
+      if (++put == p.stages) put = 0, put_turn ^= 1;
+    };
+    for (int i = 0; i < p.stages; ++i) next();
+    while (take) {
+      const int l = __ffs(take) - 1;
+      take &= take - 1;
+      if (!__all_sync(kAll, mbar_wait(smem_u32(&bars[warp][got]), got_turn, p.status))) {
+        // Not in time: what is on its way still has to arrive.
+        for (; got != put || got_turn != put_turn;) {
+          mbar_wait(smem_u32(&bars[warp][got]), got_turn, p.status);
+          if (++got == p.stages) got = 0, got_turn ^= 1;
+        }
+        return;
+      }
+      summary_of<R, D, KV8>(p, ring + got * tile_bytes, __shfl_sync(kAll, at, l), __shfl_sync(kAll, rows, l),
+                            __shfl_sync(kAll, mul, l));
+      __syncwarp();  // the tile has been read
+      if (++got == p.stages) got = 0, got_turn ^= 1;
+      next();
+    }
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kSummaryThreads) summary_f32_kernel(const __grid_constant__ SummaryParams p) {
+  const int64_t step = (int64_t)gridDim.x * kSummaryWarps;
+  for (int64_t x = (int64_t)blockIdx.x * kSummaryWarps + (threadIdx.x >> 5); x < p.items; x += step) {
+    int64_t at;
+    int rows;
+    if (summary_item(p, x, at, rows)) summary_of_f32<N>(p, at, rows);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -259,10 +331,15 @@ struct SelectParams {
   int* status;
 };
 
-constexpr int kSelectThreads = 256;
+constexpr int kSelectThreads = 128;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectMaxCluster = 8;
-constexpr int kSelectTile = 16;  // blocks of one matrix product
+constexpr int kSelectTile = 16;       // blocks of one matrix product
+constexpr int kSelectStages = 3;      // tiles of a warp on their way
+constexpr int kDigit = 9;            // bits of a digit
+constexpr int kBins = 1 << kDigit;    // its values, a 32nd of them to a lane
+constexpr int kPasses = 4;            // digits of a score
+constexpr int kLaneBins = kBins / 32 + 4;  // a lane's bins are apart by 16 bytes more, in other banks
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -274,6 +351,32 @@ __device__ __forceinline__ int remote_int(const void* local, int rank) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+
+__device__ __forceinline__ uint2 remote_pair(const void* local, int rank) {
+  uint32_t a;
+  uint2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 remote_int4(const void* local, int rank) {
+  uint32_t a;
+  int4 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+// Shared memory of the tiles on their way, which the counts take over.
+constexpr int select_stages(int d) { return d <= 128 ? kSelectStages : 2; }
+constexpr int select_ring_bytes(int d) {
+  const int ring = kSelectWarps * select_stages(d) * (kSelectTile * 2 * d + kSelectTile * 4);
+  const int counts = (kPasses + 1) * 32 * kLaneBins * 4;
+  return ring > counts ? ring : counts;
+}
+__device__ __forceinline__ int bin_at(uint32_t digit) { return digit + digit / (kBins / 32) * 4; }
 
 // Scores as unsigned numbers of the same order.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -292,49 +395,39 @@ __device__ __forceinline__ void s8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(bias));
 }
 
-// Exclusive prefix sum over the CTA's threads; `scratch` is kSelectWarps + 1
-// ints. Contains barriers.
-__device__ __forceinline__ int select_scan(int v, int* scratch, int& total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) scratch[w] = x;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kSelectWarps; ++i) {
-    const int s = scratch[i];
-    before += i < w ? s : 0;
-    total += s;
-  }
-  return before + x - v;
-}
-
-// One cluster per (sequence, KV head). Its CTAs split the row's blocks, score
-// them 16 at a time on the tensor cores (codes up to 127 are exact in fp16,
-// their products' sums exact in fp32), keep the scores in shared memory, and
-// find the score of the last block to take by counting digits of 8 bits from
-// the top, a cluster-wide histogram each.
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectParams p) {
+// One cluster (with CL; else one CTA) per (sequence, KV head). Its CTAs split
+// the row's blocks, score them 16 at a time on the tensor cores (codes up to
+// 127 are exact in fp16, their products' sums exact in fp32) and keep the
+// scores in shared memory. The score of the last block to take is found by
+// counting: digits of 10 bits from the top of the range that the row's scores
+// span, so that the first splits them well whatever their size, and the
+// search ends when a digit's blocks are all taken (after two digits, mostly).
+//
+// The summaries come by asynchronous copies, kSelectStages tiles ahead of
+// each warp: 16 blocks' rows as they lie, but for the halves of 128 bytes of
+// every other row, which change places so that a fragment's rows take all
+// banks. (One tile ahead in registers took twice as long: a warp then waits
+// for memory once a tile.)
+template <typename T, int D, bool CL>
+__global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kernel(const __grid_constant__ SelectParams p) {
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int Q2 = 2 * D + 4;  // fp16 of a query row in shared memory: 8 bytes on, so that rows take other banks
+  constexpr int kRow = 2 * D, kPieces = kRow / 16, kTile = kSelectTile * kRow + kSelectTile * 4;
+  constexpr bool kSwap = kRow % 128 == 0;  // (other rows start 64 bytes apart by themselves)
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int hist[4][256];
-  __shared__ int scratch[kSelectWarps];
-  __shared__ int range[2], totals[2], found[3];
-  __half* qs = reinterpret_cast<__half*>(smem);
-  float* q_scale = reinterpret_cast<float*>(smem + p.head_tiles * 8 * Q2 * 2);
+  __shared__ uint32_t scratch[kSelectWarps], total;
+  __shared__ __align__(8) uint32_t range[2];
+  // The tiles' ring, later the counts; the queries; the scores.
+  int(*hist)[32 * kLaneBins] = reinterpret_cast<int(*)[32 * kLaneBins]>(smem);
+  int* sum = hist[kPasses];
+  __half* qs = reinterpret_cast<__half*>(smem + select_ring_bytes(D));
+  float* q_scale = reinterpret_cast<float*>(qs + p.head_tiles * 8 * Q2);
   uint32_t* keys = reinterpret_cast<uint32_t*>(q_scale + p.head_tiles * 8);
-  int ranks, rank;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  int ranks = 1, rank = 0;
+  if constexpr (CL) {
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  }
   const int row = blockIdx.x / ranks, seq = row / p.num_kv_heads, head = row - seq * p.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   int32_t* list = p.lists + (int64_t)row * p.max_list_len;
@@ -351,15 +444,61 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     if (rank == 0 && tid == 0) p.list_lens[row] = nb;
     return;
   }
-  for (int i = tid; i < 4 * 256; i += kSelectThreads) (&hist[0][0])[i] = 0;
+  const int sink = p.num_sink, some = nb - sink - p.num_recent;  // blocks that compete
+  int need = p.max_list_len - sink - p.num_recent;               // of which so many are taken
+  const int chunk = ((some + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile;
+  const int lo = min(rank * chunk, some), mine = min(chunk, some - lo);
+
+  // Lane i < 16 finds block i of a tile (behind the end: the last block).
+  constexpr int kStep = kSelectWarps * kSelectTile, kStages = select_stages(D);
+  auto find = [&](int b0) -> int32_t {
+    return lane < kSelectTile && b0 < mine ? table[sink + lo + min(b0 + lane, mine - 1)] : 0;
+  };
+  uint8_t* ring = smem + warp * kStages * kTile;
+  auto fetch = [&](int b0, int stage, int32_t id) {
+    if (b0 < mine) {
+      const bool there = id >= 0 && id < p.num_blocks;
+      const int32_t blk = there ? id : 0;
+      const uint32_t to = smem_u32(ring + stage * kTile);
+#pragma unroll
+      for (int i = 0; i < kSelectTile * kPieces / 32; ++i) {
+        const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
+        const int64_t at = (int64_t)__shfl_sync(kAll, blk, row) * p.num_kv_heads + head;
+        copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
+                     p.summaries + at * kRow + piece * 16);
+      }
+      if (lane < kSelectTile) {
+        const uint32_t s = to + kSelectTile * kRow + lane * 4;
+        if (there) {
+          copy_async4(s, p.scales + (int64_t)blk * p.num_kv_heads + head);
+        } else {  // a mark that no scale has
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s), "r"(0xffc00001u) : "memory");
+          if (b0 + lane < mine) record_error(p.status, PA_ERR_BLOCK_OOB);
+        }
+      }
+    }
+    copy_async_commit();
+  };
+  int32_t id = find(warp * kSelectTile);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    const int b0 = warp * kSelectTile + i * kStep;
+    const int32_t next = find(b0 + kStep);
+    fetch(b0, i, id);
+    id = next;
+  }
+  if (tid == 0) {
+    range[0] = 0xffffffffu;
+    range[1] = 0;
+  }
   // The queries' codes, their positive and their negative part.
   for (int h = warp; h < p.head_tiles * 8; h += kSelectWarps) {
     float x[D / 32], top = 0.f;
-    const bool there = h < p.group;
-    const T* q = static_cast<const T*>(p.q) + ((int64_t)seq * p.num_q_heads + head * p.group + (there ? h : 0)) * D;
+    const bool real = h < p.group;
+    const T* q = static_cast<const T*>(p.q) + ((int64_t)seq * p.num_q_heads + head * p.group + (real ? h : 0)) * D;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      x[i] = there ? to_f32(q[lane + 32 * i]) : 0.f;
+      x[i] = real ? to_f32(q[lane + 32 * i]) : 0.f;
       top = fabsf(x[i]) <= 3.402823466e38f ? fmaxf(top, fabsf(x[i])) : __int_as_float(0x7f800000);
     }
 #pragma unroll
@@ -375,35 +514,33 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     if (lane == 0) q_scale[h] = scale;
   }
   __syncthreads();
-  const int sink = p.num_sink, some = nb - sink - p.num_recent;  // blocks that compete
-  int need = p.max_list_len - sink - p.num_recent;               // of which so many are taken
-  const int chunk = ((some + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile;
-  const int lo = min(rank * chunk, some), mine = min(chunk, some - lo);
+
   uint32_t kmin = 0xffffffffu, kmax = 0;
-  for (int b0 = warp * kSelectTile; b0 < mine; b0 += kSelectWarps * kSelectTile) {
-    // Lane (r, c) reads 16 bytes of each 64 of the rows of blocks r and r + 8.
-    uint4 a[2][D / 32];
-    float mul[2];
-    bool ok[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int b = b0 + r + 8 * i;
-      const int32_t blk = b < mine ? table[sink + lo + b] : 0;
-      ok[i] = blk >= 0 && blk < p.num_blocks;
-      const int64_t at = (int64_t)(ok[i] ? blk : 0) * p.num_kv_heads + head;
-      mul[i] = p.scales[at];
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        a[i][j] = *reinterpret_cast<const uint4*>(p.summaries + at * 2 * D + 64 * j + 16 * c);
+  int stage = 0;
+  for (int b0 = warp * kSelectTile; b0 < mine; b0 += kStep) {
+    {
+      const int ahead = b0 + (kStages - 1) * kStep;
+      const int32_t next = find(ahead + kStep);
+      fetch(ahead, stage == 0 ? kStages - 1 : stage - 1, id);
+      id = next;
     }
+    copy_async_wait<kStages - 1>();
+    __syncwarp();
+    // Lane (r, c): 16 bytes of each 64 of the rows of blocks r and r + 8.
+    const uint8_t* tile = ring + stage * kTile;
+    const uint8_t* at = tile + r * kRow;
+    const int swap = kSwap ? (r & 1) << 2 : 0;
     float best[2] = {__int_as_float(0xff800000), __int_as_float(0xff800000)};
     for (int n = 0; n < p.head_tiles; ++n) {
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       const __half* qn = qs + (n * 8 + r) * Q2 + 16 * c;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        const uint32_t w0[4] = {a[0][j].x, a[0][j].y, a[0][j].z, a[0][j].w};
-        const uint32_t w1[4] = {a[1][j].x, a[1][j].y, a[1][j].z, a[1][j].w};
+        const int piece = (4 * j + c ^ swap) * 16;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(at + piece);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(at + 8 * kRow + piece);
+        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
+        const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t f[4];
@@ -428,88 +565,143 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
       best[i] = fmaxf(best[i], __shfl_xor_sync(kAll, best[i], 2));
       const int b = b0 + r + 8 * i;
       if (c == 0 && b < mine) {
-        // A block with keys that are not finite comes before all others.
-        // (Scale 0: all its keys are 0, whatever else overflows.)
-        uint32_t key = !(mul[i] <= 3.402823466e38f) ? 0xff800000u
-                                                    : ordered(mul[i] == 0.f ? 0.f : __fmul_rn(best[i], mul[i]));
-        if (!ok[i]) {
-          record_error(p.status, PA_ERR_BLOCK_OOB);
-          key = 0;
-        }
+        // A block with keys that are not finite comes before all others, one
+        // outside the pool behind. (Scale 0: all its keys are 0, whatever
+        // else overflows.)
+        const float scale = reinterpret_cast<const float*>(tile + kSelectTile * kRow)[r + 8 * i];
+        const uint32_t key = __float_as_uint(scale) == 0xffc00001u ? 0u
+                             : !(scale <= 3.402823466e38f)         ? 0xff800000u
+                                                           : ordered(scale == 0.f ? 0.f : __fmul_rn(best[i], scale));
         keys[b] = key;
         kmin = min(kmin, key);
         kmax = max(kmax, key);
       }
     }
+    __syncwarp();  // the tile has been read
+    if (++stage == kStages) stage = 0;
   }
-  // The row's range: digits are counted of key - kmin, from its top bit down.
-  if (tid == 0) {
-    range[0] = (int)0xffffffffu;
-    range[1] = 0;
-  }
+  copy_async_wait<0>();
   __syncthreads();
+  for (int i = tid; i < kPasses * 32 * kLaneBins / 4; i += kSelectThreads)
+    reinterpret_cast<int4*>(smem)[i] = make_int4(0, 0, 0, 0);
   kmin = __reduce_min_sync(kAll, kmin);
   kmax = __reduce_max_sync(kAll, kmax);
   if (lane == 0) {
-    atomicMin(reinterpret_cast<uint32_t*>(&range[0]), kmin);
-    atomicMax(reinterpret_cast<uint32_t*>(&range[1]), kmax);
+    atomicMin(&range[0], kmin);
+    atomicMax(&range[1], kmax);
   }
-  cluster_sync_all();
-  for (int i = 0; i < ranks; ++i) {
-    kmin = min(kmin, (uint32_t)remote_int(&range[0], i));
-    kmax = max(kmax, (uint32_t)remote_int(&range[1], i));
+  if constexpr (CL) {
+    cluster_sync_all();
+    const uint2 x = remote_pair(range, lane % ranks);
+    kmin = __reduce_min_sync(kAll, x.x);
+    kmax = __reduce_max_sync(kAll, x.y);
+  } else {
+    __syncthreads();
+    kmin = range[0];
+    kmax = range[1];
   }
-  // Keys from `base` on are still in question; those above `over` are taken.
+  // Keys from `base` to base + width are in question; those above are taken.
   int bits = 32 - __clz(kmax - kmin);
-  uint32_t base = kmin, width = kmax - kmin;  // keys base .. base + width
+  uint32_t base = kmin, width = kmax - kmin;
   int pass = 0;
   bool whole = false;  // all keys in question are taken
   while (need > 0 && bits > 0 && !whole) {
-    const int shift = max(bits - 8, 0);
+    const int shift = max(bits - kDigit, 0);
     for (int i = tid; i < mine; i += kSelectThreads) {
-      const uint32_t x = keys[i] - base;
-      if (keys[i] >= base && x <= width) atomicAdd(&hist[pass][x >> shift], 1);
+      const uint32_t key = keys[i];
+      if (key >= base && key - base <= width) atomicAdd(&hist[pass][bin_at((key - base) >> shift)], 1);
     }
-    cluster_sync_all();
-    // Thread t counts digit 255 - t; the first digits from the top that make
-    // up `need` end in the one looked for.
-    int count = 0, total;
-    for (int i = 0; i < ranks; ++i) count += remote_int(&hist[pass][255 - tid], i);
-    const int above = select_scan(count, scratch, total);
-    if (above < need && above + count >= need) {
-      found[0] = 255 - tid;
-      found[1] = above;
-      found[2] = count;
+    const int* bins = hist[pass];
+    if constexpr (CL) {
+      cluster_sync_all();
+      // (A thread has four digits' counts, all CTAs' at once.)
+      static_assert(kBins == 4 * kSelectThreads, "");
+      int4 x[kSelectMaxCluster];
+#pragma unroll
+      for (int j = 0; j < kSelectMaxCluster; ++j)
+        x[j] = j < ranks ? remote_int4(&hist[pass][bin_at(4 * tid)], j) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 1; j < kSelectMaxCluster; ++j) {
+        x[0].x += x[j].x;
+        x[0].y += x[j].y;
+        x[0].z += x[j].z;
+        x[0].w += x[j].w;
+      }
+      *reinterpret_cast<int4*>(&sum[bin_at(4 * tid)]) = x[0];
+      bins = sum;
     }
     __syncthreads();
-    need -= found[1];
-    base += (uint32_t)found[0] << shift;
+    // Every warp counts for itself: lane 31 has the lowest digits, and the
+    // lanes' sums from the top tell whose digit makes up `need`.
+    int v[kBins / 32], count = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / 128; ++i) {
+      const int4 x = *reinterpret_cast<const int4*>(bins + (31 - lane) * kLaneBins + 4 * i);
+      v[4 * i] = x.x;
+      v[4 * i + 1] = x.y;
+      v[4 * i + 2] = x.z;
+      v[4 * i + 3] = x.w;
+      count += x.x + x.y + x.z + x.w;
+    }
+    int above = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, above, o);
+      if (lane >= o) above += y;
+    }
+    const int who = __ffs(__ballot_sync(kAll, above >= need)) - 1;
+    above -= count;
+    int digit = 0, here = 0;
+#pragma unroll
+    for (int i = kBins / 32 - 1; i >= 0; --i) {  // from the top to the first that makes up `need`
+      if (above + here < need) {
+        above += here;
+        here = v[i];
+        digit = i;
+      }
+    }
+    digit = __shfl_sync(kAll, (31 - lane) * (kBins / 32) + digit, who);
+    need -= __shfl_sync(kAll, above, who);
+    here = __shfl_sync(kAll, here, who);
+    base += (uint32_t)digit << shift;
     width = min((1u << shift) - 1u, kmax - base);
-    whole = need == found[2];
+    whole = need == here;
     bits = shift;
     ++pass;
-    __syncthreads();
+    if constexpr (CL) __syncthreads();  // `sum` is read
   }
   // Taken: keys above base + width, those of [base, base + width] if `whole`,
   // or else (all equal then) the first `need` of them.
   const uint32_t over = base + width;
   const int seg = (mine + kSelectThreads - 1) / kSelectThreads | 1;  // odd: other banks
   const int s0 = min(tid * seg, mine), s1 = min(s0 + seg, mine);
-  int more = 0, same = 0;
-  for (int i = s0; i < s1; ++i) {
-    more += keys[i] > over;
-    same += keys[i] >= base && keys[i] <= over;
+  // Taken for certain, and in question (upper half), in the segments before.
+  uint32_t before = 0;
+  for (int i = s0; i < s1; ++i) before += keys[i] > over ? 1u : keys[i] >= base ? 1u << 16 : 0u;
+  {
+    const uint32_t own = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, before, o);
+      if (lane >= o) before += y;
+    }
+    if (lane == 31) scratch[warp] = before;
+    before -= own;
   }
-  int all_more, all_same;
-  int more_before = select_scan(more, scratch, all_more), same_before = select_scan(same, scratch, all_same);
-  if (tid == 0) {
-    totals[0] = all_more;
-    totals[1] = all_same;
+  __syncthreads();
+  uint32_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kSelectWarps; ++i) {
+    before += i < warp ? scratch[i] : 0u;
+    all += scratch[i];
   }
-  cluster_sync_all();
-  for (int i = 0; i < rank; ++i) {
-    more_before += remote_int(&totals[0], i);
-    same_before += remote_int(&totals[1], i);
+  int more_before = before & 0xffff, same_before = before >> 16;
+  if constexpr (CL) {
+    if (tid == 0) total = all;
+    cluster_sync_all();
+    const uint32_t x = lane < rank ? remote_int(&total, lane) : 0u;
+    more_before += __reduce_add_sync(kAll, x & 0xffff);
+    same_before += __reduce_add_sync(kAll, x >> 16);
   }
   int out = sink + more_before + min(same_before, need);
   for (int i = s0; i < s1; ++i) {
@@ -523,7 +715,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
       list[p.max_list_len - p.num_recent + i] = nb - p.num_recent + i;
     if (tid == 0) p.list_lens[row] = p.max_list_len;
   }
-  cluster_sync_all();  // no CTA leaves while another reads its totals
+  if constexpr (CL) cluster_sync_all();  // no CTA leaves while another reads its totals
 }
 
 namespace {
@@ -535,18 +727,18 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   SelectParams p = p0;
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
   const int blocks = (p.max_seq_len - 1) / p.block_size + 1;
-  // CTAs of a row: as many as keep the batch within three per SM and leave
-  // each 128 blocks.
+  // CTAs of a row: as many as keep the batch within four per SM and leave
+  // each 64 blocks.
   int ranks = 1;
-  while (ranks < kSelectMaxCluster && rows * ranks * 2 <= 3 * num_sms_current_device() && blocks >= ranks * 2 * 128)
+  while (ranks < kSelectMaxCluster && rows * ranks * 2 <= 4 * num_sms_current_device() && blocks >= ranks * 2 * 64)
     ranks *= 2;
-  const int fixed = p.head_tiles * 8 * ((2 * D + 4) * 2 + 4), most = 200 * 1024;
+  const int fixed = select_ring_bytes(D) + p.head_tiles * 8 * ((2 * D + 4) * 2 + 4), most = 220 * 1024;
   auto bytes = [&] { return fixed + (((blocks + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile) * 4; };
   while (ranks < kSelectMaxCluster && bytes() > most) ranks *= 2;
   const int smem = bytes();
   if (smem > most) return PA_ERR_UNSUPPORTED;
-  const auto kernel = select_kernel<T, D>;
-  if (smem > 32 * 1024 && set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), most) != PA_OK)
+  const auto kernel = ranks > 1 ? select_kernel<T, D, true> : select_kernel<T, D, false>;
+  if (smem > 47 * 1024 && set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), most) != PA_OK)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * ranks));
@@ -598,23 +790,25 @@ int block_summaries(const void* k_cache, const float* kv_scales, const int32_t* 
   // New tokens may start at the end of a block; a sequence has no more blocks than its table.
   p.seq_blocks = (int32_t)std::min<int64_t>(((int64_t)max_new_tokens + block_size - 2) / block_size + 1,
                                             (int64_t)max_blocks_per_seq + 1);
+  if ((int64_t)num_seqs * p.seq_blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
   p.items = (int64_t)num_seqs * p.seq_blocks * num_kv_heads;
-  const int64_t ctas = (p.items + kSummaryThreads / 32 - 1) / (kSummaryThreads / 32);
-  if (ctas > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
-  const unsigned n = (unsigned)ctas;
-#define PA_SUM(R, KV8)                                                                       \
-  (head_dim == 64 ? (summary_kernel<R, 64, KV8><<<n, kSummaryThreads, 0, stream>>>(p), 0)    \
-                  : (summary_kernel<R, 128, KV8><<<n, kSummaryThreads, 0, stream>>>(p), 0))
-  if (kv8 == 1 + PA_KV_E4M3) {
-    PA_SUM(HalfRange, 1);
-  } else if (kv8) {
-    PA_SUM(HalfRange, 2);
-  } else if (dtype == PA_F16) {
-    PA_SUM(HalfRange, 0);
-  } else if (dtype == PA_BF16) {
-    PA_SUM(Bf16Range, 0);
-  } else {
+  // Three CTAs an SM, with 64 KB of tiles each.
+  const int tile = block_size * head_dim * (kv8 ? 1 : 2);
+  p.stages = std::max(2, std::min(kSummaryMaxStages, 64 * 1024 / (kSummaryWarps * tile)));
+  const int smem = kSummaryWarps * p.stages * tile;
+  const unsigned n = (unsigned)std::min<int64_t>((p.items + kSummaryWarps - 1) / kSummaryWarps,
+                                                 (wide ? 8 : 3) * num_sms_current_device());
+#define PA_SUM_D(R, D, KV8)                                                                                  \
+  {                                                                                                          \
+    const auto kernel = summary_kernel<R, D, KV8>;                                                           \
+    if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), 128 * 1024) != PA_OK) return PA_ERR_CUDA;\
+    kernel<<<n, kSummaryThreads, smem, stream>>>(p);                                                         \
+  }
+#define PA_SUM(R, KV8)                        \
+  if (head_dim == 64) PA_SUM_D(R, 64, KV8)    \
+  else PA_SUM_D(R, 128, KV8)
+  if (wide) {
     switch (head_dim / 32) {
       case 1: summary_f32_kernel<1><<<n, kSummaryThreads, 0, stream>>>(p); break;
       case 2: summary_f32_kernel<2><<<n, kSummaryThreads, 0, stream>>>(p); break;
@@ -625,7 +819,16 @@ int block_summaries(const void* k_cache, const float* kv_scales, const int32_t* 
       case 7: summary_f32_kernel<7><<<n, kSummaryThreads, 0, stream>>>(p); break;
       default: summary_f32_kernel<8><<<n, kSummaryThreads, 0, stream>>>(p); break;
     }
+  } else if (kv8 == 1 + PA_KV_E4M3) {
+    PA_SUM(HalfRange, 1)
+  } else if (kv8) {
+    PA_SUM(HalfRange, 2)
+  } else if (dtype == PA_F16) {
+    PA_SUM(HalfRange, 0)
+  } else {
+    PA_SUM(Bf16Range, 0)
   }
+#undef PA_SUM_D
 #undef PA_SUM
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

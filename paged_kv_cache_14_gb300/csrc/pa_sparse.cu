@@ -3,10 +3,10 @@
 //
 // The bytes of the listed K and V rows bound it: a block's keys meet the
 // query heads of one group only (4 G operations for 2 x 2 bytes). One cluster
-// works on a (sequence, KV head), its warps on 16 tokens at a time. A warp
-// loads them straight into the fragments of its matrix products, 16 bytes a
-// lane, which the products' free order of k (the head's dimensions) and of m
-// (the output's) allows:
+// works on a (sequence, KV head), its warps on 16 tokens at a time. Asynchronous
+// copies bring the next tiles into each warp's part of shared memory, and
+// fragments are read from there 16 bytes a lane, which the products' free order
+// of k (the head's dimensions) and of m (the output's) allows:
 //   scores S[16 tokens][8 heads] = K q^T, lane (r, c) holding 8 dimensions
 //     from 32 j + 8 c on of tokens r and r + 8;
 //   output O^T[D][8 heads] += V^T P^T, lane (r, c) holding 8 dimensions from
@@ -46,6 +46,8 @@ struct SparseParams {
 constexpr int kSparseWarps = 4;
 constexpr int kSparseThreads = kSparseWarps * 32;
 constexpr int kSparseMaxCluster = 8;
+// Tiles (K and V) of a warp in shared memory, the one in use among them.
+constexpr int sparse_stages(int tile_bytes) { return tile_bytes >= 4096 ? 2 : 4; }
 constexpr float kMoveAt = 8.f;  // log2 of the weight that moves the reference
 
 namespace {
@@ -164,15 +166,16 @@ __device__ __forceinline__ void sparse_join(const SparseParams& p, const SparseR
 // back; a block's V scale multiplies the block's product, so that no weight
 // carries it). NT: tiles of 8 query heads.
 template <typename T, int KV8, int D, int NT>
-__global__ void __launch_bounds__(kSparseThreads) sparse_kernel(const __grid_constant__ SparseParams p) {
+__global__ void __launch_bounds__(kSparseThreads, NT == 1 ? 3 : 2) sparse_kernel(const __grid_constant__ SparseParams p) {
   using M = typename std::conditional<KV8 != 0, __half, T>::type;  // the products' type
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int H = 8 * NT;
-  constexpr int KP = KV8 ? D / 64 : D / 32;  // 16-byte pieces of a K row for a lane
-  constexpr int VP = KV8 ? D / 128 : D / 64; // 16-byte pieces of a V row for a lane
-  constexpr int MT = D / 16;                 // tiles of 16 output dimensions
-  constexpr int KS = D / 16;                 // steps of the score product
-  __shared__ __align__(16) float so[kSparseWarps][H][D];
+  constexpr int KP = KV8 ? D / 64 : D / 32;   // 16-byte pieces of a K row for a lane
+  constexpr int VP = KV8 ? D / 128 : D / 64;  // 16-byte pieces of a V row for a lane
+  constexpr int MT = D / 16;                  // tiles of 16 output dimensions
+  constexpr int KS = D / 16;                  // steps of the score product
+  extern __shared__ __align__(16) uint8_t smem[];  // the warps' tiles, later their outputs
+  float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
   __shared__ float sm[kSparseWarps][H], sl[kSparseWarps][H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   const SparseRow w = sparse_row(p, H);
@@ -244,9 +247,9 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_kernel(const __grid_con
   }
 
   const int warps = w.ranks * kSparseWarps, me = w.rank * kSparseWarps + warp, items = w.entries * halves;
-  const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache);
-  const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache);
   constexpr int RB = KV8 ? D : 2 * D;  // bytes of a row
+  constexpr int kTile = 16 * RB, kStages = sparse_stages(kTile);
+  uint8_t* ring = smem + warp * kStages * 2 * kTile;
   for (int base = me; base < items; base += 32 * warps) {
     // 32 items ahead, one a lane.
     const int mine = base + lane * warps;
@@ -262,33 +265,48 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_kernel(const __grid_con
       }
     }
     const int count = min(32, (items - base + warps - 1) / warps);
+    // Item x's K and V rows into a stage (rows behind its last: that row once
+    // more; an item without tokens: the pool's first row, which weighs nothing).
+    // The 16-byte pieces of a row change places by its number, so that those
+    // that eight lanes read together lie in different banks.
+    auto fetch = [&](int x, int stage) {
+      if (x < count) {
+        const int blk = __shfl_sync(kAll, it.x, x), last = max(__shfl_sync(kAll, it.y, x) - 1, 0);
+        const int sub = halves == 2 ? (base + x * warps) & 1 : 0;
+        const int64_t at = (((int64_t)blk * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * RB;
+        const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + at;
+        const uint8_t* vc = static_cast<const uint8_t*>(p.v_cache) + at;
+        const uint32_t to = smem_u32(ring + stage * 2 * kTile);
+#pragma unroll
+        for (int i = 0; i < kTile / 512; ++i) {
+          const int y = i * 32 + lane, row = y / (RB / 16), piece = y % (RB / 16), from = min(row, last) * RB + piece * 16;
+          copy_async16(to + row * RB + (piece ^ (row & 1) << 2) * 16, kc + from);
+          copy_async16(to + kTile + row * RB + (piece ^ (row & 6)) * 16, vc + from);
+        }
+      }
+      copy_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+    int stage = 0;
     for (int x = 0; x < count; ++x) {
-      const int blk = __shfl_sync(kAll, it.x, x), n_tok = __shfl_sync(kAll, it.y, x);
+      fetch(x + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      copy_async_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* kt = ring + stage * 2 * kTile + r * RB;
+      const uint8_t* vt = ring + stage * 2 * kTile + kTile + 2 * c * RB;
+      const int n_tok = __shfl_sync(kAll, it.y, x);
       const float k_scale = KV8 ? __shfl_sync(kAll, ks, x) : 1.f, v_scale = KV8 ? __shfl_sync(kAll, vs, x) : 1.f;
-      if (n_tok == 0) continue;
-      const int sub = halves == 2 ? (base + x * warps) & 1 : 0;
-      const int64_t at = (((int64_t)blk * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * RB;
-      const int last = n_tok - 1;
-      uint4 kr[2][KP], vr[4][VP];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < KP; ++j)
-          kr[i][j] = *reinterpret_cast<const uint4*>(kc + at + min(r + 8 * i, last) * RB + 64 * j + 16 * c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < VP; ++j)
-          vr[i][j] = *reinterpret_cast<const uint4*>(vc + at + min(2 * c + (i & 1) + 8 * (i >> 1), last) * RB +
-                                                     128 * j + 16 * r);
       // Scores.
       float s[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < KP; ++j) {
-        const uint32_t a0[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
-        const uint32_t a1[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
+        const int piece = (4 * j + c ^ (r & 1) << 2) * 16;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(kt + piece);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(kt + 8 * RB + piece);
+        const uint32_t a0[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
         if constexpr (KV8 == 0) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -360,7 +378,8 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_kernel(const __grid_con
         const bool there = 2 * c + (i & 1) + 8 * (i >> 1) < n_tok;
 #pragma unroll
         for (int j = 0; j < VP; ++j) {
-          const uint32_t x4[4] = {vr[i][j].x, vr[i][j].y, vr[i][j].z, vr[i][j].w};
+          const uint4 y = *reinterpret_cast<const uint4*>(vt + ((i & 1) + 8 * (i >> 1)) * RB + (8 * j + r ^ 2 * c) * 16);
+          const uint32_t x4[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t word = there ? x4[k] : 0u;
@@ -389,12 +408,16 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_kernel(const __grid_con
           }
         }
       }
+      __syncwarp();  // the tiles have been read
+      if (++stage == kStages) stage = 0;
     }
   }
 
   // Join the warps. Element e of a lane's list is dimension e of 16-byte
   // piece e / per, `per` elements each, its pieces 8 lanes apart.
   constexpr int PER = KV8 ? 16 : 8;
+  copy_async_wait<0>();
+  __syncthreads();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -447,8 +470,8 @@ template <int D>
 __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid_constant__ SparseParams p) {
   constexpr int H = 8, TOK = 16, ST = D + 4;
   constexpr int DT = (D + kSparseThreads - 1) / kSparseThreads;  // dimensions of a thread
-  extern __shared__ __align__(16) float sh[];
-  float* so = sh;                  // [H][D]
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* so = reinterpret_cast<float*>(smem);  // [H][D]
   float* sq = so + H * D;          // [H][ST]
   float* sk = sq + H * ST;         // [TOK][ST]
   float* sv = sk + TOK * ST;       // [TOK][D]
@@ -548,10 +571,10 @@ int launch_sparse(void (*kernel)(SparseParams), const SparseParams& p, int smem,
                   cudaStream_t stream) {
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
   const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
-  // CTAs of a row: as many as keep the batch within three per SM and leave
+  // CTAs of a row: as many as keep the batch within four per SM and leave
   // each enough items.
   int ranks = 1;
-  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 3 * num_sms_current_device() &&
+  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 4 * num_sms_current_device() &&
          items >= (int64_t)ranks * 2 * items_per_cta)
     ranks *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -579,8 +602,11 @@ int launch_sparse_f32(const SparseParams& p, cudaStream_t stream) {
 
 template <typename T, int KV8, int D>
 int launch_sparse_tc(const SparseParams& p, cudaStream_t stream) {
-  return p.group <= 8 ? launch_sparse(sparse_kernel<T, KV8, D, 1>, p, 0, 2 * kSparseWarps, stream)
-                      : launch_sparse(sparse_kernel<T, KV8, D, 2>, p, 0, 2 * kSparseWarps, stream);
+  constexpr int tile = 16 * D * (KV8 ? 1 : 2), smem = kSparseWarps * sparse_stages(tile) * 2 * tile;
+  static_assert(smem >= kSparseWarps * 16 * D * 4, "the outputs fit into the tiles");
+  const auto kernel = p.group <= 8 ? sparse_kernel<T, KV8, D, 1> : sparse_kernel<T, KV8, D, 2>;
+  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem) != PA_OK) return PA_ERR_CUDA;
+  return launch_sparse(kernel, p, smem, 2 * kSparseWarps, stream);
 }
 
 // kv8: 0, or 1 + the format of an 8-bit cache.
