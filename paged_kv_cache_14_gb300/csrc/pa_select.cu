@@ -6,7 +6,7 @@
 // floor(min_t k / s). For a query in 8 bits, q = s_q * code, no key of the
 // block has a larger product with it than
 //   s_q s  sum_d max(code_d hi_d, code_d lo_d),
-// whose sum is a whole number below 2^22. Scores are therefore exact up to two
+// whose sum is a whole number below 2^23. Scores are therefore exact up to two
 // fp32 products in a fixed order: the choice does not depend on the order in
 // which the device runs, and a tie goes to the lower block.
 #include <algorithm>
@@ -331,11 +331,11 @@ struct SelectParams {
   int* status;
 };
 
-constexpr int kSelectThreads = 128;
-constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectMaxWarps = 16;
+constexpr int kSelectRoom = 24;  // warps that an SM's registers and shared memory hold
 constexpr int kSelectMaxCluster = 8;
 constexpr int kSelectTile = 16;       // blocks of one matrix product
-constexpr int kSelectStages = 3;      // tiles of a warp on their way
+constexpr int kSelectStages = 2;      // tiles of a warp in shared memory
 constexpr int kDigit = 9;            // bits of a digit
 constexpr int kBins = 1 << kDigit;    // its values, a 32nd of them to a lane
 constexpr int kPasses = 4;            // digits of a score
@@ -370,9 +370,11 @@ __device__ __forceinline__ int4 remote_int4(const void* local, int rank) {
   return v;
 }
 // Shared memory of the tiles on their way, which the counts take over.
-constexpr int select_stages(int d) { return d <= 128 ? kSelectStages : 2; }
-constexpr int select_ring_bytes(int d) {
-  const int ring = kSelectWarps * select_stages(d) * (kSelectTile * 2 * d + kSelectTile * 4);
+// A query row's codes, 64 bytes on where rows would lie in the same banks.
+constexpr int select_query_bytes(int d) { return 2 * d + (d % 64 == 0 ? 64 : 0); }
+constexpr uint32_t kNoBlock = 0xffc00001u;  // a scale (a NaN) that marks a block outside the pool
+constexpr int select_ring_bytes(int d, int warps) {
+  const int ring = warps * kSelectStages * (kSelectTile * 2 * d + kSelectTile * 4);
   const int counts = (kPasses + 1) * 32 * kLaneBins * 4;
   return ring > counts ? ring : counts;
 }
@@ -384,21 +386,19 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Four signed bytes to two pairs of fp16, exactly: with the sign bit flipped
-// a byte is code + 128, and behind the byte 0x64 it is the mantissa of
-// 1024 + 128 + code.
-__device__ __forceinline__ void s8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  w ^= 0x80808080u;
-  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-  const uint32_t bias = 0xe480e480u;  // -1152
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(bias));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(bias));
+// 16 x 8 sums of 32 products of signed bytes.
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // One cluster (with CL; else one CTA) per (sequence, KV head). Its CTAs split
-// the row's blocks, score them 16 at a time on the tensor cores (codes up to
-// 127 are exact in fp16, their products' sums exact in fp32) and keep the
-// scores in shared memory. The score of the last block to take is found by
+// the row's blocks, score them 16 at a time by matrix products of bytes and keep
+// the scores in shared memory. The score of the last block to take is found by
 // counting: digits of 10 bits from the top of the range that the row's scores
 // span, so that the first splits them well whatever their size, and the
 // search ends when a digit's blocks are all taken (after two digits, mostly).
@@ -409,19 +409,20 @@ __device__ __forceinline__ void s8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t
 // banks. (One tile ahead in registers took twice as long: a warp then waits
 // for memory once a tile.)
 template <typename T, int D, bool CL>
-__global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxWarps) select_kernel(const __grid_constant__ SelectParams p) {
   constexpr unsigned kAll = 0xffffffffu;
-  constexpr int Q2 = 2 * D + 4;  // fp16 of a query row in shared memory: 8 bytes on, so that rows take other banks
   constexpr int kRow = 2 * D, kPieces = kRow / 16, kTile = kSelectTile * kRow + kSelectTile * 4;
+  constexpr int kQuery = select_query_bytes(D);
   constexpr bool kSwap = kRow % 128 == 0;  // (other rows start 64 bytes apart by themselves)
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t scratch[kSelectWarps], total;
+  __shared__ uint32_t scratch[kSelectMaxWarps], total;
   __shared__ __align__(8) uint32_t range[2];
+  const int threads = blockDim.x, warps = threads >> 5;
   // The tiles' ring, later the counts; the queries; the scores.
   int(*hist)[32 * kLaneBins] = reinterpret_cast<int(*)[32 * kLaneBins]>(smem);
   int* sum = hist[kPasses];
-  __half* qs = reinterpret_cast<__half*>(smem + select_ring_bytes(D));
-  float* q_scale = reinterpret_cast<float*>(qs + p.head_tiles * 8 * Q2);
+  uint8_t* qs = smem + select_ring_bytes(D, warps);
+  float* q_scale = reinterpret_cast<float*>(qs + p.head_tiles * 8 * kQuery);
   uint32_t* keys = reinterpret_cast<uint32_t*>(q_scale + p.head_tiles * 8);
   int ranks = 1, rank = 0;
   if constexpr (CL) {
@@ -433,13 +434,17 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
   int32_t* list = p.lists + (int64_t)row * p.max_list_len;
   const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
   const int len = p.seq_lens[seq];
+  const T* q = static_cast<const T*>(p.q) + ((int64_t)seq * p.num_q_heads + head * p.group) * D;
+  float x[D / 32];  // the first query row of this warp, asked for before anything waits
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) x[i] = warp < p.group ? to_f32(q[warp * D + lane + 32 * i]) : 0.f;
   int nb = len > 0 ? (len - 1) / p.block_size + 1 : 0;
   if (len < 0 || len > p.max_seq_len || nb > p.max_blocks_per_seq) {
     if (rank == 0 && tid == 0 && head == 0) record_error(p.status, PA_ERR_SEQLEN);
     nb = 0;
   }
   if (nb <= p.max_list_len) {  // all of them (the same for the whole cluster)
-    for (int i = rank * kSelectThreads + tid; i < p.max_list_len; i += ranks * kSelectThreads)
+    for (int i = rank * threads + tid; i < p.max_list_len; i += ranks * threads)
       list[i] = i < nb ? i : -1;
     if (rank == 0 && tid == 0) p.list_lens[row] = nb;
     return;
@@ -449,81 +454,77 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
   const int chunk = ((some + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile;
   const int lo = min(rank * chunk, some), mine = min(chunk, some - lo);
 
-  // Lane i < 16 finds block i of a tile (behind the end: the last block).
-  constexpr int kStep = kSelectWarps * kSelectTile, kStages = select_stages(D);
-  auto find = [&](int b0) -> int32_t {
-    return lane < kSelectTile && b0 < mine ? table[sink + lo + min(b0 + lane, mine - 1)] : 0;
-  };
-  uint8_t* ring = smem + warp * kStages * kTile;
-  auto fetch = [&](int b0, int stage, int32_t id) {
-    if (b0 < mine) {
-      const bool there = id >= 0 && id < p.num_blocks;
-      const int32_t blk = there ? id : 0;
-      const uint32_t to = smem_u32(ring + stage * kTile);
-#pragma unroll
-      for (int i = 0; i < kSelectTile * kPieces / 32; ++i) {
-        const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
-        const int64_t at = (int64_t)__shfl_sync(kAll, blk, row) * p.num_kv_heads + head;
-        copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
-                     p.summaries + at * kRow + piece * 16);
-      }
-      if (lane < kSelectTile) {
-        const uint32_t s = to + kSelectTile * kRow + lane * 4;
-        if (there) {
-          copy_async4(s, p.scales + (int64_t)blk * p.num_kv_heads + head);
-        } else {  // a mark that no scale has
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s), "r"(0xffc00001u) : "memory");
-          if (b0 + lane < mine) record_error(p.status, PA_ERR_BLOCK_OOB);
-        }
-      }
-    }
-    copy_async_commit();
-  };
-  int32_t id = find(warp * kSelectTile);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    const int b0 = warp * kSelectTile + i * kStep;
-    const int32_t next = find(b0 + kStep);
-    fetch(b0, i, id);
-    id = next;
-  }
+  // A block's number lies where its score will be (by copies of their own, all
+  // under way at once; behind the end: the last one's).
+  for (int i = tid; i < (mine + kSelectTile - 1) / kSelectTile * kSelectTile; i += threads)
+    copy_async4(smem_u32(&keys[i]), table + sink + lo + min(i, mine - 1));
+  copy_async_commit();
   if (tid == 0) {
     range[0] = 0xffffffffu;
     range[1] = 0;
   }
   // The queries' codes, their positive and their negative part.
-  for (int h = warp; h < p.head_tiles * 8; h += kSelectWarps) {
-    float x[D / 32], top = 0.f;
-    const bool real = h < p.group;
-    const T* q = static_cast<const T*>(p.q) + ((int64_t)seq * p.num_q_heads + head * p.group + (real ? h : 0)) * D;
+  for (int h = warp; h < p.head_tiles * 8; h += warps) {
+    if (h != warp) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      x[i] = real ? to_f32(q[lane + 32 * i]) : 0.f;
-      top = fabsf(x[i]) <= 3.402823466e38f ? fmaxf(top, fabsf(x[i])) : __int_as_float(0x7f800000);
+      for (int i = 0; i < D / 32; ++i) x[i] = h < p.group ? to_f32(q[h * D + lane + 32 * i]) : 0.f;
     }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      top = fabsf(x[i]) <= 3.402823466e38f ? fmaxf(top, fabsf(x[i])) : __int_as_float(0x7f800000);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
     // (A row that is not all finite counts as zeros.)
     const float scale = top <= 3.402823466e38f ? __fdiv_rn(top, 127.f) : 0.f;
+    const Divisor div = divisor(scale);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const float code = scale > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -127.f), 127.f) : 0.f;
-      qs[h * Q2 + lane + 32 * i] = __float2half_rn(fmaxf(code, 0.f));
-      qs[h * Q2 + D + lane + 32 * i] = __float2half_rn(fminf(code, 0.f));
+      const float code = scale > 0.f ? fminf(fmaxf(rintf(quotient(x[i], div)), -127.f), 127.f) : 0.f;
+      qs[h * kQuery + lane + 32 * i] = (uint8_t)(int)fmaxf(code, 0.f);
+      qs[h * kQuery + D + lane + 32 * i] = (uint8_t)(int)fminf(code, 0.f);
     }
     if (lane == 0) q_scale[h] = scale;
   }
+  copy_async_wait<0>();
   __syncthreads();
+
+  const int step = warps * kSelectTile;
+  constexpr int kStages = kSelectStages;
+  uint8_t* ring = smem + warp * kStages * kTile;
+  // The tile at b0 into a stage.
+  const uint32_t block_bytes = p.num_kv_heads * kRow;
+  const int8_t* summaries = p.summaries + (int64_t)head * kRow;
+  auto fetch = [&](int b0, int stage) {
+    if (b0 < mine) {
+      const uint32_t to = smem_u32(ring + stage * kTile);
+#pragma unroll
+      for (int i = 0; i < kSelectTile * kPieces / 32; ++i) {
+        const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
+        const uint32_t at = keys[b0 + row], id = at < (uint32_t)p.num_blocks ? at : 0u;
+        copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
+                     summaries + (uint64_t)id * block_bytes + piece * 16);
+      }
+      if (lane < kSelectTile) {
+        const uint32_t s = to + kSelectTile * kRow + lane * 4;
+        const uint32_t id = keys[b0 + lane];
+        if (id < (uint32_t)p.num_blocks) {
+          copy_async4(s, p.scales + (int64_t)id * p.num_kv_heads + head);
+        } else {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s), "r"(kNoBlock) : "memory");
+          record_error(p.status, PA_ERR_BLOCK_OOB);
+        }
+      }
+    }
+    copy_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(warp * kSelectTile + i * step, i);
 
   uint32_t kmin = 0xffffffffu, kmax = 0;
   int stage = 0;
-  for (int b0 = warp * kSelectTile; b0 < mine; b0 += kStep) {
-    {
-      const int ahead = b0 + (kStages - 1) * kStep;
-      const int32_t next = find(ahead + kStep);
-      fetch(ahead, stage == 0 ? kStages - 1 : stage - 1, id);
-      id = next;
-    }
+  for (int b0 = warp * kSelectTile; b0 < mine; b0 += step) {
+    fetch(b0 + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
     copy_async_wait<kStages - 1>();
     __syncwarp();
     // Lane (r, c): 16 bytes of each 64 of the rows of blocks r and r + 8.
@@ -532,24 +533,20 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
     const int swap = kSwap ? (r & 1) << 2 : 0;
     float best[2] = {__int_as_float(0xff800000), __int_as_float(0xff800000)};
     for (int n = 0; n < p.head_tiles; ++n) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      const __half* qn = qs + (n * 8 + r) * Q2 + 16 * c;
+      int part[4][4] = {};  // (four sums, so that a product need not wait for the one before)
+      const uint8_t* qn = qs + (n * 8 + r) * kQuery + 16 * c;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         const int piece = (4 * j + c ^ swap) * 16;
         const uint4 x0 = *reinterpret_cast<const uint4*>(at + piece);
         const uint4 x1 = *reinterpret_cast<const uint4*>(at + 8 * kRow + piece);
-        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w};
-        const uint32_t w1[4] = {x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t f[4];
-          s8x4_to_f16x4(w0[k], f[0], f[2]);
-          s8x4_to_f16x4(w1[k], f[1], f[3]);
-          const uint2 b = *reinterpret_cast<const uint2*>(qn + 64 * j + 4 * k);
-          MmaOp<__half>::run(acc, f, b.x, b.y);
-        }
+        const uint4 y = *reinterpret_cast<const uint4*>(qn + 64 * j);
+        mma_s8(part[2 * j & 3], x0.x, x1.x, x0.y, x1.y, y.x, y.y);
+        mma_s8(part[2 * j + 1 & 3], x0.z, x1.z, x0.w, x1.w, y.z, y.w);
       }
+      float acc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = (float)(part[0][i] + part[1][i] + (part[2][i] + part[3][i]));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = n * 8 + 2 * c + i;
@@ -569,7 +566,7 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
         // outside the pool behind. (Scale 0: all its keys are 0, whatever
         // else overflows.)
         const float scale = reinterpret_cast<const float*>(tile + kSelectTile * kRow)[r + 8 * i];
-        const uint32_t key = __float_as_uint(scale) == 0xffc00001u ? 0u
+        const uint32_t key = __float_as_uint(scale) == kNoBlock ? 0u
                              : !(scale <= 3.402823466e38f)         ? 0xff800000u
                                                            : ordered(scale == 0.f ? 0.f : __fmul_rn(best[i], scale));
         keys[b] = key;
@@ -582,7 +579,7 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
   }
   copy_async_wait<0>();
   __syncthreads();
-  for (int i = tid; i < kPasses * 32 * kLaneBins / 4; i += kSelectThreads)
+  for (int i = tid; i < kPasses * 32 * kLaneBins / 4; i += threads)
     reinterpret_cast<int4*>(smem)[i] = make_int4(0, 0, 0, 0);
   kmin = __reduce_min_sync(kAll, kmin);
   kmax = __reduce_max_sync(kAll, kmax);
@@ -607,7 +604,7 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
   bool whole = false;  // all keys in question are taken
   while (need > 0 && bits > 0 && !whole) {
     const int shift = max(bits - kDigit, 0);
-    for (int i = tid; i < mine; i += kSelectThreads) {
+    for (int i = tid; i < mine; i += threads) {
       const uint32_t key = keys[i];
       if (key >= base && key - base <= width) atomicAdd(&hist[pass][bin_at((key - base) >> shift)], 1);
     }
@@ -615,19 +612,20 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
     if constexpr (CL) {
       cluster_sync_all();
       // (A thread has four digits' counts, all CTAs' at once.)
-      static_assert(kBins == 4 * kSelectThreads, "");
-      int4 x[kSelectMaxCluster];
+      for (int i = 4 * tid; i < kBins; i += 4 * threads) {
+        int4 y[kSelectMaxCluster];
 #pragma unroll
-      for (int j = 0; j < kSelectMaxCluster; ++j)
-        x[j] = j < ranks ? remote_int4(&hist[pass][bin_at(4 * tid)], j) : make_int4(0, 0, 0, 0);
+        for (int j = 0; j < kSelectMaxCluster; ++j)
+          y[j] = j < ranks ? remote_int4(&hist[pass][bin_at(i)], j) : make_int4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 1; j < kSelectMaxCluster; ++j) {
-        x[0].x += x[j].x;
-        x[0].y += x[j].y;
-        x[0].z += x[j].z;
-        x[0].w += x[j].w;
+        for (int j = 1; j < kSelectMaxCluster; ++j) {
+          y[0].x += y[j].x;
+          y[0].y += y[j].y;
+          y[0].z += y[j].z;
+          y[0].w += y[j].w;
+        }
+        *reinterpret_cast<int4*>(&sum[bin_at(i)]) = y[0];
       }
-      *reinterpret_cast<int4*>(&sum[bin_at(4 * tid)]) = x[0];
       bins = sum;
     }
     __syncthreads();
@@ -673,7 +671,7 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
   // Taken: keys above base + width, those of [base, base + width] if `whole`,
   // or else (all equal then) the first `need` of them.
   const uint32_t over = base + width;
-  const int seg = (mine + kSelectThreads - 1) / kSelectThreads | 1;  // odd: other banks
+  const int seg = (mine + threads - 1) / threads | 1;  // odd: other banks
   const int s0 = min(tid * seg, mine), s1 = min(s0 + seg, mine);
   // Taken for certain, and in question (upper half), in the segments before.
   uint32_t before = 0;
@@ -691,7 +689,8 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
   __syncthreads();
   uint32_t all = 0;
 #pragma unroll
-  for (int i = 0; i < kSelectWarps; ++i) {
+  for (int i = 0; i < kSelectMaxWarps; ++i) {
+    if (i >= warps) break;
     before += i < warp ? scratch[i] : 0u;
     all += scratch[i];
   }
@@ -710,8 +709,8 @@ __global__ void __launch_bounds__(kSelectThreads, D <= 128 ? 4 : 2) select_kerne
     same_before += tie;
   }
   if (rank == 0) {
-    for (int i = tid; i < sink; i += kSelectThreads) list[i] = i;
-    for (int i = tid; i < p.num_recent; i += kSelectThreads)
+    for (int i = tid; i < sink; i += threads) list[i] = i;
+    for (int i = tid; i < p.num_recent; i += threads)
       list[p.max_list_len - p.num_recent + i] = nb - p.num_recent + i;
     if (tid == 0) p.list_lens[row] = p.max_list_len;
   }
@@ -727,22 +726,28 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   SelectParams p = p0;
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
   const int blocks = (p.max_seq_len - 1) / p.block_size + 1;
-  // CTAs of a row: as many as keep the batch within four per SM and leave
-  // each 64 blocks.
+  // CTAs of a row (a power of two): as many as keep the batch within two an SM
+  // and leave each 128 blocks, or as shared memory takes to hold the scores;
+  // then the warps of each so that all CTAs run at once.
+  const int sms = num_sms_current_device(), most = 220 * 1024;
   int ranks = 1;
-  while (ranks < kSelectMaxCluster && rows * ranks * 2 <= 4 * num_sms_current_device() && blocks >= ranks * 2 * 64)
-    ranks *= 2;
-  const int fixed = select_ring_bytes(D) + p.head_tiles * 8 * ((2 * D + 4) * 2 + 4), most = 220 * 1024;
-  auto bytes = [&] { return fixed + (((blocks + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile) * 4; };
-  while (ranks < kSelectMaxCluster && bytes() > most) ranks *= 2;
-  const int smem = bytes();
+  while (ranks < kSelectMaxCluster && rows * ranks <= sms && blocks >= ranks * 2 * 128) ranks *= 2;
+  auto scores = [&] { return ((blocks + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile; };
+  const int queries = p.head_tiles * 8 * (select_query_bytes(D) + 4);
+  auto bytes = [&](int warps) { return select_ring_bytes(D, warps) + queries + scores() * 4; };
+  while (ranks < kSelectMaxCluster && bytes(4) > most) ranks *= 2;
+  const int64_t per_sm = (rows * ranks + sms - 1) / sms;
+  int warps = (int)std::min<int64_t>(std::min(kSelectMaxWarps, scores() / kSelectTile), kSelectRoom / per_sm);
+  while (warps > 4 && bytes(warps) > most / std::min<int64_t>(per_sm, kSelectRoom / 4)) --warps;
+  warps = std::max(warps, 4);
+  const int smem = bytes(warps);
   if (smem > most) return PA_ERR_UNSUPPORTED;
   const auto kernel = ranks > 1 ? select_kernel<T, D, true> : select_kernel<T, D, false>;
   if (smem > 47 * 1024 && set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), most) != PA_OK)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * ranks));
-  cfg.blockDim = dim3(kSelectThreads);
+  cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -881,7 +886,8 @@ int pa_select_blocks(const void* q, const int8_t* summaries, const float* summar
   if (num_q_heads % num_kv_heads) return PA_ERR_HEADS;
   if (block_size != 16 && block_size != 32) return PA_ERR_BLOCKSIZE;
   if (head_dim < 32 || head_dim > 256 || head_dim % 32 || num_q_heads / num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
-  if (num_seqs > 65535 || (int64_t)num_seqs * num_kv_heads > (1 << 26)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > (1 << 20) || (int64_t)num_seqs * num_kv_heads > (1 << 26))
+    return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!q || !summaries || !summary_scales || !block_tables || !seq_lens || !block_lists || !list_lens)
     return PA_ERR_ARG;

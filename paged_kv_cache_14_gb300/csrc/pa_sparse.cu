@@ -43,11 +43,11 @@ struct SparseParams {
   int* status;
 };
 
-constexpr int kSparseWarps = 4;
-constexpr int kSparseThreads = kSparseWarps * 32;
+constexpr int kSparseMaxWarps = 8;
+constexpr int kSparseF32Threads = 128;
 constexpr int kSparseMaxCluster = 8;
 // Tiles (K and V) of a warp in shared memory, the one in use among them.
-constexpr int sparse_stages(int tile_bytes) { return tile_bytes >= 4096 ? 2 : 4; }
+constexpr int sparse_stages(int tile_bytes) { return 8192 / tile_bytes; }
 constexpr float kMoveAt = 8.f;  // log2 of the weight that moves the reference
 
 namespace {
@@ -134,7 +134,7 @@ __device__ __forceinline__ void sparse_join(const SparseParams& p, const SparseR
                                             const float* l) {
   cluster_sync();
   const int quads = w.heads * (D / 4);
-  for (int x = w.rank * kSparseThreads + threadIdx.x; x < quads; x += w.ranks * kSparseThreads) {
+  for (int x = w.rank * blockDim.x + threadIdx.x; x < quads; x += w.ranks * blockDim.x) {
     const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
     float top = neg_inf(), sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -166,7 +166,7 @@ __device__ __forceinline__ void sparse_join(const SparseParams& p, const SparseR
 // back; a block's V scale multiplies the block's product, so that no weight
 // carries it). NT: tiles of 8 query heads.
 template <typename T, int KV8, int D, int NT>
-__global__ void __launch_bounds__(kSparseThreads, NT == 1 ? 3 : 2) sparse_kernel(const __grid_constant__ SparseParams p) {
+__global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __grid_constant__ SparseParams p) {
   using M = typename std::conditional<KV8 != 0, __half, T>::type;  // the products' type
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int H = 8 * NT;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kSparseThreads, NT == 1 ? 3 : 2) sparse_kernel
   constexpr int KS = D / 16;                  // steps of the score product
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' tiles, later their outputs
   float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
-  __shared__ float sm[kSparseWarps][H], sl[kSparseWarps][H];
+  __shared__ float sm[kSparseMaxWarps][H], sl[kSparseMaxWarps][H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   const SparseRow w = sparse_row(p, H);
   const int halves = p.block_size >> 4;  // items of a block
@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kSparseThreads, NT == 1 ? 3 : 2) sparse_kernel
     l[n][0] = l[n][1] = 0.f;
   }
 
-  const int warps = w.ranks * kSparseWarps, me = w.rank * kSparseWarps + warp, items = w.entries * halves;
+  const int cta_warps = blockDim.x >> 5;
+  const int warps = w.ranks * cta_warps, me = w.rank * cta_warps + warp, items = w.entries * halves;
   constexpr int RB = KV8 ? D : 2 * D;  // bytes of a row
   constexpr int kTile = 16 * RB, kStages = sparse_stages(kTile);
   uint8_t* ring = smem + warp * kStages * 2 * kTile;
@@ -439,37 +440,43 @@ __global__ void __launch_bounds__(kSparseThreads, NT == 1 ? 3 : 2) sparse_kernel
     }
   }
   __syncthreads();
-  for (int x = tid; x < H * D; x += kSparseThreads) {
-    const int h = x / D, d = x - h * D;
-    float top = sm[0][h], acc = 0.f;
-#pragma unroll
-    for (int i = 1; i < kSparseWarps; ++i) top = fmaxf(top, sm[i][h]);
-#pragma unroll
-    for (int i = 0; i < kSparseWarps; ++i)
-      acc += (sm[i][h] == neg_inf() ? 1.f : exp2f(sm[i][h] - top)) * so[i][h][d];
-    so[0][h][d] = acc;
-  }
-  __syncthreads();
+  // Each warp's weight in the join, in its l's place.
   if (tid < H) {
     float top = sm[0][tid], sum = 0.f;
-#pragma unroll
-    for (int i = 1; i < kSparseWarps; ++i) top = fmaxf(top, sm[i][tid]);
-#pragma unroll
-    for (int i = 0; i < kSparseWarps; ++i)
-      sum += (sm[i][tid] == neg_inf() ? 1.f : exp2f(sm[i][tid] - top)) * sl[i][tid];
-    sm[0][tid] = top;
+    for (int i = 1; i < cta_warps; ++i) top = fmaxf(top, sm[i][tid]);
+    for (int i = 0; i < cta_warps; ++i) {
+      // (A warp that saw no score: zeros, or a NaN to keep.)
+      const float f = sm[i][tid] == neg_inf() ? 1.f : exp2f(sm[i][tid] - top);
+      sum += f * sl[i][tid];
+      sm[i][tid] = f;
+    }
     sl[0][tid] = sum;
+    sl[1][tid] = top;
   }
-  sparse_join<T, D>(p, w, &so[0][0][0], sm[0], sl[0]);
+  __syncthreads();
+  for (int x = tid; x < H * D / 4; x += blockDim.x) {
+    const int h = x / (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < cta_warps; ++i) {
+      const float f = sm[i][h];
+      const float4 v = reinterpret_cast<const float4*>(so[i])[x];
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    reinterpret_cast<float4*>(so[0])[x] = acc;
+  }
+  sparse_join<T, D>(p, w, &so[0][0][0], sl[1], sl[0]);
 }
 
 // fp32 on CUDA cores, exact fp32 arithmetic: a CTA takes 16 tokens at a time,
 // scores them pair by pair of (head, token) and adds their values, a thread to
 // each dimension, for 8 query heads.
 template <int D>
-__global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid_constant__ SparseParams p) {
+__global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __grid_constant__ SparseParams p) {
   constexpr int H = 8, TOK = 16, ST = D + 4;
-  constexpr int DT = (D + kSparseThreads - 1) / kSparseThreads;  // dimensions of a thread
+  constexpr int DT = (D + kSparseF32Threads - 1) / kSparseF32Threads;  // dimensions of a thread
   extern __shared__ __align__(16) uint8_t smem[];
   float* so = reinterpret_cast<float*>(smem);  // [H][D]
   float* sq = so + H * D;          // [H][ST]
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid
   const SparseRow w = sparse_row(p, H);
   const int halves = p.block_size >> 4, items = w.entries * halves;
   const float* q = static_cast<const float*>(p.q) + ((int64_t)w.seq * p.num_q_heads + w.first_head) * D;
-  for (int x = tid; x < w.heads * D; x += kSparseThreads) sq[x / D * ST + x % D] = q[x];
+  for (int x = tid; x < w.heads * D; x += kSparseF32Threads) sq[x / D * ST + x % D] = q[x];
   if (tid < H) {
     sm[tid] = neg_inf();
     sl[tid] = 0.f;
@@ -497,7 +504,7 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid
     if (it.y == 0) continue;
     const int64_t at = (((int64_t)it.x * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * D;
     __syncthreads();
-    for (int y = tid; y < it.y * (D / 4); y += kSparseThreads) {
+    for (int y = tid; y < it.y * (D / 4); y += kSparseF32Threads) {
       const int t = y / (D / 4), d = (y - t * (D / 4)) * 4;
       *reinterpret_cast<float4*>(sk + t * ST + d) =
           *reinterpret_cast<const float4*>(static_cast<const float*>(p.k_cache) + at + t * D + d);
@@ -549,7 +556,7 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid
         const float e = ss[h][t];
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
-          const int d = tid + i * kSparseThreads;
+          const int d = tid + i * kSparseF32Threads;
           if (d < D) acc[h][i] = fmaf(e, sv[t * D + d], acc[h][i]);
         }
       }
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const __grid
   for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int i = 0; i < DT; ++i)
-      if (tid + i * kSparseThreads < D) so[h * D + tid + i * kSparseThreads] = acc[h][i];
+      if (tid + i * kSparseF32Threads < D) so[h * D + tid + i * kSparseF32Threads] = acc[h][i];
   sparse_join<float, D>(p, w, so, sm, sl);
 }
 
@@ -567,19 +574,11 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int launch_sparse(void (*kernel)(SparseParams), const SparseParams& p, int smem, int items_per_cta,
+int launch_sparse(void (*kernel)(SparseParams), const SparseParams& p, int ranks, int warps, int smem,
                   cudaStream_t stream) {
-  const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
-  const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
-  // CTAs of a row: as many as keep the batch within four per SM and leave
-  // each enough items.
-  int ranks = 1;
-  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 4 * num_sms_current_device() &&
-         items >= (int64_t)ranks * 2 * items_per_cta)
-    ranks *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * ranks));
-  cfg.blockDim = dim3(kSparseThreads);
+  cfg.gridDim = dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * p.row_groups * ranks));
+  cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -597,16 +596,41 @@ int launch_sparse_f32(const SparseParams& p, cudaStream_t stream) {
   if (smem > 40 * 1024 &&
       set_max_dynamic_smem(reinterpret_cast<const void*>(sparse_f32_kernel<D>), smem) != PA_OK)
     return PA_ERR_CUDA;
-  return launch_sparse(sparse_f32_kernel<D>, p, smem, 4, stream);
+  // CTAs of a row: as many as keep the batch within four per SM and leave each
+  // four items.
+  const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
+  const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
+  int ranks = 1;
+  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 4 * num_sms_current_device() && items >= ranks * 2 * 4)
+    ranks *= 2;
+  return launch_sparse(sparse_f32_kernel<D>, p, ranks, kSparseF32Threads / 32, smem, stream);
+}
+
+template <typename T, int KV8, int D, int NT>
+int launch_sparse_tc(const SparseParams& p, cudaStream_t stream) {
+  constexpr int tile = 16 * D * (KV8 ? 1 : 2), warp_smem = sparse_stages(tile) * 2 * tile;
+  constexpr int kRoom = NT == 1 ? 12 : 8;  // warps that an SM's registers (and shared memory) hold
+  static_assert(warp_smem >= 8 * NT * D * 4, "a warp's output fits into its tiles");
+  // All CTAs at once, if an SM's warps suffice: a row's CTAs (a power of two)
+  // and the warps of each so that every SM gets its share and no warp less
+  // than two items.
+  const int sms = num_sms_current_device();
+  const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
+  const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
+  int ranks = 1;
+  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 2 * sms && items >= ranks * 8) ranks *= 2;
+  const int64_t per_sm = (rows * ranks + sms - 1) / sms;
+  int warps = (int)std::min<int64_t>(kSparseMaxWarps, per_sm * 2 <= kRoom ? kRoom / per_sm : 4);
+  warps = (int)std::min<int64_t>(warps, std::max<int64_t>(2, (items + 2 * ranks - 1) / (2 * ranks)));
+  const auto kernel = sparse_kernel<T, KV8, D, NT>;
+  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSparseMaxWarps * warp_smem) != PA_OK)
+    return PA_ERR_CUDA;
+  return launch_sparse(kernel, p, ranks, warps, warps * warp_smem, stream);
 }
 
 template <typename T, int KV8, int D>
 int launch_sparse_tc(const SparseParams& p, cudaStream_t stream) {
-  constexpr int tile = 16 * D * (KV8 ? 1 : 2), smem = kSparseWarps * sparse_stages(tile) * 2 * tile;
-  static_assert(smem >= kSparseWarps * 16 * D * 4, "the outputs fit into the tiles");
-  const auto kernel = p.group <= 8 ? sparse_kernel<T, KV8, D, 1> : sparse_kernel<T, KV8, D, 2>;
-  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem) != PA_OK) return PA_ERR_CUDA;
-  return launch_sparse(kernel, p, smem, 2 * kSparseWarps, stream);
+  return p.group <= 8 ? launch_sparse_tc<T, KV8, D, 1>(p, stream) : launch_sparse_tc<T, KV8, D, 2>(p, stream);
 }
 
 // kv8: 0, or 1 + the format of an 8-bit cache.
