@@ -99,7 +99,7 @@ struct RopeParams {
   int32_t rows;       // rows of a token: queries, and keys and values of a 16- or 32-bit cache
   int32_t pass_rows;  // rows that a CTA does at a time
   int32_t chunks;     // CTAs of a token
-  int64_t q_ctas;     // 8-bit caches: CTAs that rotate queries
+  uint32_t cache_ctas;  // 8-bit caches: CTAs that write them
   int32_t group;      // 8-bit caches: tokens of a warp
   int* status;
 };
@@ -110,19 +110,24 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-// Where a token goes: its table row, or nullptr if it is skipped.
-__device__ __forceinline__ const float* rope_row(const RopeParams& p, int64_t t, int64_t slot, bool report) {
-  if (slot < 0) return nullptr;  // padding
-  if (slot >= (int64_t)p.num_blocks * p.block_size) {
+// Where a token goes: its slot (-1: it is skipped) and its row of the table.
+// (Both are asked for at once.)
+struct RopePlace {
+  int64_t slot;
+  int32_t pos;
+};
+__device__ __forceinline__ RopePlace rope_place(const RopeParams& p, int64_t t, bool report) {
+  RopePlace at{p.slots[t], p.positions[t]};
+  if (at.slot < 0) {  // padding
+    at.slot = -1;
+  } else if (at.slot >= (int64_t)p.num_blocks * p.block_size) {
     if (report) record_error(p.status, PA_ERR_BLOCK_OOB);
-    return nullptr;
-  }
-  const int32_t pos = p.positions[t];
-  if (pos < 0 || pos >= p.num_positions) {
+    at.slot = -1;
+  } else if (at.pos < 0 || at.pos >= p.num_positions) {
     if (report) record_error(p.status, PA_ERR_SEQLEN);
-    return nullptr;
+    at.slot = -1;
   }
-  return p.table + (int64_t)pos * p.rot;
+  return at;
 }
 
 template <typename T>
@@ -181,18 +186,19 @@ __device__ __forceinline__ T* rope_target(const RopeParams& p, int64_t t, int64_
 // place is a vector of each half, or a vector that stays (kRopeHalves); a
 // vector of pairs (kRopePairs); an element of each half, or one that stays
 // (kRopeHalvesOdd: a half that is no whole number of vectors). Rows are read
-// once and written once, kRopeBatch of them in flight; a query may be rotated
+// once and written once, rope_batch of them in flight; a query may be rotated
 // in place, because the thread that writes an element is the one that reads it.
-constexpr int kRopeBatch = 4;
+constexpr int rope_batch(int layout) { return layout == kRopePairs ? 5 : 3; }
 
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void rope_token(const RopeParams& p, int64_t t, int chunk) {
   constexpr int N = LAYOUT == kRopeHalvesOdd ? 1 : Vec16<T>::N;
   constexpr int PAIRS = LAYOUT == kRopePairs ? N / 2 : N;
+  constexpr int B = rope_batch(LAYOUT);
   using V = typename std::conditional<LAYOUT == kRopeHalvesOdd, Vec1<T>, Vec16<T>>::type;
   const int places = min(p.row_units, kRopeThreads), row0 = threadIdx.x / places;
   const int half = p.rot >> 1, rotated = p.num_q_heads + p.num_kv_heads, step = p.chunks * p.pass_rows;
-  const int64_t slot = p.slots[t];
+  const RopePlace place = rope_place(p, t, chunk == 0 && threadIdx.x == 0);
   if (row0 >= p.pass_rows) return;
   for (int u = threadIdx.x - row0 * places; u < p.row_units; u += places) {
     const int d = u * N;
@@ -201,10 +207,10 @@ __device__ __forceinline__ void rope_token(const RopeParams& p, int64_t t, int c
     const int at = LAYOUT == kRopePairs || two ? d : half + d;  // a place behind the halves
     const int turning = LAYOUT == kRopePairs ? max(0, min(PAIRS, (p.rot - d) >> 1)) : two ? PAIRS : 0;
     int r0 = chunk * p.pass_rows + row0;
-    V x[kRopeBatch], y[kRopeBatch];
+    V x[B], y[B];
     auto load = [&] {
 #pragma unroll
-      for (int k = 0; k < kRopeBatch; ++k) {
+      for (int k = 0; k < B; ++k) {
         if (r0 + k * step >= p.rows) break;
         const T* src = rope_source<T>(p, t, r0 + k * step);
         x[k].load(src + at);
@@ -212,10 +218,10 @@ __device__ __forceinline__ void rope_token(const RopeParams& p, int64_t t, int c
       }
     };
     load();  // (before the token's place is known: its rows are there in any case)
-    const float* cs = rope_row(p, t, slot, chunk == 0 && threadIdx.x == 0);
-    if (!cs) return;
-    const int64_t blk = slot / p.block_size;
-    const int off = (int)(slot - blk * p.block_size);
+    if (place.slot < 0) return;
+    const float* cs = p.table + (int64_t)place.pos * p.rot;
+    const int64_t blk = place.slot / p.block_size;
+    const int off = (int)(place.slot - blk * p.block_size);
     float c[PAIRS], s[PAIRS];
     const float* from = cs + (LAYOUT == kRopePairs ? d >> 1 : d);
     if (turning == PAIRS && PAIRS % 4 == 0 && (half & 3) == 0) {
@@ -233,7 +239,7 @@ __device__ __forceinline__ void rope_token(const RopeParams& p, int64_t t, int c
     }
     while (true) {
 #pragma unroll
-      for (int k = 0; k < kRopeBatch; ++k) {
+      for (int k = 0; k < B; ++k) {
         const int row = r0 + k * step;
         if (row >= p.rows) break;
         if (row < rotated) {
@@ -261,7 +267,7 @@ __device__ __forceinline__ void rope_token(const RopeParams& p, int64_t t, int c
         x[k].store(dst + at);
         if (two) y[k].store(dst + half + d);
       }
-      r0 += kRopeBatch * step;
+      r0 += B * step;
       if (r0 >= p.rows) break;
       load();
     }
@@ -309,13 +315,15 @@ __device__ __forceinline__ void rope_values(const T* row, const float* cs, int d
   if (whole) {
     const bool upper = d >= half;
     const int lo = upper ? d - half : d;
-    float y[VEC];
+    float y[VEC], c[VEC], s[VEC];
     row_values<T, VEC>(row, upper ? lo : d + half, y);
+    row_values<float, VEC>(cs, lo, c);
+    row_values<float, VEC>(cs + half, lo, s);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      float a = upper ? y[i] : x[i], b = upper ? x[i] : y[i];
-      rotate(a, b, cs[lo + i], cs[half + lo + i]);
-      x[i] = upper ? b : a;
+      // (Half of the pair, with the operations of rotate().)
+      x[i] = upper ? __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]))
+                   : __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
     }
     return;
   }
@@ -331,17 +339,15 @@ __device__ __forceinline__ void rope_values(const T* row, const float* cs, int d
   }
 }
 
-// A token's place, or -1 if it is skipped.
-__device__ __forceinline__ int64_t rope_place(const RopeParams& p, int64_t j) {
-  if (j < 0 || j >= p.num_tokens) return -1;
-  const int64_t s = p.slots[j];
-  if (s < 0 || s >= (int64_t)p.num_blocks * p.block_size) return -1;
-  const int32_t pos = p.positions[j];
-  return pos >= 0 && pos < p.num_positions ? s : -1;
+// The place of token j, which need not exist.
+__device__ __forceinline__ RopePlace rope_place_or_none(const RopeParams& p, int64_t j) {
+  return j >= 0 && j < p.num_tokens ? rope_place(p, j, false) : RopePlace{-1, 0};
 }
 
+constexpr int kRunBatch = 2;
+
 // The run of tokens that starts with token t (its place: slot): one KV head of
-// one pool. Rows are loaded kRopeBatch at a time; the rows of a run that is no
+// one pool. Rows are loaded kRunBatch at a time; the rows of a run that is no
 // longer are kept from the search for the largest value to their encoding.
 template <typename T, int VEC, bool E5>
 __device__ __forceinline__ void rope_run_8bit(const RopeParams& p, bool inter, int64_t t, int64_t slot, int h,
@@ -349,25 +355,25 @@ __device__ __forceinline__ void rope_run_8bit(const RopeParams& p, bool inter, i
   constexpr int D = VEC * 32;
   constexpr unsigned kFull = 0xffffffffu;
   const int lane = threadIdx.x & 31, bs = p.block_size;
-  const int64_t blk = slot / bs, at = blk * p.num_kv_heads + h;
+  const int64_t blk = slot / bs, tile = blk * p.num_kv_heads + h;
   const T* src = static_cast<const T*>(pool == 0 ? p.k : p.v) + h * D;
   const int64_t stride = pool == 0 ? p.k_stride : p.v_stride;
   const bool whole = (p.rot >> 1) % VEC == 0;
-  uint8_t* codes = static_cast<uint8_t*>(pool == 0 ? p.k_cache : p.v_cache) + at * bs * D + lane * VEC;
-  float* sp = p.kv_scales + at * 2 + pool;
+  uint8_t* codes = static_cast<uint8_t*>(pool == 0 ? p.k_cache : p.v_cache) + tile * bs * D + lane * VEC;
+  float* sp = p.kv_scales + tile * 2 + pool;
   const float stored = *sp;
-  float x[kRopeBatch][VEC];
-  int off[kRopeBatch];
-  // The next rows of `mem` (tokens base + its bits, in blocks' offsets sj).
-  auto take = [&](int64_t base, int64_t sj, unsigned& mem) {
+  float x[kRunBatch][VEC];
+  int off[kRunBatch];
+  // The next rows of `mem` (tokens base + its bits; lanes have their places).
+  auto take = [&](int64_t base, const RopePlace& at, unsigned& mem) {
     int n = 0;
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
+    for (int k = 0; k < kRunBatch; ++k) {
       if (!mem) break;
       const int ln = __ffs(mem) - 1;
       mem &= mem - 1;
-      off[k] = (int)(__shfl_sync(kFull, sj, ln) - blk * bs);
-      const float* cs = pool == 0 ? p.table + (int64_t)p.positions[base + ln] * p.rot : nullptr;
+      off[k] = (int)(__shfl_sync(kFull, at.slot, ln) - blk * bs);
+      const float* cs = pool == 0 ? p.table + (int64_t)__shfl_sync(kFull, at.pos, ln) * p.rot : nullptr;
       rope_values<T, VEC>(src + (base + ln) * stride, cs, lane * VEC, p.rot, inter, whole, x[k]);
       n = k + 1;
     }
@@ -377,15 +383,15 @@ __device__ __forceinline__ void rope_run_8bit(const RopeParams& p, bool inter, i
   int omin = bs, rows = 0, kept = 0;
   int64_t end = p.num_tokens;
   for (int64_t base = t; base < p.num_tokens; base += 32) {
-    const int64_t sj = rope_place(p, base + lane);
-    const unsigned other = __ballot_sync(kFull, sj >= 0 && sj / bs != blk);
+    const RopePlace at = rope_place_or_none(p, base + lane);
+    const unsigned other = __ballot_sync(kFull, at.slot >= 0 && at.slot / bs != blk);
     const int lim = other ? __ffs(other) - 1 : 32;
-    unsigned mem = __ballot_sync(kFull, sj >= 0 && lane < lim);
+    unsigned mem = __ballot_sync(kFull, at.slot >= 0 && lane < lim);
     while (mem) {
-      kept = take(base, sj, mem);
+      kept = take(base, at, mem);
       rows += kept;
 #pragma unroll
-      for (int k = 0; k < kRopeBatch; ++k) {
+      for (int k = 0; k < kRunBatch; ++k) {
         if (k >= kept) break;
         omin = min(omin, off[k]);
 #pragma unroll
@@ -421,7 +427,7 @@ __device__ __forceinline__ void rope_run_8bit(const RopeParams& p, bool inter, i
   const Divisor div = divisor(s_new);
   auto encode = [&](int n) {
 #pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
+    for (int k = 0; k < kRunBatch; ++k) {
       if (k >= n) break;
       uint32_t c[VEC / 2];
 #pragma unroll
@@ -434,9 +440,9 @@ __device__ __forceinline__ void rope_run_8bit(const RopeParams& p, bool inter, i
     encode(kept);
   } else {
     for (int64_t base = t; base < end; base += 32) {
-      const int64_t sj = base + lane < end ? rope_place(p, base + lane) : -1;
-      unsigned mem = __ballot_sync(kFull, sj >= 0);
-      while (mem) encode(take(base, sj, mem));
+      const RopePlace at = rope_place_or_none(p, base + lane < end ? base + lane : -1);
+      unsigned mem = __ballot_sync(kFull, at.slot >= 0);
+      while (mem) encode(take(base, at, mem));
     }
   }
   if (lane == 0) *sp = s_new;
@@ -454,8 +460,8 @@ __device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter,
   const int rem = (int)(w - g * hkv * 2), h = rem >> 1, pool = rem & 1;
   const int64_t t = t0 - 16 + lane;
   const bool mine = lane >= 16 && lane < 16 + p.group && t < p.num_tokens;
-  const int64_t slot = rope_place(p, t);
-  if (mine && slot < 0 && rem == 0) rope_row(p, t, p.slots[t], true);
+  const int64_t slot = rope_place_or_none(p, t).slot;
+  if (mine && slot < 0 && rem == 0) rope_place(p, t, true);  // (what is wrong with it)
   const unsigned ok = __ballot_sync(kFull, slot >= 0);
   const unsigned below = ok & ((1u << lane) - 1u);
   const int64_t before = __shfl_sync(kFull, slot, below ? 31 - __clz(below) : 0);
@@ -466,7 +472,7 @@ __device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter,
     const int ln = __ffs(unsure) - 1;
     const int64_t blk = __shfl_sync(kFull, slot, ln) / bs;
     for (int64_t base = t0 - 17; base >= 0; base -= 32) {
-      const int64_t sj = rope_place(p, base - lane);
+      const int64_t sj = rope_place_or_none(p, base - lane).slot;
       const unsigned found = __ballot_sync(kFull, sj >= 0);
       if (found) {
         const int64_t near = __shfl_sync(kFull, sj, __ffs(found) - 1);  // lowest lane = latest token
@@ -482,16 +488,17 @@ __device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter,
   }
 }
 
+// The caches' CTAs come first: they take longer than the queries'.
 template <typename T, int VEC, bool E5, int LAYOUT>
-__global__ void __launch_bounds__(kRopeThreads) rope_8bit_kernel(const __grid_constant__ RopeParams p) {
-  if (blockIdx.x >= p.q_ctas) {
-    const int64_t w = (blockIdx.x - p.q_ctas) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_8bit_kernel(const __grid_constant__ RopeParams p) {
+  if (blockIdx.x < p.cache_ctas) {
+    const int64_t w = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     if (w < (p.num_tokens + p.group - 1) / p.group * p.num_kv_heads * 2)
       rope_cache_8bit<T, VEC, E5>(p, LAYOUT == kRopePairs, w);
     return;
   }
-  const unsigned t = blockIdx.x / p.chunks;
-  rope_token<T, LAYOUT>(p, t, blockIdx.x - t * p.chunks);
+  const unsigned x = blockIdx.x - p.cache_ctas, t = x / p.chunks;
+  rope_token<T, LAYOUT>(p, t, x - t * p.chunks);
 }
 
 namespace {
@@ -503,8 +510,7 @@ int launch_rope(const RopeParams& p, int kv8, cudaStream_t stream) {
   if (!kv8) {
     rope_kernel<T, LAYOUT><<<(unsigned)(p.num_tokens * p.chunks), kRopeThreads, 0, stream>>>(p);
   } else {
-    const int64_t warps = (p.num_tokens + p.group - 1) / p.group * p.num_kv_heads * 2;
-    const unsigned ctas = (unsigned)(p.q_ctas + (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
+    const unsigned ctas = p.cache_ctas + (p.num_q_heads > 0 ? (unsigned)(p.num_tokens * p.chunks) : 0u);
     const bool e5 = kv8 == 1 + PA_KV_E5M2;
     if (p.head_dim == 64 && e5) rope_8bit_kernel<T, 2, true, LAYOUT><<<ctas, kRopeThreads, 0, stream>>>(p);
     else if (p.head_dim == 64) rope_8bit_kernel<T, 2, false, LAYOUT><<<ctas, kRopeThreads, 0, stream>>>(p);
@@ -576,11 +582,12 @@ int rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_str
   const int passes = std::max(1, (p.rows + p.pass_rows - 1) / p.pass_rows);
   const int64_t room = 16 * num_sms_current_device();
   p.chunks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(passes, room / num_tokens));
-  p.q_ctas = num_q_heads > 0 ? num_tokens * p.chunks : 0;
   // Tokens of a warp (8-bit caches): more than one when that leaves each SM 32 warps.
   const int64_t warps = num_tokens * num_kv_heads * 2;
   p.group = (int32_t)std::max<int64_t>(1, std::min<int64_t>(16, warps / (32 * num_sms_current_device())));
   if (num_tokens > (1ll << 30) || num_tokens * num_kv_heads > (1ll << 30)) return PA_ERR_UNSUPPORTED;
+  p.cache_ctas = (uint32_t)(((num_tokens + p.group - 1) / p.group * num_kv_heads * 2 + kRopeThreads / 32 - 1) /
+                            (kRopeThreads / 32));
   if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
 #define PA_ROPE(T)                                                       \
   (layout == kRopePairs    ? launch_rope<T, kRopePairs>(p, kv8, stream)  \
@@ -634,8 +641,9 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
     steps.step[i] = turns >= 1.0 ? 0 : (unsigned long long)(turns * 18446744073709551616.0);
   }
   const int n = half % 4 == 0 ? 4 : 1, rows = kRopeThreads / (half / n);
-  // Four positions a thread, and no more CTAs than that takes.
-  const unsigned ctas = (unsigned)((num_positions + 4 * rows - 1) / (4 * rows));
+  // Eight CTAs an SM: threads find their steps once, which takes as long as
+  // several positions (131072 of 128: 17 us with four positions a thread).
+  const unsigned ctas = (unsigned)std::min<int64_t>((num_positions + rows - 1) / rows, 8 * num_sms_current_device());
   const auto kernel = n == 4 ? rope_table_kernel<4> : rope_table_kernel<1>;
   kernel<<<ctas, kRopeThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       cos_sin, (uint32_t)first_position, (uint32_t)num_positions, half, (float)amplitude, steps);

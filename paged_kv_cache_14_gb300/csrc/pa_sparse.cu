@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
 
 // The cluster's row: its sequence, KV head and query heads, and its list.
 struct SparseRow {
-  int ranks, rank, seq, head, first_head, heads, len, entries;
+  int ranks, rank, row, seq, head, first_head, heads, len, entries;
   const int32_t* list;
   const int32_t* table;
 };
@@ -91,31 +91,39 @@ __device__ __forceinline__ SparseRow sparse_row(const SparseParams& p, int heads
   SparseRow w;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(w.ranks));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(w.rank));
-  int row = blockIdx.x / w.ranks;
-  const int rg = row % p.row_groups;
-  row /= p.row_groups;
-  w.seq = row / p.num_kv_heads;
-  w.head = row - w.seq * p.num_kv_heads;
+  const int x = blockIdx.x / w.ranks;
+  w.row = x / p.row_groups;
+  const int rg = x - w.row * p.row_groups;
+  w.seq = w.row / p.num_kv_heads;
+  w.head = w.row - w.seq * p.num_kv_heads;
   w.first_head = w.head * p.group + rg * heads_per_row;
   w.heads = min(heads_per_row, p.group - rg * heads_per_row);
   w.len = p.seq_lens[w.seq];
-  w.entries = p.list_lens[row];
-  w.list = p.lists + (int64_t)row * p.max_list_len;
+  w.entries = p.list_lens[w.row];
+  w.list = p.lists + (int64_t)w.row * p.max_list_len;
   w.table = p.block_tables + (int64_t)w.seq * p.max_blocks_per_seq;
+  return w;
+}
+// Its lengths, once they are there: entries 0 if they are refused.
+__device__ __forceinline__ void sparse_check(const SparseParams& p, SparseRow& w) {
   if (w.entries < 0 || w.entries > p.max_list_len || w.len < 0 ||
       (w.len > 0 && (w.len - 1) / p.block_size >= p.max_blocks_per_seq)) {
     if (threadIdx.x == 0) record_error(p.status, PA_ERR_SEQLEN);
     w.entries = 0;
   }
-  return w;
 }
 
-// Tokens `16 sub ..` of list entry i: (block, tokens there); no tokens for an
+// List entry i and the one before it, wherever the list ends (asked for before
+// its length is known).
+__device__ __forceinline__ int2 sparse_entry(const SparseParams& p, const SparseRow& w, int i) {
+  return i < p.max_list_len ? make_int2(i > 0 ? w.list[i - 1] : -1, w.list[i]) : make_int2(-1, -1);
+}
+// Tokens `16 sub ..` of an entry: (block, tokens there); no tokens for an
 // entry that is refused.
-__device__ __forceinline__ int2 sparse_item(const SparseParams& p, const SparseRow& w, int i, int sub) {
-  const int lb = w.list[i], before = i > 0 ? w.list[i - 1] : -1;
-  if (lb <= before || lb < 0 || w.len <= 0 || lb > (w.len - 1) / p.block_size) {
-    record_error(p.status, lb <= before || lb < 0 ? PA_ERR_ARG : PA_ERR_SEQLEN);
+__device__ __forceinline__ int2 sparse_item(const SparseParams& p, const SparseRow& w, int2 entry, int sub) {
+  const int lb = entry.y;
+  if (lb <= entry.x || lb < 0 || w.len <= 0 || lb > (w.len - 1) / p.block_size) {
+    record_error(p.status, lb <= entry.x || lb < 0 ? PA_ERR_ARG : PA_ERR_SEQLEN);
     return make_int2(0, 0);
   }
   const int blk = w.table[lb];
@@ -178,8 +186,10 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
   float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
   __shared__ float sm[kSparseMaxWarps][H], sl[kSparseMaxWarps][H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
-  const SparseRow w = sparse_row(p, H);
+  SparseRow w = sparse_row(p, H);
   const int halves = p.block_size >> 4;  // items of a block
+  const int cta_warps = blockDim.x >> 5, warps = w.ranks * cta_warps, me = w.rank * cta_warps + warp;
+  int2 entry = sparse_entry(p, w, (me + lane * warps) / halves);  // of the first items
 
   // The queries' fragments: head r (and r + 8), 16 bytes as the keys lie.
   uint32_t qf[NT][KS][2];
@@ -246,8 +256,8 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
     l[n][0] = l[n][1] = 0.f;
   }
 
-  const int cta_warps = blockDim.x >> 5;
-  const int warps = w.ranks * cta_warps, me = w.rank * cta_warps + warp, items = w.entries * halves;
+  sparse_check(p, w);
+  const int items = w.entries * halves;
   constexpr int RB = KV8 ? D : 2 * D;  // bytes of a row
   constexpr int kTile = 16 * RB, kStages = sparse_stages(kTile);
   uint8_t* ring = smem + warp * kStages * 2 * kTile;
@@ -257,8 +267,8 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
     int2 it = make_int2(0, 0);
     float ks = 1.f, vs = 1.f;
     if (mine < items) {
-      const int i = halves == 2 ? mine >> 1 : mine, sub = halves == 2 ? mine & 1 : 0;
-      it = sparse_item(p, w, i, sub);
+      if (base != me) entry = sparse_entry(p, w, mine / halves);
+      it = sparse_item(p, w, entry, halves == 2 ? mine & 1 : 0);
       if constexpr (KV8 != 0) {
         const float2 s = *reinterpret_cast<const float2*>(p.kv_scales + ((int64_t)it.x * p.num_kv_heads + w.head) * 2);
         ks = s.x;
@@ -484,7 +494,8 @@ __global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __g
   float* sv = sk + TOK * ST;       // [TOK][D]
   __shared__ float ss[H][TOK], sm[H], sl[H], sf[H];
   const int tid = threadIdx.x;
-  const SparseRow w = sparse_row(p, H);
+  SparseRow w = sparse_row(p, H);
+  sparse_check(p, w);
   const int halves = p.block_size >> 4, items = w.entries * halves;
   const float* q = static_cast<const float*>(p.q) + ((int64_t)w.seq * p.num_q_heads + w.first_head) * D;
   for (int x = tid; x < w.heads * D; x += kSparseF32Threads) sq[x / D * ST + x % D] = q[x];
@@ -500,7 +511,7 @@ __global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __g
   for (int x = w.rank; x < items; x += w.ranks) {
     const int sub = halves == 2 ? x & 1 : 0;
     // (Every thread asks: the answer is the same.)
-    const int2 it = sparse_item(p, w, halves == 2 ? x >> 1 : x, sub);
+    const int2 it = sparse_item(p, w, sparse_entry(p, w, x / halves), sub);
     if (it.y == 0) continue;
     const int64_t at = (((int64_t)it.x * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * D;
     __syncthreads();
