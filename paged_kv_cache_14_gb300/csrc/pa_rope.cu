@@ -30,12 +30,13 @@ struct RopeSteps {
   unsigned long long step[kRopeMaxDim / 2];
 };
 
-// cos and sin of t / 2^64 turns: the nearest quarter turn is taken out, and
-// the rest, at most pi/4, goes through the Taylor polynomials of degree 9 and
-// 10 (their next terms are below 2^-28).
-__device__ __forceinline__ void turn(unsigned long long t, float& c, float& s) {
-  const unsigned quarter = (unsigned)((t + (1ull << 61)) >> 62);
-  const float x = __ll2float_rn((long long)(t << 2)) * (float)(1.5707963267948966 / 18446744073709551616.0);
+// cos and sin of position p: the upper 32 bits of its angle (2^-32 of a turn is
+// 1.5e-9) less the nearest quarter turn, and the rest, at most pi/4, through
+// the Taylor polynomials of degree 9 and 10 (their next terms are below 2^-28).
+__device__ __forceinline__ void turn(uint32_t p, unsigned long long step, float& c, float& s) {
+  const uint32_t t = p * (uint32_t)(step >> 32) + __umulhi(p, (uint32_t)step);
+  const uint32_t quarter = (t + (1u << 29)) >> 30;
+  const float x = __int2float_rn((int)(t << 2)) * (float)(1.5707963267948966 / 4294967296.0);
   const float y = x * x;
   const float sn =
       x + x * y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880))));
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(float* __restr
     float c[N], s[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      turn((first + (unsigned long long)p) * step[k], c[k], s[k]);
+      turn(first + (uint32_t)p, step[k], c[k], s[k]);
       c[k] *= amplitude;
       s[k] *= amplitude;
     }
