@@ -327,23 +327,29 @@ __device__ __forceinline__ void copy_async_wait() {  // for all groups but the l
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Quotients by one divisor, each correctly rounded: with a correctly rounded
-// reciprocal, a quotient and its exact remainder give the rounded quotient
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990) as long as nothing overflows or loses bits below the
-// normal numbers, which a divisor from 2^-80 to 1 sees to for the uses here
-// (quotients of at most 2^16 in size, of which those below 2^-40 matter by
-// their sign alone). Other divisors go through the division itself.
+// Quotients by one divisor, each correctly rounded. The product with a
+// correctly rounded reciprocal is within 1.5 units of the quotient's last
+// place, a step with its remainder (exact in a fused multiply-add) brings it
+// within one, and from there another such step gives the rounded quotient,
+// unless the divisor's significand is all ones (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990). That
+// holds while nothing overflows or loses bits below the normal numbers, which a
+// divisor from 2^-80 to 1 sees to for the uses here (quotients of at most 2^16
+// in size, of which those below 2^-40 matter by their sign alone). Other
+// divisors go through the division itself. (Summaries of 190000 tokens: 95 us
+// with divisions, 76 us so.)
 struct Divisor {
   float by, inv;
   bool quick;
 };
 __device__ __forceinline__ Divisor divisor(float s) {
-  return Divisor{s, __fdiv_rn(1.f, s), s >= 8.27180613e-25f && s <= 1.f};
+  return Divisor{s, __fdiv_rn(1.f, s),
+                 s >= 8.27180613e-25f && s <= 1.f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu};
 }
 __device__ __forceinline__ float quotient(float x, const Divisor& d) {
   if (!d.quick) return __fdiv_rn(x, d.by);
-  const float y = __fmul_rn(x, d.inv);
+  float y = __fmul_rn(x, d.inv);
+  y = __fmaf_rn(__fmaf_rn(-y, d.by, x), d.inv, y);
   return __fmaf_rn(__fmaf_rn(-y, d.by, x), d.inv, y);
 }
 

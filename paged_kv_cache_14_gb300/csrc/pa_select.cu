@@ -328,6 +328,7 @@ struct SelectParams {
   int32_t* list_lens;
   int32_t max_blocks_per_seq, num_seqs, max_seq_len, num_q_heads, num_kv_heads, num_blocks, block_size, group;
   int32_t max_list_len, num_sink, num_recent, head_tiles;
+  pa_dtype dtype;
   int* status;
 };
 
@@ -335,7 +336,7 @@ constexpr int kSelectMaxWarps = 16;
 constexpr int kSelectRoom = 24;  // warps that an SM's registers and shared memory hold
 constexpr int kSelectMaxCluster = 8;
 constexpr int kSelectTile = 16;       // blocks of one matrix product
-constexpr int kSelectStages = 2;      // tiles of a warp in shared memory
+constexpr int kSelectStages = 2;      // tiles of a warp in shared memory: in use, on its way
 constexpr int kDigit = 9;            // bits of a digit
 constexpr int kBins = 1 << kDigit;    // its values, a 32nd of them to a lane
 constexpr int kPasses = 4;            // digits of a score
@@ -399,17 +400,17 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 // One cluster (with CL; else one CTA) per (sequence, KV head). Its CTAs split
 // the row's blocks, score them 16 at a time by matrix products of bytes and keep
 // the scores in shared memory. The score of the last block to take is found by
-// counting: digits of 10 bits from the top of the range that the row's scores
+// counting: digits of 9 bits from the top of the range that the row's scores
 // span, so that the first splits them well whatever their size, and the
 // search ends when a digit's blocks are all taken (after two digits, mostly).
 //
-// The summaries come by asynchronous copies, kSelectStages tiles ahead of
-// each warp: 16 blocks' rows as they lie, but for the halves of 128 bytes of
-// every other row, which change places so that a fragment's rows take all
-// banks. (One tile ahead in registers took twice as long: a warp then waits
-// for memory once a tile.)
-template <typename T, int D, bool CL>
-__global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxWarps) select_kernel(const __grid_constant__ SelectParams p) {
+// The summaries come by asynchronous copies, a tile ahead of each warp: 16
+// blocks' rows as they lie, but for the halves of 128 bytes of every other
+// row, which change places so that a fragment's rows take all banks. ONE: the
+// group's heads fit one tile of 8, whose codes then stay in registers.
+template <int D, bool CL, bool ONE>
+__global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxWarps)
+    select_kernel(const __grid_constant__ SelectParams p) {
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kRow = 2 * D, kPieces = kRow / 16, kTile = kSelectTile * kRow + kSelectTile * 4;
   constexpr int kQuery = select_query_bytes(D);
@@ -434,10 +435,17 @@ __global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxW
   int32_t* list = p.lists + (int64_t)row * p.max_list_len;
   const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq;
   const int len = p.seq_lens[seq];
-  const T* q = static_cast<const T*>(p.q) + ((int64_t)seq * p.num_q_heads + head * p.group) * D;
   float x[D / 32];  // the first query row of this warp, asked for before anything waits
+  auto query = [&](int h) {
+    const int64_t at = ((int64_t)seq * p.num_q_heads + head * p.group + h) * D + lane;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) x[i] = warp < p.group ? to_f32(q[warp * D + lane + 32 * i]) : 0.f;
+    for (int i = 0; i < D / 32; ++i)
+      x[i] = h >= p.group         ? 0.f
+             : p.dtype == PA_F32 ? static_cast<const float*>(p.q)[at + 32 * i]
+             : p.dtype == PA_F16 ? to_f32(static_cast<const __half*>(p.q)[at + 32 * i])
+                                 : to_f32(static_cast<const __nv_bfloat16*>(p.q)[at + 32 * i]);
+  };
+  query(warp);
   int nb = len > 0 ? (len - 1) / p.block_size + 1 : 0;
   if (len < 0 || len > p.max_seq_len || nb > p.max_blocks_per_seq) {
     if (rank == 0 && tid == 0 && head == 0) record_error(p.status, PA_ERR_SEQLEN);
@@ -465,10 +473,7 @@ __global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxW
   }
   // The queries' codes, their positive and their negative part.
   for (int h = warp; h < p.head_tiles * 8; h += warps) {
-    if (h != warp) {
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) x[i] = h < p.group ? to_f32(q[h * D + lane + 32 * i]) : 0.f;
-    }
+    if (h != warp) query(h);
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
@@ -490,20 +495,36 @@ __global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxW
   __syncthreads();
 
   const int step = warps * kSelectTile;
-  constexpr int kStages = kSelectStages;
-  uint8_t* ring = smem + warp * kStages * kTile;
+  uint8_t* ring = smem + warp * kSelectStages * kTile;
   // The tile at b0 into a stage.
   const uint32_t block_bytes = p.num_kv_heads * kRow;
   const int8_t* summaries = p.summaries + (int64_t)head * kRow;
   auto fetch = [&](int b0, int stage) {
     if (b0 < mine) {
       const uint32_t to = smem_u32(ring + stage * kTile);
+      // Instruction i takes whole rows, and a lane its neighbours in the next
+      // ones, so that four of its blocks' numbers are one load.
+      constexpr int kCopies = kSelectTile * kPieces / 32;
+      const uint32_t most = p.num_blocks - 1;
+      if constexpr (kCopies % 4 == 0 && 32 % kPieces == 0) {
+        const int row0 = lane / kPieces * kCopies, piece = lane % kPieces;
+        const int8_t* from = summaries + piece * 16;
 #pragma unroll
-      for (int i = 0; i < kSelectTile * kPieces / 32; ++i) {
-        const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
-        const uint32_t at = keys[b0 + row], id = at < (uint32_t)p.num_blocks ? at : 0u;
-        copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
-                     summaries + (uint64_t)id * block_bytes + piece * 16);
+        for (int i = 0; i < kCopies; i += 4) {
+          const uint4 id = *reinterpret_cast<const uint4*>(keys + b0 + row0 + i);
+          const uint32_t ids[4] = {id.x, id.y, id.z, id.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            copy_async16(to + (row0 + i + k) * kRow + (kSwap ? piece ^ (i + k & 1) << 2 : piece) * 16,
+                         from + (uint64_t)min(ids[k], most) * block_bytes);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
+          copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
+                       summaries + (uint64_t)min(keys[b0 + row], most) * block_bytes + piece * 16);
+        }
       }
       if (lane < kSelectTile) {
         const uint32_t s = to + kSelectTile * kRow + lane * 4;
@@ -518,64 +539,79 @@ __global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxW
     }
     copy_async_commit();
   };
+  fetch(warp * kSelectTile, 0);
+  uint4 qf[ONE ? D / 32 : 1];
+  float qs0 = 0.f, qs1 = 0.f;
+  if constexpr (ONE) {
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(warp * kSelectTile + i * step, i);
+    for (int j = 0; j < D / 32; ++j) qf[j] = *reinterpret_cast<const uint4*>(qs + r * kQuery + 16 * c + 64 * j);
+    qs0 = q_scale[2 * c];
+    qs1 = q_scale[2 * c + 1];
+  }
+  const float none = __int_as_float(0xff800000);
+  const bool odd = c & 1, upper = c & 2;
 
   uint32_t kmin = 0xffffffffu, kmax = 0;
-  int stage = 0;
-  for (int b0 = warp * kSelectTile; b0 < mine; b0 += step) {
-    fetch(b0 + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-    copy_async_wait<kStages - 1>();
-    __syncwarp();
-    // Lane (r, c): 16 bytes of each 64 of the rows of blocks r and r + 8.
-    const uint8_t* tile = ring + stage * kTile;
-    const uint8_t* at = tile + r * kRow;
-    const int swap = kSwap ? (r & 1) << 2 : 0;
-    float best[2] = {__int_as_float(0xff800000), __int_as_float(0xff800000)};
-    for (int n = 0; n < p.head_tiles; ++n) {
-      int part[4][4] = {};  // (four sums, so that a product need not wait for the one before)
-      const uint8_t* qn = qs + (n * 8 + r) * kQuery + 16 * c;
+  for (int b0 = warp * kSelectTile; b0 < mine; b0 += 2 * step) {
+    float best[2][2], scale = 0.f;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const int piece = (4 * j + c ^ swap) * 16;
-        const uint4 x0 = *reinterpret_cast<const uint4*>(at + piece);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(at + 8 * kRow + piece);
-        const uint4 y = *reinterpret_cast<const uint4*>(qn + 64 * j);
-        mma_s8(part[2 * j & 3], x0.x, x1.x, x0.y, x1.y, y.x, y.y);
-        mma_s8(part[2 * j + 1 & 3], x0.z, x1.z, x0.w, x1.w, y.z, y.w);
-      }
-      float acc[4];
+    for (int t = 0; t < 2; ++t) {
+      // Lane (r, c): 16 bytes of each 64 of the rows of blocks r and r + 8.
+      best[t][0] = best[t][1] = none;
+      fetch(b0 + (t + 1) * step, t ^ 1);
+      copy_async_wait<1>();
+      __syncwarp();
+      if (b0 + t * step < mine) {
+        const uint8_t* tile = ring + t * kTile;
+        const uint8_t* at = tile + r * kRow;
+        const int swap = kSwap ? (r & 1) << 2 : 0;
+        for (int n = 0; n < (ONE ? 1 : p.head_tiles); ++n) {
+          int part[4][4] = {};  // (four sums, so that a product need not wait for the one before)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = (float)(part[0][i] + part[1][i] + (part[2][i] + part[3][i]));
+          for (int j = 0; j < D / 32; ++j) {
+            const int piece = (4 * j + c ^ swap) * 16;
+            const uint4 x0 = *reinterpret_cast<const uint4*>(at + piece);
+            const uint4 x1 = *reinterpret_cast<const uint4*>(at + 8 * kRow + piece);
+            const uint4 y = ONE ? qf[ONE ? j : 0]
+                                : *reinterpret_cast<const uint4*>(qs + (n * 8 + r) * kQuery + 16 * c + 64 * j);
+            mma_s8(part[2 * j & 3], x0.x, x1.x, x0.y, x1.y, y.x, y.y);
+            mma_s8(part[2 * j + 1 & 3], x0.z, x1.z, x0.w, x1.w, y.z, y.w);
+          }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = n * 8 + 2 * c + i;
-        if (h < p.group) {
-          best[0] = fmaxf(best[0], __fmul_rn(acc[i], q_scale[h]));
-          best[1] = fmaxf(best[1], __fmul_rn(acc[2 + i], q_scale[h]));
+          for (int i = 0; i < 2; ++i) {
+            const int h = n * 8 + 2 * c + i;
+            const float s = ONE ? i ? qs1 : qs0 : q_scale[h];
+            if (h < p.group) {
+              best[t][0] = fmaxf(best[t][0], __fmul_rn((float)(part[0][i] + part[1][i] + (part[2][i] + part[3][i])), s));
+              best[t][1] =
+                  fmaxf(best[t][1],
+                        __fmul_rn((float)(part[0][2 + i] + part[1][2 + i] + (part[2][2 + i] + part[3][2 + i])), s));
+            }
+          }
         }
+        if (odd == (t == 1)) scale = reinterpret_cast<const float*>(tile + kSelectTile * kRow)[r + (upper ? 8 : 0)];
       }
+      __syncwarp();  // the tile has been read
     }
+    // The maximum over the group's heads, which four lanes share: each gives
+    // the others what they keep, and keeps one block of the two tiles' 32.
+    float m[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      best[i] = fmaxf(best[i], __shfl_xor_sync(kAll, best[i], 1));
-      best[i] = fmaxf(best[i], __shfl_xor_sync(kAll, best[i], 2));
-      const int b = b0 + r + 8 * i;
-      if (c == 0 && b < mine) {
-        // A block with keys that are not finite comes before all others, one
-        // outside the pool behind. (Scale 0: all its keys are 0, whatever
-        // else overflows.)
-        const float scale = reinterpret_cast<const float*>(tile + kSelectTile * kRow)[r + 8 * i];
-        const uint32_t key = __float_as_uint(scale) == kNoBlock ? 0u
-                             : !(scale <= 3.402823466e38f)         ? 0xff800000u
-                                                           : ordered(scale == 0.f ? 0.f : __fmul_rn(best[i], scale));
-        keys[b] = key;
-        kmin = min(kmin, key);
-        kmax = max(kmax, key);
-      }
+    for (int i = 0; i < 2; ++i)
+      m[i] = fmaxf(odd ? best[1][i] : best[0][i], __shfl_xor_sync(kAll, odd ? best[0][i] : best[1][i], 1));
+    const float top = fmaxf(upper ? m[1] : m[0], __shfl_xor_sync(kAll, upper ? m[0] : m[1], 2));
+    const int b = b0 + (odd ? step : 0) + r + (upper ? 8 : 0);
+    if (b < mine) {
+      // A block with keys that are not finite comes before all others, one
+      // outside the pool behind. (Scale 0: all its keys are 0, whatever else
+      // overflows.)
+      const uint32_t key = __float_as_uint(scale) == kNoBlock ? 0u
+                           : !(scale <= 3.402823466e38f)         ? 0xff800000u
+                                                         : ordered(scale == 0.f ? 0.f : __fmul_rn(top, scale));
+      keys[b] = key;
+      kmin = min(kmin, key);
+      kmax = max(kmax, key);
     }
-    __syncwarp();  // the tile has been read
-    if (++stage == kStages) stage = 0;
   }
   copy_async_wait<0>();
   __syncthreads();
@@ -721,7 +757,7 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, int D>
+template <int D>
 int launch_select(const SelectParams& p0, cudaStream_t stream) {
   SelectParams p = p0;
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
@@ -742,7 +778,10 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   warps = std::max(warps, 4);
   const int smem = bytes(warps);
   if (smem > most) return PA_ERR_UNSUPPORTED;
-  const auto kernel = ranks > 1 ? select_kernel<T, D, true> : select_kernel<T, D, false>;
+  const bool one = p.head_tiles == 1;
+  const auto kernel = ranks > 1 ? one ? select_kernel<D, true, true> : select_kernel<D, true, false>
+                      : one    ? select_kernel<D, false, true>
+                               : select_kernel<D, false, false>;
   if (smem > 47 * 1024 && set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), most) != PA_OK)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -755,7 +794,7 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -915,23 +954,19 @@ int pa_select_blocks(const void* q, const int8_t* summaries, const float* summar
   p.num_sink = num_sink;
   p.num_recent = num_recent;
   p.head_tiles = (p.group + 7) / 8;
+  p.dtype = dtype;
   if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define PA_SEL_D(D)                                                                          \
-  (dtype == PA_F32   ? launch_select<float, D>(p, s)                                         \
-   : dtype == PA_F16 ? launch_select<__half, D>(p, s)                                        \
-                     : launch_select<__nv_bfloat16, D>(p, s))
   switch (head_dim) {
-    case 32: return PA_SEL_D(32);
-    case 64: return PA_SEL_D(64);
-    case 96: return PA_SEL_D(96);
-    case 128: return PA_SEL_D(128);
-    case 160: return PA_SEL_D(160);
-    case 192: return PA_SEL_D(192);
-    case 224: return PA_SEL_D(224);
-    default: return PA_SEL_D(256);
+    case 32: return launch_select<32>(p, s);
+    case 64: return launch_select<64>(p, s);
+    case 96: return launch_select<96>(p, s);
+    case 128: return launch_select<128>(p, s);
+    case 160: return launch_select<160>(p, s);
+    case 192: return launch_select<192>(p, s);
+    case 224: return launch_select<224>(p, s);
+    default: return launch_select<256>(p, s);
   }
-#undef PA_SEL_D
 }
 
 }  // extern "C"

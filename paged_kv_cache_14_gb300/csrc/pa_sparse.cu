@@ -480,19 +480,22 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
   sparse_join<T, D>(p, w, &so[0][0][0], sl[1], sl[0]);
 }
 
-// fp32 on CUDA cores, exact fp32 arithmetic: a CTA takes 16 tokens at a time,
-// scores them pair by pair of (head, token) and adds their values, a thread to
-// each dimension, for 8 query heads.
+// fp32 on CUDA cores, exact fp32 arithmetic, for 8 query heads: a CTA scores 16
+// tokens at a time, a (head, token) pair a thread, and adds their values, a
+// dimension (or two) a thread, while copies bring the next 16 tokens.
+constexpr int sparse_f32_smem(int d) { return (8 * d + 8 * (d + 4) + 2 * 16 * (d + 4) + 2 * 16 * d) * 4; }
+
 template <int D>
 __global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __grid_constant__ SparseParams p) {
   constexpr int H = 8, TOK = 16, ST = D + 4;
   constexpr int DT = (D + kSparseF32Threads - 1) / kSparseF32Threads;  // dimensions of a thread
   extern __shared__ __align__(16) uint8_t smem[];
   float* so = reinterpret_cast<float*>(smem);  // [H][D]
-  float* sq = so + H * D;          // [H][ST]
-  float* sk = sq + H * ST;         // [TOK][ST]
-  float* sv = sk + TOK * ST;       // [TOK][D]
-  __shared__ float ss[H][TOK], sm[H], sl[H], sf[H];
+  float* sq = so + H * D;                      // [H][ST]
+  float* sk = sq + H * ST;                     // [2][TOK][ST]
+  float* sv = sk + 2 * TOK * ST;               // [2][TOK][D]
+  __shared__ __align__(16) float ss[TOK][H];
+  __shared__ float sm[H], sl[H], sf[H];
   const int tid = threadIdx.x;
   SparseRow w = sparse_row(p, H);
   sparse_check(p, w);
@@ -508,29 +511,38 @@ __global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __g
   for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int i = 0; i < DT; ++i) acc[h][i] = 0.f;
-  for (int x = w.rank; x < items; x += w.ranks) {
-    const int sub = halves == 2 ? x & 1 : 0;
-    // (Every thread asks: the answer is the same.)
-    const int2 it = sparse_item(p, w, sparse_entry(p, w, x / halves), sub);
-    if (it.y == 0) continue;
-    const int64_t at = (((int64_t)it.x * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * D;
-    __syncthreads();
-    for (int y = tid; y < it.y * (D / 4); y += kSparseF32Threads) {
-      const int t = y / (D / 4), d = (y - t * (D / 4)) * 4;
-      *reinterpret_cast<float4*>(sk + t * ST + d) =
-          *reinterpret_cast<const float4*>(static_cast<const float*>(p.k_cache) + at + t * D + d);
-      *reinterpret_cast<float4*>(sv + t * D + d) =
-          *reinterpret_cast<const float4*>(static_cast<const float*>(p.v_cache) + at + t * D + d);
+  // Item x's tokens into a half of the buffers (every thread asks what it is:
+  // the answer is the same); the number of them.
+  auto fetch = [&](int x, int half) {
+    int tokens = 0;
+    if (x < items) {
+      const int sub = halves == 2 ? x & 1 : 0;
+      const int2 it = sparse_item(p, w, sparse_entry(p, w, x / halves), sub);
+      tokens = it.y;
+      const int64_t at = (((int64_t)it.x * p.num_kv_heads + w.head) * p.block_size + 16 * sub) * D;
+      for (int y = tid; y < tokens * (D / 4); y += kSparseF32Threads) {
+        const int t = y / (D / 4), d = (y - t * (D / 4)) * 4;
+        copy_async16(smem_u32(sk + (half * TOK + t) * ST + d), static_cast<const float*>(p.k_cache) + at + t * D + d);
+        copy_async16(smem_u32(sv + (half * TOK + t) * D + d), static_cast<const float*>(p.v_cache) + at + t * D + d);
+      }
     }
+    copy_async_commit();
+    return tokens;
+  };
+  int half = 0, tokens = fetch(w.rank, 0);
+  for (int x = w.rank; x < items; x += w.ranks, half ^= 1) {
+    const int next = fetch(x + w.ranks, half ^ 1);
+    copy_async_wait<1>();
     __syncthreads();
+    const float *kt = sk + half * TOK * ST, *vt = sv + half * TOK * D;
     {
       const int t = tid % TOK, h = tid / TOK;  // 16 tokens x 8 heads
       float s = neg_inf();
-      if (t < it.y && h < w.heads) {
+      if (t < tokens && h < w.heads) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int d = 0; d < D; d += 4) {
-          const float4 x4 = *reinterpret_cast<const float4*>(sk + t * ST + d);
+          const float4 x4 = *reinterpret_cast<const float4*>(kt + t * ST + d);
           const float4 y4 = *reinterpret_cast<const float4*>(sq + h * ST + d);
           a.x = fmaf(x4.x, y4.x, a.x);
           a.y = fmaf(x4.y, y4.y, a.y);
@@ -548,7 +560,7 @@ __global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __g
       float sum = e;
 #pragma unroll
       for (int i = 1; i < TOK; i <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-      ss[h][t] = e;
+      ss[t][h] = e;
       __syncwarp();
       if (t == 0) {
         const float f = old == neg_inf() ? 1.f : exp2f(old - ref);
@@ -563,16 +575,22 @@ __global__ void __launch_bounds__(kSparseF32Threads) sparse_f32_kernel(const __g
       const float f = sf[h];
 #pragma unroll
       for (int i = 0; i < DT; ++i) acc[h][i] *= f;
-      for (int t = 0; t < it.y; ++t) {
-        const float e = ss[h][t];
+    }
+    for (int t = 0; t < tokens; ++t) {
+      const float4 e0 = *reinterpret_cast<const float4*>(&ss[t][0]), e1 = *reinterpret_cast<const float4*>(&ss[t][4]);
+      const float e[H] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          const int d = tid + i * kSparseF32Threads;
-          if (d < D) acc[h][i] = fmaf(e, sv[t * D + d], acc[h][i]);
-        }
+      for (int i = 0; i < DT; ++i) {
+        const int d = tid + i * kSparseF32Threads;
+        const float v = d < D ? vt[t * D + d] : 0.f;
+#pragma unroll
+        for (int h = 0; h < H; ++h) acc[h][i] = fmaf(e[h], v, acc[h][i]);
       }
     }
+    tokens = next;
+    __syncthreads();  // the buffers' half and the weights have been read
   }
+  copy_async_wait<0>();
 #pragma unroll
   for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -597,13 +615,13 @@ int launch_sparse(void (*kernel)(SparseParams), const SparseParams& p, int ranks
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <int D>
 int launch_sparse_f32(const SparseParams& p, cudaStream_t stream) {
-  constexpr int smem = (8 * D + 24 * (D + 4) + 16 * D) * 4;
+  constexpr int smem = sparse_f32_smem(D);
   if (smem > 40 * 1024 &&
       set_max_dynamic_smem(reinterpret_cast<const void*>(sparse_f32_kernel<D>), smem) != PA_OK)
     return PA_ERR_CUDA;
