@@ -178,6 +178,17 @@ inline CascadeWorkspace cascade_workspace_layout(int64_t num_seqs, int64_t num_g
   return w;
 }
 
+// CTAs of a row (one cluster, a power of two up to 8, `most` at most) where
+// `rows` rows share `places` of CTAs: as many as leave each CTA a place. More, so
+// that every place has its share, cost more than they balance: 64 rows on 152
+// SMs took 37 us with 2 CTAs each (select, 8 x 131072 tokens), 38 with 4, 39
+// with 8, and 42 to 44 with 3, 5 and 7, whose clusters do not pack.
+inline int cluster_ranks(int64_t rows, int64_t places, int64_t most) {
+  int r = 1;
+  while (r < 8 && 2 * r <= most && rows * r * 2 <= places) r *= 2;
+  return r;
+}
+
 // Returns the device status word of the current device (nullptr on error).
 int* device_status_ptr();
 int num_sms_current_device();

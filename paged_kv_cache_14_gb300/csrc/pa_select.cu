@@ -332,8 +332,9 @@ struct SelectParams {
   int* status;
 };
 
-constexpr int kSelectMaxWarps = 16;
-constexpr int kSelectRoom = 24;  // warps that an SM's registers and shared memory hold
+constexpr int kSelectMaxWarps = 16;  // (24: 41 us for 8 x 131072 tokens; 16: 37)
+// Warps that an SM's registers and shared memory hold.
+constexpr int select_room(int d) { return d <= 128 ? 24 : 16; }
 constexpr int kSelectMaxCluster = 8;
 constexpr int kSelectTile = 16;       // blocks of one matrix product
 constexpr int kSelectStages = 2;      // tiles of a warp in shared memory: in use, on its way
@@ -409,7 +410,7 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 // row, which change places so that a fragment's rows take all banks. ONE: the
 // group's heads fit one tile of 8, whose codes then stay in registers.
 template <int D, bool CL, bool ONE>
-__global__ void __launch_bounds__(D <= 128 ? 32 * kSelectRoom : 32 * kSelectMaxWarps)
+__global__ void __launch_bounds__(32 * select_room(D))
     select_kernel(const __grid_constant__ SelectParams p) {
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kRow = 2 * D, kPieces = kRow / 16, kTile = kSelectTile * kRow + kSelectTile * 4;
@@ -762,19 +763,17 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   SelectParams p = p0;
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads;
   const int blocks = (p.max_seq_len - 1) / p.block_size + 1;
-  // CTAs of a row (a power of two): as many as keep the batch within two an SM
-  // and leave each 128 blocks, or as shared memory takes to hold the scores;
-  // then the warps of each so that all CTAs run at once.
+  // CTAs of a row: of 128 blocks at least, or as many as shared memory takes to
+  // hold the scores; then the warps of each so that all CTAs run at once.
   const int sms = num_sms_current_device(), most = 220 * 1024;
-  int ranks = 1;
-  while (ranks < kSelectMaxCluster && rows * ranks <= sms && blocks >= ranks * 2 * 128) ranks *= 2;
+  int ranks = cluster_ranks(rows, sms, blocks / 128);
   auto scores = [&] { return ((blocks + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile; };
   const int queries = p.head_tiles * 8 * (select_query_bytes(D) + 4);
   auto bytes = [&](int warps) { return select_ring_bytes(D, warps) + queries + scores() * 4; };
   while (ranks < kSelectMaxCluster && bytes(4) > most) ranks *= 2;
   const int64_t per_sm = (rows * ranks + sms - 1) / sms;
-  int warps = (int)std::min<int64_t>(std::min(kSelectMaxWarps, scores() / kSelectTile), kSelectRoom / per_sm);
-  while (warps > 4 && bytes(warps) > most / std::min<int64_t>(per_sm, kSelectRoom / 4)) --warps;
+  int warps = (int)std::min<int64_t>(std::min(kSelectMaxWarps, scores() / kSelectTile), select_room(D) / per_sm);
+  while (warps > 4 && bytes(warps) > most / std::min<int64_t>(per_sm, select_room(D) / 4)) --warps;
   warps = std::max(warps, 4);
   const int smem = bytes(warps);
   if (smem > most) return PA_ERR_UNSUPPORTED;

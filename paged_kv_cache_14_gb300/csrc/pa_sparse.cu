@@ -43,9 +43,8 @@ struct SparseParams {
   int* status;
 };
 
-constexpr int kSparseMaxWarps = 8;
+constexpr int kSparseMaxWarps = 12;
 constexpr int kSparseF32Threads = 128;
-constexpr int kSparseMaxCluster = 8;
 // Tiles (K and V) of a warp in shared memory, the one in use among them.
 constexpr int sparse_stages(int tile_bytes) { return 8192 / tile_bytes; }
 constexpr float kMoveAt = 8.f;  // log2 of the weight that moves the reference
@@ -625,13 +624,10 @@ int launch_sparse_f32(const SparseParams& p, cudaStream_t stream) {
   if (smem > 40 * 1024 &&
       set_max_dynamic_smem(reinterpret_cast<const void*>(sparse_f32_kernel<D>), smem) != PA_OK)
     return PA_ERR_CUDA;
-  // CTAs of a row: as many as keep the batch within four per SM and leave each
-  // four items.
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
   const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
-  int ranks = 1;
-  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 4 * num_sms_current_device() && items >= ranks * 2 * 4)
-    ranks *= 2;
+  const int sms = num_sms_current_device();
+  const int ranks = cluster_ranks(rows, 4 * sms, items / 4);  // (four CTAs an SM)
   return launch_sparse(sparse_f32_kernel<D>, p, ranks, kSparseF32Threads / 32, smem, stream);
 }
 
@@ -640,19 +636,17 @@ int launch_sparse_tc(const SparseParams& p, cudaStream_t stream) {
   constexpr int tile = 16 * D * (KV8 ? 1 : 2), warp_smem = sparse_stages(tile) * 2 * tile;
   constexpr int kRoom = NT == 1 ? 12 : 8;  // warps that an SM's registers (and shared memory) hold
   static_assert(warp_smem >= 8 * NT * D * 4, "a warp's output fits into its tiles");
-  // All CTAs at once, if an SM's warps suffice: a row's CTAs (a power of two)
-  // and the warps of each so that every SM gets its share and no warp less
-  // than two items.
+  // All CTAs at once, if an SM's warps suffice: the CTAs of a row (of 8 items at
+  // least) and the warps of each, no warp with less than two items.
   const int sms = num_sms_current_device();
   const int64_t rows = (int64_t)p.num_seqs * p.num_kv_heads * p.row_groups;
   const int64_t items = (int64_t)p.max_list_len * (p.block_size / 16);
-  int ranks = 1;
-  while (ranks < kSparseMaxCluster && rows * ranks * 2 <= 2 * sms && items >= ranks * 8) ranks *= 2;
+  const int ranks = cluster_ranks(rows, sms, items / 8);
   const int64_t per_sm = (rows * ranks + sms - 1) / sms;
-  int warps = (int)std::min<int64_t>(kSparseMaxWarps, per_sm * 2 <= kRoom ? kRoom / per_sm : 4);
+  int warps = (int)std::min<int64_t>(kRoom, per_sm * 2 <= kRoom ? kRoom / per_sm : 4);
   warps = (int)std::min<int64_t>(warps, std::max<int64_t>(2, (items + 2 * ranks - 1) / (2 * ranks)));
   const auto kernel = sparse_kernel<T, KV8, D, NT>;
-  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSparseMaxWarps * warp_smem) != PA_OK)
+  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kRoom * warp_smem) != PA_OK)
     return PA_ERR_CUDA;
   return launch_sparse(kernel, p, ranks, warps, warps * warp_smem, stream);
 }
