@@ -463,15 +463,75 @@ __global__ void __launch_bounds__(32 * select_room(D))
   const int chunk = ((some + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile;
   const int lo = min(rank * chunk, some), mine = min(chunk, some - lo);
 
-  // A block's number lies where its score will be (by copies of their own, all
-  // under way at once; behind the end: the last one's).
+  // The first tile's blocks from the table (behind the end: the last block).
+  // All blocks' numbers lie where their scores will be, by copies of their own,
+  // so that no other tile waits for the table.
+  const int32_t* from_table = table + sink + lo;
+  const uint32_t first_id =
+      mine > warp * kSelectTile && lane < kSelectTile ? from_table[min(warp * kSelectTile + lane, mine - 1)] : 0u;
   for (int i = tid; i < (mine + kSelectTile - 1) / kSelectTile * kSelectTile; i += threads)
-    copy_async4(smem_u32(&keys[i]), table + sink + lo + min(i, mine - 1));
+    copy_async4(smem_u32(&keys[i]), from_table + min(i, mine - 1));
   copy_async_commit();
   if (tid == 0) {
     range[0] = 0xffffffffu;
     range[1] = 0;
   }
+  const int step = warps * kSelectTile;
+  uint8_t* ring = smem + warp * kSelectStages * kTile;
+  // The tile at b0 into a stage.
+  const uint32_t block_bytes = p.num_kv_heads * kRow;
+  const int8_t* summaries = p.summaries + (int64_t)head * kRow;
+  auto fetch = [&](int b0, int stage, bool first) {
+    if (b0 < mine) {
+      const uint32_t to = smem_u32(ring + stage * kTile);
+      // Instruction i takes whole rows, and a lane its neighbours in the next
+      // ones, so that four of its blocks' numbers are one load.
+      constexpr int kCopies = kSelectTile * kPieces / 32;
+      const uint32_t most = p.num_blocks - 1;
+      if constexpr (kCopies % 4 == 0 && 32 % kPieces == 0) {
+        const int row0 = lane / kPieces * kCopies, piece = lane % kPieces;
+        const int8_t* from = summaries + piece * 16;
+#pragma unroll
+        for (int i = 0; i < kCopies; i += 4) {
+          uint32_t ids[4];
+          if (first) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ids[k] = __shfl_sync(kAll, first_id, row0 + i + k);
+          } else {
+            const uint4 id = *reinterpret_cast<const uint4*>(keys + b0 + row0 + i);
+            ids[0] = id.x;
+            ids[1] = id.y;
+            ids[2] = id.z;
+            ids[3] = id.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            copy_async16(to + (row0 + i + k) * kRow + (kSwap ? piece ^ (i + k & 1) << 2 : piece) * 16,
+                         from + (uint64_t)min(ids[k], most) * block_bytes);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
+          copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
+                       summaries + (uint64_t)min(first ? __shfl_sync(kAll, first_id, row) : keys[b0 + row], most) *
+                                       block_bytes + piece * 16);
+        }
+      }
+      if (lane < kSelectTile) {
+        const uint32_t s = to + kSelectTile * kRow + lane * 4;
+        const uint32_t id = first ? first_id : keys[b0 + lane];
+        if (id < (uint32_t)p.num_blocks) {
+          copy_async4(s, p.scales + (int64_t)id * p.num_kv_heads + head);
+        } else {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s), "r"(kNoBlock) : "memory");
+          record_error(p.status, PA_ERR_BLOCK_OOB);
+        }
+      }
+    }
+    copy_async_commit();
+  };
+  fetch(warp * kSelectTile, 0, true);
   // The queries' codes, their positive and their negative part.
   for (int h = warp; h < p.head_tiles * 8; h += warps) {
     if (h != warp) query(h);
@@ -492,55 +552,8 @@ __global__ void __launch_bounds__(32 * select_room(D))
     }
     if (lane == 0) q_scale[h] = scale;
   }
-  copy_async_wait<0>();
+  copy_async_wait<1>();  // the table's entries (the first tile may still be on its way)
   __syncthreads();
-
-  const int step = warps * kSelectTile;
-  uint8_t* ring = smem + warp * kSelectStages * kTile;
-  // The tile at b0 into a stage.
-  const uint32_t block_bytes = p.num_kv_heads * kRow;
-  const int8_t* summaries = p.summaries + (int64_t)head * kRow;
-  auto fetch = [&](int b0, int stage) {
-    if (b0 < mine) {
-      const uint32_t to = smem_u32(ring + stage * kTile);
-      // Instruction i takes whole rows, and a lane its neighbours in the next
-      // ones, so that four of its blocks' numbers are one load.
-      constexpr int kCopies = kSelectTile * kPieces / 32;
-      const uint32_t most = p.num_blocks - 1;
-      if constexpr (kCopies % 4 == 0 && 32 % kPieces == 0) {
-        const int row0 = lane / kPieces * kCopies, piece = lane % kPieces;
-        const int8_t* from = summaries + piece * 16;
-#pragma unroll
-        for (int i = 0; i < kCopies; i += 4) {
-          const uint4 id = *reinterpret_cast<const uint4*>(keys + b0 + row0 + i);
-          const uint32_t ids[4] = {id.x, id.y, id.z, id.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            copy_async16(to + (row0 + i + k) * kRow + (kSwap ? piece ^ (i + k & 1) << 2 : piece) * 16,
-                         from + (uint64_t)min(ids[k], most) * block_bytes);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          const int x = i * 32 + lane, row = x / kPieces, piece = x - row * kPieces;
-          copy_async16(to + row * kRow + (kSwap ? piece ^ (row & 1) << 2 : piece) * 16,
-                       summaries + (uint64_t)min(keys[b0 + row], most) * block_bytes + piece * 16);
-        }
-      }
-      if (lane < kSelectTile) {
-        const uint32_t s = to + kSelectTile * kRow + lane * 4;
-        const uint32_t id = keys[b0 + lane];
-        if (id < (uint32_t)p.num_blocks) {
-          copy_async4(s, p.scales + (int64_t)id * p.num_kv_heads + head);
-        } else {
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s), "r"(kNoBlock) : "memory");
-          record_error(p.status, PA_ERR_BLOCK_OOB);
-        }
-      }
-    }
-    copy_async_commit();
-  };
-  fetch(warp * kSelectTile, 0);
   uint4 qf[ONE ? D / 32 : 1];
   float qs0 = 0.f, qs1 = 0.f;
   if constexpr (ONE) {
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(32 * select_room(D))
     for (int t = 0; t < 2; ++t) {
       // Lane (r, c): 16 bytes of each 64 of the rows of blocks r and r + 8.
       best[t][0] = best[t][1] = none;
-      fetch(b0 + (t + 1) * step, t ^ 1);
+      fetch(b0 + (t + 1) * step, t ^ 1, false);
       copy_async_wait<1>();
       __syncwarp();
       if (b0 + t * step < mine) {

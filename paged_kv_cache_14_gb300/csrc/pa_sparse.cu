@@ -44,6 +44,7 @@ struct SparseParams {
 };
 
 constexpr int kSparseMaxWarps = 12;
+constexpr int kSparseMaxCluster = 8;
 constexpr int kSparseF32Threads = 128;
 // Tiles (K and V) of a warp in shared memory, the one in use among them.
 constexpr int sparse_stages(int tile_bytes) { return 8192 / tile_bytes; }
@@ -133,6 +134,22 @@ __device__ __forceinline__ int2 sparse_item(const SparseParams& p, const SparseR
   return make_int2(blk, min(16, max(0, w.len - lb * p.block_size - 16 * sub)));
 }
 
+// One output of four dimensions: a row without blocks is zeros.
+template <typename T, int D>
+__device__ __forceinline__ void sparse_store(const SparseParams& p, const SparseRow& w, int h, int d, float4 acc,
+                                             float sum) {
+  const float inv = w.entries > 0 ? 1.f / sum : 0.f;
+  acc.x *= inv;
+  acc.y *= inv;
+  acc.z *= inv;
+  acc.w *= inv;
+  store4(static_cast<T*>(p.out) + ((int64_t)w.seq * p.num_q_heads + w.first_head + h) * D + d, acc);
+}
+
+// A part's weight in a join where `top` is the largest reference. (A part that
+// saw no score has zeros, or a NaN to keep.)
+__device__ __forceinline__ float part_weight(float m, float top) { return m == neg_inf() ? 1.f : exp2f(m - top); }
+
 // Joins a cluster's CTAs: o [heads][D], m and l in every CTA's shared memory
 // (o relative to m); each CTA writes its share of the output. Ends with a
 // cluster barrier, after which shared memory may go.
@@ -143,25 +160,32 @@ __device__ __forceinline__ void sparse_join(const SparseParams& p, const SparseR
   const int quads = w.heads * (D / 4);
   for (int x = w.rank * blockDim.x + threadIdx.x; x < quads; x += w.ranks * blockDim.x) {
     const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
+    // All CTAs' parts at once.
+    float mi[kSparseMaxCluster], li[kSparseMaxCluster];
+    float4 v[kSparseMaxCluster];
+#pragma unroll
+    for (int i = 0; i < kSparseMaxCluster; ++i) {
+      if (i >= w.ranks) break;
+      mi[i] = remote_f32(remote(m + h, i));
+      li[i] = remote_f32(remote(l + h, i));
+      v[i] = remote_f32x4(remote(o + h * D + d, i));
+    }
     float top = neg_inf(), sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < w.ranks; ++i) top = fmaxf(top, remote_f32(remote(m + h, i)));
-    for (int i = 0; i < w.ranks; ++i) {
-      const float mi = remote_f32(remote(m + h, i));
-      const float f = mi == neg_inf() ? 1.f : exp2f(mi - top);  // (without tokens: zeros, or a NaN to keep)
-      const float4 v = remote_f32x4(remote(o + h * D + d, i));
-      sum += f * remote_f32(remote(l + h, i));
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
+#pragma unroll
+    for (int i = 0; i < kSparseMaxCluster; ++i)
+      if (i < w.ranks) top = fmaxf(top, mi[i]);
+#pragma unroll
+    for (int i = 0; i < kSparseMaxCluster; ++i) {
+      if (i >= w.ranks) break;
+      const float f = part_weight(mi[i], top);
+      sum += f * li[i];
+      acc.x += f * v[i].x;
+      acc.y += f * v[i].y;
+      acc.z += f * v[i].z;
+      acc.w += f * v[i].w;
     }
-    const float inv = w.entries > 0 ? 1.f / sum : 0.f;  // a row without blocks: zeros
-    acc.x *= inv;
-    acc.y *= inv;
-    acc.z *= inv;
-    acc.w *= inv;
-    store4(static_cast<T*>(p.out) + ((int64_t)w.seq * p.num_q_heads + w.first_head + h) * D + d, acc);
+    sparse_store<T, D>(p, w, h, d, acc, sum);
   }
   cluster_sync();
 }
@@ -183,7 +207,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
   constexpr int KS = D / 16;                  // steps of the score product
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' tiles, later their outputs
   float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
-  __shared__ float sm[kSparseMaxWarps][H], sl[kSparseMaxWarps][H];
+  __shared__ float sm[kSparseMaxWarps][H], sl[kSparseMaxWarps][H], cta_m[H], cta_l[H];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
   SparseRow w = sparse_row(p, H);
   const int halves = p.block_size >> 4;  // items of a block
@@ -192,32 +216,27 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
 
   // The queries' fragments: head r (and r + 8), 16 bytes as the keys lie.
   uint32_t qf[NT][KS][2];
-  float mul[NT][2];  // of the scores of heads 2 c, 2 c + 1
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int h = n * 8 + r;
     const T* q = static_cast<const T*>(p.q) + ((int64_t)w.seq * p.num_q_heads + w.first_head + (h < w.heads ? h : 0)) * D;
-    if constexpr (KV8 == 0) {
 #pragma unroll
-      for (int j = 0; j < KP; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4*>(q + 32 * j + 8 * c);
-        qf[n][2 * j][0] = x.x;
-        qf[n][2 * j][1] = x.y;
-        qf[n][2 * j + 1][0] = x.z;
-        qf[n][2 * j + 1][1] = x.w;
-      }
+    for (int j = 0; j < D / 32; ++j) {
+      // (Two 16-byte pieces of an 8-bit row's 16 dimensions, or one of 8.)
+      const uint4 x = *reinterpret_cast<const uint4*>(KV8 ? q + 64 * (j / 2) + 16 * c + 8 * (j & 1) : q + 32 * j + 8 * c);
+      qf[n][2 * j][0] = x.x;
+      qf[n][2 * j][1] = x.y;
+      qf[n][2 * j + 1][0] = x.z;
+      qf[n][2 * j + 1][1] = x.w;
+    }
+  }
+  float mul[NT][2];  // of the scores of heads 2 c, 2 c + 1
+  // (Done when the first tiles are on their way.)
+  auto scale_queries = [&] {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       mul[n][0] = mul[n][1] = p.scale_log2;
-    } else {
-      float f = 1.f;
-#pragma unroll
-      for (int j = 0; j < KP; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * c);
-        const uint4 y = *reinterpret_cast<const uint4*>(q + 64 * j + 16 * c + 8);
-        const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) qf[n][4 * j + i / 2][i & 1] = v[i];
-      }
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      if constexpr (KV8 != 0 && std::is_same<T, __nv_bfloat16>::value) {
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k)
@@ -231,8 +250,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
         // The row's largest value goes to [2^14, 2^15): what that puts below
         // fp16's normal numbers is 2^28 times smaller.
         const int e = top > 0.f ? min(max((__float_as_int(top) >> 23) - 127 - 14, -126), 113) : 0;
-        const float down = __int_as_float((127 - e) << 23);
-        f = __int_as_float((127 + e) << 23);
+        const float down = __int_as_float((127 - e) << 23), up = __int_as_float((127 + e) << 23);
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -240,11 +258,11 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
             const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qf[n][k][i]));
             qf[n][k][i] = MmaOp<__half>::pack(v.x * down, v.y * down);
           }
+        mul[n][0] *= __shfl_sync(kAll, up, 8 * c);
+        mul[n][1] *= __shfl_sync(kAll, up, 8 * c + 4);
       }
-      mul[n][0] = p.scale_log2 * __shfl_sync(kAll, f, 8 * c);
-      mul[n][1] = p.scale_log2 * __shfl_sync(kAll, f, 8 * c + 4);
     }
-  }
+  };
 
   float o[NT][MT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -298,6 +316,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+    if (base == me) scale_queries();
     int stage = 0;
     for (int x = 0; x < count; ++x) {
       fetch(x + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
@@ -449,34 +468,32 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
     }
   }
   __syncthreads();
-  // Each warp's weight in the join, in its l's place.
-  if (tid < H) {
-    float top = sm[0][tid], sum = 0.f;
-    for (int i = 1; i < cta_warps; ++i) top = fmaxf(top, sm[i][tid]);
-    for (int i = 0; i < cta_warps; ++i) {
-      // (A warp that saw no score: zeros, or a NaN to keep.)
-      const float f = sm[i][tid] == neg_inf() ? 1.f : exp2f(sm[i][tid] - top);
-      sum += f * sl[i][tid];
-      sm[i][tid] = f;
-    }
-    sl[0][tid] = sum;
-    sl[1][tid] = top;
-  }
-  __syncthreads();
+  // A thread takes four dimensions of a head; a CTA alone writes them out.
   for (int x = tid; x < H * D / 4; x += blockDim.x) {
-    const int h = x / (D / 4);
+    const int h = x / (D / 4), d = (x - h * (D / 4)) * 4;
+    float top = neg_inf(), sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < cta_warps; ++i) top = fmaxf(top, sm[i][h]);
     for (int i = 0; i < cta_warps; ++i) {
-      const float f = sm[i][h];
+      const float f = part_weight(sm[i][h], top);
       const float4 v = reinterpret_cast<const float4*>(so[i])[x];
+      sum += f * sl[i][h];
       acc.x = fmaf(f, v.x, acc.x);
       acc.y = fmaf(f, v.y, acc.y);
       acc.z = fmaf(f, v.z, acc.z);
       acc.w = fmaf(f, v.w, acc.w);
     }
-    reinterpret_cast<float4*>(so[0])[x] = acc;
+    if (w.ranks == 1) {
+      if (h < w.heads) sparse_store<T, D>(p, w, h, d, acc, sum);
+    } else {
+      reinterpret_cast<float4*>(so[0])[x] = acc;
+      if (d == 0) {
+        cta_m[h] = top;
+        cta_l[h] = sum;
+      }
+    }
   }
-  sparse_join<T, D>(p, w, &so[0][0][0], sl[1], sl[0]);
+  if (w.ranks > 1) sparse_join<T, D>(p, w, &so[0][0][0], cta_m, cta_l);
 }
 
 // fp32 on CUDA cores, exact fp32 arithmetic, for 8 query heads: a CTA scores 16
