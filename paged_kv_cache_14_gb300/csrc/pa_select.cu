@@ -247,7 +247,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 constexpr int kSummaryMaxStages = 8;
 
 // Each warp for itself: it finds 32 items at a time, a lane each, keeps the
-// next tiles on their way into shared memory and takes them in order.
+// next tiles on their way into shared memory and takes them in order. Bound by
+// HBM: the blocks of 4 x 65536 tokens (428 MB with what is written) in 74 us,
+// 5.8 TB/s; over e4m3 pools by the widening and encoding (61 us for half the
+// bytes). One tile a warp from global memory into registers took 92 us. A decode
+// step's call (64 sequences, a block each) is a chain of latencies, 3 us.
 template <typename R, int D, int KV8>
 __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const __grid_constant__ SummaryParams p) {
   constexpr unsigned kAll = 0xffffffffu;
@@ -332,9 +336,9 @@ struct SelectParams {
   int* status;
 };
 
-constexpr int kSelectMaxWarps = 16;  // (24: 41 us for 8 x 131072 tokens; 16: 37)
-// Warps that an SM's registers and shared memory hold.
-constexpr int select_room(int d) { return d <= 128 ? 24 : 16; }
+// Warps of a CTA, and of an SM: 128 registers each. (24 of 80 registers, which
+// spill: 41 us for 8 x 131072 tokens where 16 take 37.)
+constexpr int kSelectMaxWarps = 16;
 constexpr int kSelectMaxCluster = 8;
 constexpr int kSelectTile = 16;       // blocks of one matrix product
 constexpr int kSelectStages = 2;      // tiles of a warp in shared memory: in use, on its way
@@ -405,12 +409,20 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 // span, so that the first splits them well whatever their size, and the
 // search ends when a digit's blocks are all taken (after two digits, mostly).
 //
+// What bounds it is the chain of its phases: for 64 sequences of up to 8192
+// tokens 4 us to the first tile (lengths, table, summaries), 8 to score all
+// (53 MB at HBM's rate), 1 for the digits and 1 for the list, in a call of 22;
+// for 8 of up to 131072 (cluster barriers between the phases) 4, 19 (102 MB;
+// an SM takes 40 GB/s), 5 and 2 in a call of 35. The byte products keep the
+// tensor pipe 64 cycles each where fp16's (m16n8k16, half as deep) take 9, but
+// widening the codes costs what that saves.
+//
 // The summaries come by asynchronous copies, a tile ahead of each warp: 16
 // blocks' rows as they lie, but for the halves of 128 bytes of every other
 // row, which change places so that a fragment's rows take all banks. ONE: the
 // group's heads fit one tile of 8, whose codes then stay in registers.
 template <int D, bool CL, bool ONE>
-__global__ void __launch_bounds__(32 * select_room(D))
+__global__ void __launch_bounds__(32 * kSelectMaxWarps)
     select_kernel(const __grid_constant__ SelectParams p) {
   constexpr unsigned kAll = 0xffffffffu;
   constexpr int kRow = 2 * D, kPieces = kRow / 16, kTile = kSelectTile * kRow + kSelectTile * 4;
@@ -785,8 +797,8 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   auto bytes = [&](int warps) { return select_ring_bytes(D, warps) + queries + scores() * 4; };
   while (ranks < kSelectMaxCluster && bytes(4) > most) ranks *= 2;
   const int64_t per_sm = (rows * ranks + sms - 1) / sms;
-  int warps = (int)std::min<int64_t>(std::min(kSelectMaxWarps, scores() / kSelectTile), select_room(D) / per_sm);
-  while (warps > 4 && bytes(warps) > most / std::min<int64_t>(per_sm, select_room(D) / 4)) --warps;
+  int warps = (int)std::min<int64_t>(std::min(kSelectMaxWarps, scores() / kSelectTile), kSelectMaxWarps / per_sm);
+  while (warps > 4 && bytes(warps) > most / std::min<int64_t>(per_sm, kSelectMaxWarps / 4)) --warps;
   warps = std::max(warps, 4);
   const int smem = bytes(warps);
   if (smem > most) return PA_ERR_UNSUPPORTED;
