@@ -632,16 +632,20 @@ def _arg(t, name: str, dtype, dev: int, shape) -> int:
     _refuse(t, name, dtype, dev, shape)
 
 
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _place(t, name: str, stream) -> tuple[int, int, object]:
     """The current device, the stream's handle, and the stream if it is not
     the current one."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return _here(torch._C._cuda_getDevice(), stream)
+    dev = _device()
+    return (dev, _raw_stream(dev), None) if stream is None else _here(dev, stream)
 
 
 def _here(dev: int, stream) -> tuple[int, int, object]:
-    here = torch._C._cuda_getCurrentRawStream(dev)
+    here = _raw_stream(dev)
     if stream is None:
         return dev, here, None
     handle = _stream(stream)
@@ -661,8 +665,6 @@ def _scratch(like, shape, dtype, side) -> torch.Tensor:
     launches takes twice torch.empty's time.)"""
     device = like
     if isinstance(like, torch.Tensor):
-        if side is None and like.dtype is dtype and like.shape == shape:
-            return torch.empty_like(like, memory_format=torch.contiguous_format)  # (a third less time)
         device = like.device
     if side is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -671,6 +673,14 @@ def _scratch(like, shape, dtype, side) -> torch.Tensor:
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(here)
     return t
+
+
+def _output(like: torch.Tensor, side) -> torch.Tensor:
+    """A new contiguous tensor of another one's shape and type, as _scratch
+    (empty_like takes a third less time)."""
+    if side is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return _scratch(like, like.shape, like.dtype, side)
 
 
 def pa_decode_tree_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
@@ -954,7 +964,7 @@ def _rope_and_cache(sym, q, k, v, positions, slot_mapping, cos_sin, k_cache, v_c
         shape = (T, hq, D)
         qp, qs = _heads(q, "q", dt, dev, shape)
         if q_out is None:
-            q_out = _scratch(q, shape, dt, side)
+            q_out = _output(q, side)
         op = _arg(q_out, "q_out", dt, dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -1100,7 +1110,7 @@ def _decode_sparse(sym, q, k_cache, v_cache, kv_scales, block_tables, seq_lens, 
     kv = dt if kv_scales is None else torch.uint8
     qp = _arg(q, "q", dt, dev, shape)
     if out is None:
-        out = _scratch(q, shape, dt, side)
+        out = _output(q, side)
     pools = (_arg(k_cache, "k_cache", kv, dev, pool), _arg(v_cache, "v_cache", kv, dev, pool))
     if kv_scales is not None:
         pools += (_arg(kv_scales, "kv_scales", torch.float32, dev, (P, hkv, 2)),)
