@@ -98,12 +98,12 @@ struct RopeParams {
   void* v_cache;
   float* kv_scales;
   int32_t num_blocks, block_size, num_q_heads, num_kv_heads, head_dim;
-  int32_t row_units;  // work units of a row
-  int32_t rows;       // rows of a token: queries, and keys and values of a 16- or 32-bit cache
-  int32_t pass_rows;  // rows that a CTA does at a time
-  int32_t chunks;     // CTAs of a token
+  int32_t row_units;    // work units of a row
+  int32_t rows;         // rows of a token: queries, and keys and values of a 16- or 32-bit cache
+  int32_t pass_rows;    // rows that a CTA does at a time
+  int32_t chunks;       // CTAs of a token
   uint32_t cache_ctas;  // 8-bit caches: CTAs that write them
-  int32_t group;      // 8-bit caches: tokens of a warp
+  int32_t group;        // 8-bit caches: tokens of a warp
   int* status;
 };
 
@@ -113,8 +113,7 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
-// Where a token goes: its slot (-1: it is skipped) and its row of the table.
-// (Both are asked for at once.)
+// A token's slot (-1: it is skipped) and position. (Both are asked for at once.)
 struct RopePlace {
   int64_t slot;
   int32_t pos;

@@ -90,7 +90,6 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 }
 
 struct HalfRange {
-  using T2 = __half2;
   __device__ __forceinline__ static uint32_t top(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -340,12 +339,22 @@ struct SelectParams {
 // spill: 41 us for 8 x 131072 tokens where 16 take 37.)
 constexpr int kSelectMaxWarps = 16;
 constexpr int kSelectMaxCluster = 8;
-constexpr int kSelectTile = 16;       // blocks of one matrix product
-constexpr int kSelectStages = 2;      // tiles of a warp in shared memory: in use, on its way
-constexpr int kDigit = 9;            // bits of a digit
-constexpr int kBins = 1 << kDigit;    // its values, a 32nd of them to a lane
-constexpr int kPasses = 4;            // digits of a score
+constexpr int kSelectTile = 16;    // blocks of one matrix product
+constexpr int kSelectStages = 2;   // tiles of a warp in shared memory: in use, on its way
+constexpr int kDigit = 9;          // bits of a digit
+constexpr int kBins = 1 << kDigit; // its values, a 32nd of them to a lane
+constexpr int kPasses = 4;         // digits of a score
 constexpr int kLaneBins = kBins / 32 + 4;  // a lane's bins are apart by 16 bytes more, in other banks
+constexpr uint32_t kNoBlock = 0xffc00001u; // a scale (a NaN) that marks a block outside the pool
+
+// A query row's codes, 64 bytes on where rows would lie in the same banks.
+constexpr int select_query_bytes(int d) { return 2 * d + (d % 64 == 0 ? 64 : 0); }
+// Shared memory of the tiles on their way, which the counts take over.
+constexpr int select_ring_bytes(int d, int warps) {
+  const int ring = warps * kSelectStages * (kSelectTile * 2 * d + kSelectTile * 4);
+  const int counts = (kPasses + 1) * 32 * kLaneBins * 4;
+  return ring > counts ? ring : counts;
+}
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -357,7 +366,6 @@ __device__ __forceinline__ int remote_int(const void* local, int rank) {
   asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-
 __device__ __forceinline__ uint2 remote_pair(const void* local, int rank) {
   uint32_t a;
   uint2 v;
@@ -374,15 +382,6 @@ __device__ __forceinline__ int4 remote_int4(const void* local, int rank) {
                : "r"(a)
                : "memory");
   return v;
-}
-// Shared memory of the tiles on their way, which the counts take over.
-// A query row's codes, 64 bytes on where rows would lie in the same banks.
-constexpr int select_query_bytes(int d) { return 2 * d + (d % 64 == 0 ? 64 : 0); }
-constexpr uint32_t kNoBlock = 0xffc00001u;  // a scale (a NaN) that marks a block outside the pool
-constexpr int select_ring_bytes(int d, int warps) {
-  const int ring = warps * kSelectStages * (kSelectTile * 2 * d + kSelectTile * 4);
-  const int counts = (kPasses + 1) * 32 * kLaneBins * 4;
-  return ring > counts ? ring : counts;
 }
 __device__ __forceinline__ int bin_at(uint32_t digit) { return digit + digit / (kBins / 32) * 4; }
 
