@@ -770,10 +770,11 @@ int pa_compact_tree_e5m2(void* const* k_caches, void* const* v_caches, float* co
  *             p holds amplitude cos(a_i) at [i] and amplitude sin(a_i) at
  *             [rot_dim/2 + i], a_i = (first_position + p) f_i
  * Angles are reduced in 64-bit fixed point from frequencies held in 64 bits:
- * an entry of amplitude 1 is within 2^-22 of the cosine or sine. Positions lie below 2^31; rot_dim is
- * even, 2 to 256 (PA_ERR_UNSUPPORTED); base > 1, factor > 0 (not read by
- * PA_ROPE_NONE), 0 < low < high and original_len >= 1 (read by PA_ROPE_BANDS
- * and PA_ROPE_RAMP only), amplitude finite (PA_ERR_ARG).
+ * an entry of amplitude 1 is within 2^-22 of the cosine or sine. Positions lie
+ * below 2^31; rot_dim is even, 2 to 256 (PA_ERR_UNSUPPORTED); base > 1, factor
+ * > 0 (not read by PA_ROPE_NONE), 0 < low < high and original_len >= 1 (read by
+ * PA_ROPE_BANDS and PA_ROPE_RAMP only), amplitude and every frequency finite
+ * (PA_ERR_ARG).
  */
 int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions, int32_t rot_dim, double base,
                   int32_t scaling, double factor, int32_t original_len, double low, double high, double amplitude,

@@ -627,9 +627,6 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
   if ((scaling == PA_ROPE_BANDS || scaling == PA_ROPE_RAMP) &&
       (original_len < 1 || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
     return PA_ERR_ARG;
-  if (num_positions == 0) return PA_OK;
-  if (!cos_sin) return PA_ERR_ARG;
-  if (!aligned16(cos_sin)) return PA_ERR_ALIGN;
   const double kTwoPi = 6.283185307179586476925;
   const int half = rot_dim / 2;
   if (scaling == PA_ROPE_BASE && rot_dim > 2) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
@@ -647,10 +644,14 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
     if (scaling == PA_ROPE_RAMP)
       stretched = std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 0.001)));
     f = (1.0 - stretched) * f + stretched * f / factor;
+    if (!std::isfinite(f)) return PA_ERR_ARG;  // (a factor that leaves the doubles' range)
     double turns = f / kTwoPi;
     turns -= std::floor(turns);
     steps.step[i] = turns >= 1.0 ? 0 : (unsigned long long)(turns * 18446744073709551616.0);
   }
+  if (num_positions == 0) return PA_OK;
+  if (!cos_sin) return PA_ERR_ARG;
+  if (!aligned16(cos_sin)) return PA_ERR_ALIGN;
   const int n = half % 4 == 0 ? 4 : 1, rows = kRopeThreads / (half / n);
   // Eight CTAs an SM: a thread reads its steps from the constant bank, one
   // address a lane, which takes as long as several positions do (131072 of 128:

@@ -165,3 +165,14 @@ def test_binding_refuses_cpu_tensors():
         pa.pa_decode_sparse(t, cache, cache, i[None], i, i[None, None], i[None], 1.0)
     with pytest.raises(ValueError):
         pa.pa_rope_table(4, 64, scaling="stretched")
+
+
+def test_table_refuses_infinite_frequencies(lib):
+    """A factor may take base or a frequency out of the doubles' range: base 0
+    makes all but the first frequency infinite, an infinite one makes them 0."""
+    assert _table(lib, kind=2, rot=4, factor=1e-200) == -1
+    for kind in (1, 3, 4):  # (over one original position no pair makes a turn: all frequencies are scaled)
+        assert _table(lib, kind=kind, rot=4, factor=1e-310, orig=1) == -1, kind
+    assert _table(lib, kind=2, rot=4, factor=1e200) == 0
+    for kind in (1, 2, 3, 4):
+        assert _table(lib, kind=kind, factor=0.25, orig=4096) == 0, kind
