@@ -172,7 +172,7 @@ def test_table_refuses_infinite_frequencies(lib):
     makes all but the first frequency infinite, an infinite one makes them 0."""
     assert _table(lib, kind=2, rot=4, factor=1e-200) == -1
     for kind in (1, 3, 4):  # (over one original position no pair makes a turn: all frequencies are scaled)
-        assert _table(lib, kind=kind, rot=4, factor=1e-310, orig=1) == -1, kind
+        assert _table(lib, kind=kind, factor=1e-310, orig=1) == -1, kind
     assert _table(lib, kind=2, rot=4, factor=1e200) == 0
     for kind in (1, 2, 3, 4):
         assert _table(lib, kind=kind, factor=0.25, orig=4096) == 0, kind
