@@ -368,6 +368,8 @@ class SparseStep:
                  kv_scales=None, kv_format: str = "e4m3"):
         if kv_format not in ("e4m3", "e5m2"):
             raise ValueError(f"kv_format {kv_format!r}: e4m3 or e5m2")
+        if not 0 <= scale < float("inf"):  # (the blocks are chosen for large scores of q as it is)
+            raise ValueError(f"scale {scale!r}: finite, not negative")
         self.k_caches, self.v_caches, self.kv_scales = list(k_caches), list(v_caches), kv_scales
         self.suffix = "" if kv_scales is None else "_fp8" if kv_format == "e4m3" else "_e5m2"
         self.block_tables, self.ctx_lens, self.seq_lens = block_tables, ctx_lens, seq_lens

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import paged_kv_cache_14_gb300 as pa
+from paged_kv_cache_14_gb300.step import SparseStep
 
 
 @pytest.fixture(scope="module")
@@ -176,3 +177,16 @@ def test_table_refuses_infinite_frequencies(lib):
     assert _table(lib, kind=2, rot=4, factor=1e200) == 0
     for kind in (1, 2, 3, 4):
         assert _table(lib, kind=kind, factor=0.25, orig=4096) == 0, kind
+
+
+@pytest.mark.parametrize("scale", [-0.1, float("nan"), float("inf")])
+def test_step_refuses_scales(scale):
+    """A negative scale would choose the blocks that weigh least."""
+    i32, f32 = (lambda *s: torch.zeros(s, dtype=torch.int32)), (lambda *s: torch.zeros(s))
+    step = lambda scale: SparseStep(  # noqa: E731
+        k_caches=[f32(4, 1, 16, 32)], v_caches=[f32(4, 1, 16, 32)], block_tables=i32(1, 4), ctx_lens=i32(1),
+        seq_lens=i32(1), new_seq_ids=i32(1), new_positions=i32(1), cos_sin=f32(64, 32), num_q_heads=1,
+        dtype=torch.float32, max_seq_len=64, max_new_tokens=1, max_list_len=2, scale=scale)
+    assert step(0.25).scale == 0.25
+    with pytest.raises(ValueError, match="scale"):
+        step(scale)
