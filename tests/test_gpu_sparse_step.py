@@ -180,3 +180,48 @@ def test_sparse_after_other_changes(lib):
     q = normal(m.rng, 1, HQ, D).bfloat16()
     assert_sparse_close(m.attention(0, q, lens), step.attend(0, q.cuda()))
     assert lib.pa_get_status() == 0
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_offsets_past_32_bits(lib, fmt):
+    """A step on the last blocks of pools of more than 2^32 elements, and a choice
+    among summaries of more than 2^32 bytes, give what the first blocks give."""
+    rng = np.random.default_rng(8)
+    hq, hkv, d, n, near = 16, 8, 128, 300, 24
+    sfx = "" if fmt is None else "_fp8"
+    q, k, v = (normal(rng, n, h, d).bfloat16().cuda() for h in (hq, hkv, hkv))
+    cs = lib.pa_rope_table(n, d)
+    pos, lens, zero = dev(np.arange(n, dtype=np.int32), np.array([n], np.int32), np.zeros(1, np.int32))
+    table = dev(rng.permutation(near)[:(n + 15) // 16].astype(np.int32)[None])
+    results = []
+    for P in (near, (1 << 32) // (hkv * 16 * d) + 100):
+        first = P - near
+        shape, dt = (P, hkv, 16, d), torch.bfloat16 if fmt is None else torch.uint8
+        kc, vc = (torch.empty(shape, dtype=dt, device="cuda") for _ in range(2))
+        sc = () if fmt is None else (torch.zeros(P, hkv, 2, device="cuda"),)
+        for x in (kc, vc):
+            x[first:] = 0
+        t = table + first
+        slots = (t[0].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten()[:n].contiguous()
+        qr = getattr(lib, "pa_rope_and_cache" + sfx)(q, k, v, pos, slots, cs, kc, vc, *sc)
+        codes = torch.zeros(P, hkv, 2, d, dtype=torch.int8, device="cuda")
+        scales = torch.zeros(P, hkv, device="cuda")
+        getattr(lib, "pa_block_summaries" + sfx)(kc, *sc, t, zero, lens, n, codes, scales)
+        last = qr[-1:].contiguous()
+        lists, counts = lib.pa_select_blocks(last, codes, scales, t, lens, n, 16, 8)
+        out = getattr(lib, "pa_decode_sparse" + sfx)(last, kc, vc, *sc, t, lens, lists, counts, d ** -0.5)
+        assert lib.pa_get_status() == 0
+        results.append([x[first:].clone() for x in (kc, vc, *sc, codes, scales)] + [qr, lists, counts, out])
+        del kc, vc, sc
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert results[0][-4].float().isfinite().all() and (results[0][-2] == 8).all()
+    codes, scales = results[0][-6:-4]
+    P = (1 << 32) // (hkv * 2 * d) + 100
+    far_codes = torch.empty(P, hkv, 2, d, dtype=torch.int8, device="cuda")
+    far_scales = torch.empty(P, hkv, device="cuda")
+    far_codes[P - near:], far_scales[P - near:] = codes, scales
+    lists, counts = lib.pa_select_blocks(results[0][-4][-1:].contiguous(), far_codes, far_scales, table + (P - near),
+                                         lens, n, 16, 8)
+    assert lib.pa_get_status() == 0
+    assert torch.equal(lists, results[0][-3]) and torch.equal(counts, results[0][-2])
