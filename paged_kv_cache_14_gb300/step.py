@@ -358,7 +358,8 @@ class SparseStep:
     through slots() and write() in the same way, with pa_chunked_prefill for
     their attention. Where a sequence's blocks change by other means (a copy on
     write, a swap, a compacted draft tree), summarize() makes their summaries
-    again.
+    again. scale is not negative (the blocks are chosen for the largest products
+    with q).
     """
 
     def __init__(self, *, k_caches, v_caches, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
