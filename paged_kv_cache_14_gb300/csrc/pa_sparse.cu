@@ -18,8 +18,9 @@
 // far from the largest fp16), so that most tiles need no maximum over the
 // warp. Warps, then the cluster's CTAs, are joined in a fixed order.
 //
-// 64 sequences of 8 KV heads with 128 listed blocks each (bf16, 533 MB) take 87
-// us, 6.1 TB/s. 8 sequences with 256 blocks (e4m3, 67 MB) take 20: 3 to the
+// 64 sequences of 8 KV heads with 128 listed blocks each (bf16, 533 MB) take 91
+// us, 5.9 TB/s (90 with weights of one bf16, whose error is that of the output's
+// rounding once more). 8 sequences with 256 blocks (e4m3, 67 MB) take 20: 3 to the
 // first tile (lists, table, tiles), 10 for the tiles at HBM's rate, 3 for the
 // joins, and the launch. One user's 64 blocks take 6, nearly all of it such
 // latencies.
@@ -85,6 +86,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+
+// The largest bf16 below a weight (0 of 0). What is left of a weight is above 0
+// then, as the weight is, so that both parts' products with an infinity are that
+// infinity (of weights below 2^-109 the rest may be rounded to 0).
+__device__ __forceinline__ float below(float e) {
+  return __int_as_float((max(__float_as_int(e), 1) - 1) & 0xffff0000);
 }
 
 // The cluster's row: its sequence, KV head and query heads, and its list.
@@ -211,6 +219,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
   constexpr int VP = KV8 ? D / 128 : D / 64;  // 16-byte pieces of a V row for a lane
   constexpr int MT = D / 16;                  // tiles of 16 output dimensions
   constexpr int KS = D / 16;                  // steps of the score product
+  constexpr bool kTwoParts = std::is_same<M, __nv_bfloat16>::value;  // of a weight
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' tiles, later their outputs
   float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
   __shared__ float sm[kSparseMaxWarps][H], sl[kSparseMaxWarps][H], cta_m[H], cta_l[H];
@@ -392,8 +401,9 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
           }
         }
       }
-      // Weights, rounded to the products' type (their sums are taken before).
-      uint32_t pf[NT][2];
+      // Weights in the products' type (their sums are taken before): rounded to
+      // fp16, 2^-11 of a weight, or, since bf16 would lose 2^-8, as two bf16.
+      uint32_t pf[NT][2], rest[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float e[4];
@@ -403,8 +413,16 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
           e[i] = fast_exp2(s[n][i] - (ref == neg_inf() ? 0.f : ref));
           l[n][i & 1] += e[i];
         }
-        pf[n][0] = transposed(MmaOp<M>::pack(e[0], e[1]));
-        pf[n][1] = transposed(MmaOp<M>::pack(e[2], e[3]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (kTwoParts) {
+            const float a = below(e[2 * i]), b = below(e[2 * i + 1]);
+            pf[n][i] = transposed(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632));
+            rest[n][i] = transposed(MmaOp<M>::pack(e[2 * i] - a, e[2 * i + 1] - b));
+          } else {
+            pf[n][i] = transposed(MmaOp<M>::pack(e[2 * i], e[2 * i + 1]));
+          }
+        }
       }
       // Lane elements: word 2 i, 2 i + 1 of token i's dimensions.
       uint32_t v[4][MT];
@@ -435,6 +453,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
         for (int n = 0; n < NT; ++n) {
           if constexpr (KV8 == 0) {
             MmaOp<M>::run(o[n][t], a, pf[n][0], pf[n][1]);
+            if constexpr (kTwoParts) MmaOp<M>::run(o[n][t], a, rest[n][0], rest[n][1]);
           } else {
             float part[4] = {0.f, 0.f, 0.f, 0.f};
             MmaOp<M>::run(part, a, pf[n][0], pf[n][1]);

@@ -1,0 +1,61 @@
+"""How exact the softmax weights of sparse attention over bf16 caches are in the
+second product: scores that carry no error of their own."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_helpers import sparse_batch
+
+pytestmark = pytest.mark.gpu
+
+
+def whole_scores(seed, lens, keep, hq, hkv, d, block):
+    """q and k of -1, 0 and 1, scale 1/16: products and sums of q k are exact."""
+    b = sparse_batch(seed, "bf16", lens, keep, hq, hkv, d, block, ragged=False, scale=1 / 16)
+    rng = np.random.default_rng(seed + 1)
+    b.q = torch.from_numpy(rng.integers(-1, 2, b.q.shape)).bfloat16()
+    b.k = torch.from_numpy(rng.integers(-1, 2, b.k.shape)).bfloat16()
+    return b
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (16, 1, 128), (12, 4, 64), (11, 1, 64)])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("lens,keep", [([700], 40), ([3, 60, 200], 12)])
+def test_weights_of_two_parts(lib, hq, hkv, d, block, lens, keep):
+    """Two bf16 parts: the first is off by less than 2^-7 of a weight, the second
+    by 2^-8 of that: 2^-15. A score's product with the scale and its difference
+    to the reference are off by 3 half steps (2^-24) of at most twice the largest
+    sum |q k|, the exponential by 2 steps of 2^-23, and that of numerator and
+    denominator both. A product of 16 tokens may lose a step of 2^-22 of the sums
+    that it adds to, n / 16 of them and 16 for the joins. The output is rounded
+    once: 2^-8."""
+    b = whole_scores(40, lens, keep, hq, hkv, d, block)
+    got = b.call(lib).double().cpu().numpy()
+    assert lib.pa_get_status() == 0
+    out, weighted, largest = b.oracle()
+    es = 3 * 2.0 ** -24 * 2 * largest[..., None] + 2.0 ** -22
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -15 + 2 * es + (max(lens) / 16 + 16) * 2.0 ** -22) * weighted
+    over = np.abs(got - out) / (tol + 1e-30)
+    assert over.max() <= 1.0, f"{over.max():.2f} times the tolerance, {(over > 1).mean():.1%} of the outputs"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_infinite_values_keep_their_sign(lib, d, value):
+    """A weight above 0 times an infinity is that infinity, whatever the weight:
+    all alike (each exactly 1), and of every size down to 2^-40."""
+    for alike in (True, False):
+        b = whole_scores(41, [160], 10, 8, 1, d, 16)
+        b.q[:] = 1.0
+        b.k[:] = 0.0
+        if not alike:
+            b.scale = 0.6931471805599453 / 4
+            for i in range(10):
+                for t in range(16):
+                    b.k[b.table[0, i], 0, t, 0] = -float(i * 16 + t)  # weights 2^-(n / 4)
+        for n in range(d):
+            b.v[b.table[0, n % 10], 0, n // 8 % 16, n] = value  # a row's own in every dimension
+        out = b.call(lib).float().cpu()
+        assert (out == value).all(), alike
