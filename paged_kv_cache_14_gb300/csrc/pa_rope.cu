@@ -643,7 +643,7 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
       stretched = 1.0 - std::min(1.0, std::max(0.0, (original_len * f / kTwoPi - low) / (high - low)));
     if (scaling == PA_ROPE_RAMP)
       stretched = std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 0.001)));
-    f = (1.0 - stretched) * f + stretched * f / factor;
+    if (scaling >= PA_ROPE_BANDS) f = (1.0 - stretched) * f + stretched * f / factor;
     if (!std::isfinite(f)) return PA_ERR_ARG;  // (a factor that leaves the doubles' range)
     double turns = f / kTwoPi;
     turns -= std::floor(turns);

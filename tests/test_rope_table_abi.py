@@ -1,0 +1,22 @@
+"""Host checks of the rotary table (no GPU needed): what a scaling does not read
+cannot refuse a call."""
+from __future__ import annotations
+
+import pytest
+
+import paged_kv_cache_14_gb300 as pa
+
+NAN = float("nan")
+
+
+def table(positions=0, rot=128, base=1e4, kind=0, factor=1.0, orig=0, low=1.0, high=4.0, amplitude=1.0, out=0x1000):
+    """A call that passes every check launches nothing: it asks for no positions."""
+    return pa.load().pa_rope_table(out, 0, positions, rot, base, kind, factor, orig, low, high, amplitude, None)
+
+
+@pytest.mark.parametrize("factor", [0.0, -1.0, NAN, float("inf")])
+def test_plain_table_reads_no_factor(factor):
+    assert table(kind=0, factor=factor) == 0
+    assert table(kind=0, factor=factor, low=NAN, high=NAN, orig=-1) == 0
+    for kind in (1, 2, 3, 4):  # the others do
+        assert table(kind=kind, factor=factor, orig=1) == -1
