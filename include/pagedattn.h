@@ -773,7 +773,7 @@ int pa_compact_tree_e5m2(void* const* k_caches, void* const* v_caches, float* co
  * an entry of amplitude 1 is within 2^-22 of the cosine or sine. Positions lie
  * below 2^31; rot_dim is even, 2 to 256 (PA_ERR_UNSUPPORTED); base > 1, factor
  * > 0 (not read by PA_ROPE_NONE), 0 < low < high and original_len >= 1 (read by
- * PA_ROPE_BANDS and PA_ROPE_RAMP only), amplitude and every frequency finite
+ * PA_ROPE_BANDS and PA_ROPE_RAMP only), amplitude (in fp32) and every frequency finite
  * (PA_ERR_ARG).
  */
 int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions, int32_t rot_dim, double base,

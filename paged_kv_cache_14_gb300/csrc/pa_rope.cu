@@ -6,6 +6,7 @@
 // Every product, sum and difference is one IEEE fp32 operation (no fused
 // multiply-add), so results can be reproduced bit for bit from the table.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -621,7 +622,7 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
       first_position + num_positions > (1ll << 31))
     return PA_ERR_ARG;
   if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > kRopeMaxDim) return PA_ERR_UNSUPPORTED;
-  if (!(base > 1.0) || !std::isfinite(base) || !std::isfinite(amplitude)) return PA_ERR_ARG;
+  if (!(base > 1.0) || !std::isfinite(base) || !(std::fabs(amplitude) <= FLT_MAX)) return PA_ERR_ARG;
   if (scaling < PA_ROPE_NONE || scaling > PA_ROPE_RAMP) return PA_ERR_ARG;
   if (scaling != PA_ROPE_NONE && (!(factor > 0.0) || !std::isfinite(factor))) return PA_ERR_ARG;
   if ((scaling == PA_ROPE_BANDS || scaling == PA_ROPE_RAMP) &&

@@ -20,3 +20,15 @@ def test_plain_table_reads_no_factor(factor):
     assert table(kind=0, factor=factor, low=NAN, high=NAN, orig=-1) == 0
     for kind in (1, 2, 3, 4):  # the others do
         assert table(kind=kind, factor=factor, orig=1) == -1
+
+
+@pytest.mark.parametrize("amplitude", [1e300, -1e300, 3.5e38, float("inf"), NAN])
+def test_amplitude_is_finite_in_fp32(amplitude):
+    """The entries are fp32: an amplitude beyond its range would be infinite."""
+    assert table(amplitude=amplitude) == -1
+
+
+def test_largest_amplitudes():
+    top = float((2 - 2 ** -23) * 2.0 ** 127)
+    for amplitude in (top, -top, 1e-300, 0.0):
+        assert table(amplitude=amplitude) == 0
