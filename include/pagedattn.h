@@ -769,8 +769,9 @@ int pa_compact_tree_e5m2(void* const* k_caches, void* const* v_caches, float* co
  *   cos_sin : float [num_positions][rot_dim] (output), 16-byte aligned; row
  *             p holds amplitude cos(a_i) at [i] and amplitude sin(a_i) at
  *             [rot_dim/2 + i], a_i = (first_position + p) f_i
- * Angles are reduced in 64-bit fixed point from frequencies held in 64 bits:
- * an entry of amplitude 1 is within 2^-22 of the cosine or sine. Positions lie
+ * Frequencies are computed in twice the doubles' precision and angles reduced
+ * in 64-bit fixed point: an entry of amplitude 1 is within 2^-22 of the cosine
+ * or sine, at frequencies of up to 2^24 radians a position. Positions lie
  * below 2^31; rot_dim is even, 2 to 256 (PA_ERR_UNSUPPORTED); base > 1, factor
  * > 0 (not read by PA_ROPE_NONE), 0 < low < high and original_len >= 1 (read by
  * PA_ROPE_BANDS and PA_ROPE_RAMP only), amplitude (in fp32) and every frequency finite

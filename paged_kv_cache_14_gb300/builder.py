@@ -20,7 +20,10 @@ SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_prefill.cu", "pa_casc
            "pa_selftest.cu", "pa_tree.cu", "pa_tree_tc.cu",
            "pa_verify.cu", "pa_compact.cu", "pa_rope.cu", "pa_select.cu", "pa_sparse.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# (Host arithmetic as it is written: products and sums that a compiler fuses on
+# one machine and not on another would differ in their last bits.)
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
+          "-Xcompiler", "-ffp-contract=off",
           "--expt-relaxed-constexpr", "-Xptxas", "-v"]
 
 

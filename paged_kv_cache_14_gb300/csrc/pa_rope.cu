@@ -517,6 +517,49 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Numbers of some 104 bits as sums of two doubles (Dekker, "A floating-point
+// technique for extending the available precision", 1971), with the fused
+// multiply-add for a product's remainder. A frequency of 53 bits is off by
+// 2^-22 of a radian at position 2^31, as far as an entry may be.
+struct Twice {
+  double hi, lo;
+};
+Twice plus(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Twice operator+(Twice a, Twice b) {
+  const Twice s = plus(a.hi, b.hi);
+  return plus(s.hi, s.lo + (a.lo + b.lo));
+}
+Twice operator-(Twice a, Twice b) { return a + Twice{-b.hi, -b.lo}; }
+Twice operator*(Twice a, Twice b) {
+  const double p = a.hi * b.hi;
+  return plus(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Twice operator/(Twice a, Twice b) {
+  const double q = a.hi / b.hi;
+  const Twice rest = a - b * Twice{q, 0.0};
+  return plus(q, rest.hi / b.hi);
+}
+// x^(-1/n), by Newton's steps from the double.
+Twice inverse_root(double x, int n) {
+  Twice r{std::pow(x, -1.0 / n), 0.0};
+  for (int step = 0; step < 2; ++step) {
+    Twice product{x, 0.0}, square = r;
+    for (int k = n; k; k >>= 1, square = square * square)
+      if (k & 1) product = product * square;
+    r = r + r * (Twice{1.0, 0.0} - product) / Twice{(double)n, 0.0};
+  }
+  return r;
+}
+// x without its whole part, in units of 2^-64.
+unsigned long long fraction(double x) {
+  const double part = std::fabs(x) - std::floor(std::fabs(x));
+  const unsigned long long units = (unsigned long long)(part * 18446744073709551616.0);
+  return x < 0 ? 0 - units : units;
+}
+
 template <typename T, int LAYOUT>
 int launch_rope(const RopeParams& p, int kv8, cudaStream_t stream) {
   if (!kv8) {
@@ -629,26 +672,38 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
       (original_len < 1 || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
     return PA_ERR_ARG;
   const double kTwoPi = 6.283185307179586476925;
+  const Twice one{1.0, 0.0}, per_turn{0.15915494309189535, -9.839338337591243e-18};  // 1, 1 / (2 pi)
+  const Twice per_factor = scaling == PA_ROPE_NONE ? one : one / Twice{factor, 0.0};
+  const Twice per_band = one / plus(high, -low), positions{(double)original_len, 0.0};
   const int half = rot_dim / 2;
-  if (scaling == PA_ROPE_BASE && rot_dim > 2) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  Twice ratio = half > 1 ? inverse_root(base, half) : one;  // from a frequency to the next
+  if (scaling == PA_ROPE_BASE && half > 1) {
+    // base * factor^(half / (half - 1)): factor's part of it is factor^(-1 / (half - 1)).
+    if (!(base * std::pow(factor, half / (half - 1.0)) > 0.0)) return PA_ERR_ARG;
+    ratio = ratio * inverse_root(factor, half - 1);
+  }
   auto pair_of = [&](double turns) {  // the pair that makes so many turns in original_len
     return rot_dim * std::log(original_len / (kTwoPi * turns)) / (2 * std::log(base));
   };
   const double first = std::max(std::floor(pair_of(high)), 0.0),
                last = std::min(std::ceil(pair_of(low)), rot_dim - 1.0);
+  const Twice per_pair = one / Twice{std::max(last - first, 0.001), 0.0};
   RopeSteps steps{};
-  for (int i = 0; i < half; ++i) {
-    double f = std::pow(base, -2.0 * i / rot_dim), stretched = 0.0;
-    if (scaling == PA_ROPE_LINEAR) f /= factor;
-    if (scaling == PA_ROPE_BANDS)
-      stretched = 1.0 - std::min(1.0, std::max(0.0, (original_len * f / kTwoPi - low) / (high - low)));
-    if (scaling == PA_ROPE_RAMP)
-      stretched = std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 0.001)));
-    if (scaling >= PA_ROPE_BANDS) f = (1.0 - stretched) * f + stretched * f / factor;
-    if (!std::isfinite(f)) return PA_ERR_ARG;  // (a factor that leaves the doubles' range)
-    double turns = f / kTwoPi;
-    turns -= std::floor(turns);
-    steps.step[i] = turns >= 1.0 ? 0 : (unsigned long long)(turns * 18446744073709551616.0);
+  Twice plain = one;
+  for (int i = 0; i < half; ++i, plain = plain * ratio) {
+    Twice f = plain;
+    if (scaling == PA_ROPE_LINEAR) f = f * per_factor;
+    if (scaling >= PA_ROPE_BANDS) {
+      // The share of the frequency that the factor divides.
+      const Twice share = scaling == PA_ROPE_BANDS
+                              ? one - (f * per_turn * positions - Twice{low, 0.0}) * per_band
+                              : Twice{i - first, 0.0} * per_pair;
+      if ((one - share).hi <= 0.0) f = f * per_factor;
+      else if (share.hi > 0.0) f = (one - share) * f + share * f * per_factor;
+    }
+    if (!std::isfinite(f.hi)) return PA_ERR_ARG;  // (a factor that leaves the doubles' range)
+    const Twice turns = f * per_turn;
+    steps.step[i] = fraction(turns.hi) + fraction(turns.lo);
   }
   if (num_positions == 0) return PA_OK;
   if (!cos_sin) return PA_ERR_ARG;
