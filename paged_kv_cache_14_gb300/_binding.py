@@ -632,7 +632,8 @@ def _arg(t, name: str, dtype, dev: int, shape) -> int:
     _refuse(t, name, dtype, dev, shape)
 
 
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (None in a torch without CUDA, whose tensors no call gets as far as these with.)
+_device, _raw_stream = (getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
 
 def _place(t, name: str, stream) -> tuple[int, int, object]:
