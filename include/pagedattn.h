@@ -887,8 +887,9 @@ int pa_block_summaries_e5m2(const void* k_cache, const float* kv_scales, const i
  * negative length) records PA_ERR_SEQLEN and lists nothing; a block outside the
  * pool records PA_ERR_BLOCK_OOB and comes last. head_dim a multiple of 32 up
  * to 256, a GQA group of at most 128, num_seqs at most 65535, num_sink +
- * num_recent at most max_list_len (PA_ERR_ARG). A sequence may have some 400000
- * blocks (8 CTAs' shared memory holds their scores; the bound is the smaller of
+ * num_recent at most max_list_len (PA_ERR_ARG). A sequence may have 169984
+ * blocks in every shape, 378752 at head_dim 128 and up to 8 heads a group (8
+ * CTAs' shared memory holds their scores; the bound is the smaller of
  * max_seq_len and the table; PA_ERR_UNSUPPORTED).
  */
 int pa_select_blocks(const void* q, const int8_t* summaries, const float* summary_scales, const int32_t* block_tables,

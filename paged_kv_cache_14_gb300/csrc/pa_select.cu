@@ -782,6 +782,18 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Shared memory of a CTA of `warps` warps with `scores` scores, and the most that
+// it may be.
+int select_bytes(int d, int head_tiles, int warps, int scores) {
+  return select_ring_bytes(d, warps) + head_tiles * 8 * (select_query_bytes(d) + 4) + scores * 4;
+}
+constexpr int kSelectMostBytes = 220 * 1024;
+// Blocks whose scores the largest cluster holds.
+int64_t select_max_blocks(int d, int head_tiles) {
+  const int scores = (kSelectMostBytes - select_bytes(d, head_tiles, 4, 0)) / 4;
+  return (int64_t)kSelectMaxCluster * (scores / kSelectTile * kSelectTile);
+}
+
 template <int D>
 int launch_select(const SelectParams& p0, cudaStream_t stream) {
   SelectParams p = p0;
@@ -789,18 +801,16 @@ int launch_select(const SelectParams& p0, cudaStream_t stream) {
   const int blocks = (p.max_seq_len - 1) / p.block_size + 1;
   // CTAs of a row: of 128 blocks at least, or as many as shared memory takes to
   // hold the scores; then the warps of each so that all CTAs run at once.
-  const int sms = num_sms_current_device(), most = 220 * 1024;
+  const int sms = num_sms_current_device(), most = kSelectMostBytes;
   int ranks = cluster_ranks(rows, sms, blocks / 128);
   auto scores = [&] { return ((blocks + ranks - 1) / ranks + kSelectTile - 1) / kSelectTile * kSelectTile; };
-  const int queries = p.head_tiles * 8 * (select_query_bytes(D) + 4);
-  auto bytes = [&](int warps) { return select_ring_bytes(D, warps) + queries + scores() * 4; };
+  auto bytes = [&](int warps) { return select_bytes(D, p.head_tiles, warps, scores()); };
   while (ranks < kSelectMaxCluster && bytes(4) > most) ranks *= 2;
   const int64_t per_sm = (rows * ranks + sms - 1) / sms;
   int warps = (int)std::min<int64_t>(std::min(kSelectMaxWarps, scores() / kSelectTile), kSelectMaxWarps / per_sm);
   while (warps > 4 && bytes(warps) > most / std::min<int64_t>(per_sm, kSelectMaxWarps / 4)) --warps;
   warps = std::max(warps, 4);
   const int smem = bytes(warps);
-  if (smem > most) return PA_ERR_UNSUPPORTED;
   const bool one = p.head_tiles == 1;
   const auto kernel = ranks > 1 ? one ? select_kernel<D, true, true> : select_kernel<D, true, false>
                       : one    ? select_kernel<D, false, true>
@@ -950,6 +960,10 @@ int pa_select_blocks(const void* q, const int8_t* summaries, const float* summar
   if (head_dim < 32 || head_dim > 256 || head_dim % 32 || num_q_heads / num_kv_heads > 128) return PA_ERR_UNSUPPORTED;
   if (num_seqs > 65535 || num_kv_heads > (1 << 20) || (int64_t)num_seqs * num_kv_heads > (1 << 26))
     return PA_ERR_UNSUPPORTED;
+  const int head_tiles = (num_q_heads / num_kv_heads + 7) / 8;
+  // No sequence is longer than its table.
+  const int64_t longest = std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * block_size);
+  if ((longest - 1) / block_size + 1 > select_max_blocks(head_dim, head_tiles)) return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PA_OK;
   if (!q || !summaries || !summary_scales || !block_tables || !seq_lens || !block_lists || !list_lens)
     return PA_ERR_ARG;
@@ -966,8 +980,7 @@ int pa_select_blocks(const void* q, const int8_t* summaries, const float* summar
   p.list_lens = list_lens;
   p.max_blocks_per_seq = max_blocks_per_seq;
   p.num_seqs = num_seqs;
-  // No sequence is longer than its table.
-  p.max_seq_len = (int32_t)std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * block_size);
+  p.max_seq_len = (int32_t)longest;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
   p.num_blocks = num_blocks;
@@ -976,7 +989,7 @@ int pa_select_blocks(const void* q, const int8_t* summaries, const float* summar
   p.max_list_len = max_list_len;
   p.num_sink = num_sink;
   p.num_recent = num_recent;
-  p.head_tiles = (p.group + 7) / 8;
+  p.head_tiles = head_tiles;
   p.dtype = dtype;
   if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
