@@ -379,6 +379,14 @@ class SparseStep:
         self.max_list_len, self.num_sink, self.num_recent = int(max_list_len), int(num_sink), int(num_recent)
         self.scale, self.interleaved = float(scale), bool(interleaved)
         self.num_blocks, hkv, self.block_size, d = self.k_caches[0].shape
+        # (The cache is written at more head_dims than attend() takes.)
+        if kv_scales is not None:
+            attends = d == 128 and dtype in (torch.float16, torch.bfloat16)
+        else:
+            attends = d % 32 == 0 and 32 <= d <= 256 if dtype == torch.float32 else d in (64, 128)
+        if not attends:
+            raise ValueError(f"no attention over listed blocks at head_dim {d} with {dtype} queries over "
+                             f"{'8-bit' if kv_scales is not None else dtype} pools")
         total, n, dev = new_positions.shape[0], seq_lens.shape[0], seq_lens.device
         self.slot_mapping = torch.empty(total, dtype=torch.int64, device=dev)
         self.q = torch.zeros(total, num_q_heads, d, dtype=dtype, device=dev)
