@@ -356,17 +356,19 @@ class SparseStep:
     Then slots(), and for every layer write(), which rotates, caches and
     summarises, and attend(), one query token a sequence. A prompt's chunks go
     through slots() and write() in the same way, with pa_chunked_prefill for
-    their attention. Where a sequence's blocks change by other means (a copy on
-    write, a swap, a compacted draft tree), summarize() makes their summaries
-    again. scale is not negative (the blocks are chosen for the largest products
-    with q).
+    their attention. A step's sizes are fixed: another step over the same caches
+    takes this one's summaries and summary_scales (2 bytes a dimension of a block
+    and KV head, in every layer). Where a sequence's blocks change by other means
+    (a copy on write, a swap, a compacted draft tree), summarize() makes their
+    summaries again. scale is not negative (the blocks are chosen for the largest
+    products with q).
     """
 
     def __init__(self, *, k_caches, v_caches, block_tables: torch.Tensor, ctx_lens: torch.Tensor,
                  seq_lens: torch.Tensor, new_seq_ids: torch.Tensor, new_positions: torch.Tensor,
                  cos_sin: torch.Tensor, num_q_heads: int, dtype: torch.dtype, max_seq_len: int, max_new_tokens: int,
                  max_list_len: int, scale: float, num_sink: int = 1, num_recent: int = 1, interleaved: bool = False,
-                 kv_scales=None, kv_format: str = "e4m3"):
+                 kv_scales=None, kv_format: str = "e4m3", summaries=None, summary_scales=None):
         if kv_format not in ("e4m3", "e5m2"):
             raise ValueError(f"kv_format {kv_format!r}: e4m3 or e5m2")
         if not 0 <= scale < float("inf"):  # (the blocks are chosen for large scores of q as it is)
@@ -393,9 +395,18 @@ class SparseStep:
         self.out = torch.empty(n, num_q_heads, d, dtype=dtype, device=dev)
         self.block_lists = torch.empty(n, hkv, self.max_list_len, dtype=torch.int32, device=dev)
         self.list_lens = torch.empty(n, hkv, dtype=torch.int32, device=dev)
-        self.summaries = [torch.zeros(self.num_blocks, hkv, 2, d, dtype=torch.int8, device=dev)
-                          for _ in self.k_caches]
-        self.summary_scales = [torch.zeros(self.num_blocks, hkv, device=dev) for _ in self.k_caches]
+        layers, shape = len(self.k_caches), (self.num_blocks, hkv)
+        if summaries is None and summary_scales is None:
+            summaries = [torch.zeros(*shape, 2, d, dtype=torch.int8, device=dev) for _ in range(layers)]
+            summary_scales = [torch.zeros(shape, device=dev) for _ in range(layers)]
+        elif summaries is None or summary_scales is None:
+            raise ValueError("summaries and summary_scales go together")
+        self.summaries, self.summary_scales = list(summaries), list(summary_scales)
+        if (len(self.summaries) != layers or len(self.summary_scales) != layers or
+                any(x.shape != (*shape, 2, d) or x.dtype != torch.int8 for x in self.summaries) or
+                any(x.shape != shape or x.dtype != torch.float32 for x in self.summary_scales)):
+            raise ValueError(f"summaries: int8 {[*shape, 2, d]} and summary_scales: float32 {[*shape]} of {layers} "
+                             "layers")
 
     def pools(self, layer: int):
         k, v = self.k_caches[layer], self.v_caches[layer]

@@ -34,3 +34,23 @@ def test_shapes_that_attend_would_refuse(dtype, kv, d):
 def test_shapes(dtype, kv, d):
     step = make(d, dtype, kv)
     assert len(step.summaries) == 2 and step.summaries[0].shape == (4, 2, 2, d)
+
+
+def test_summaries_are_shared():
+    """Steps over the same caches (a prompt's chunks, then decode) use one set."""
+    prompt = make()
+    decode = make(summaries=prompt.summaries, summary_scales=prompt.summary_scales)
+    for layer in range(2):
+        assert decode.summaries[layer] is prompt.summaries[layer]
+        assert decode.summary_scales[layer] is prompt.summary_scales[layer]
+
+
+def test_summaries_that_do_not_fit():
+    step = make()
+    for over in (dict(summaries=step.summaries), dict(summary_scales=step.summary_scales),
+                 dict(summaries=step.summaries[:1], summary_scales=step.summary_scales[:1]),
+                 dict(summaries=[x[:3] for x in step.summaries], summary_scales=step.summary_scales),
+                 dict(summaries=step.summaries, summary_scales=[x[:, :1] for x in step.summary_scales]),
+                 dict(summaries=[x.float() for x in step.summaries], summary_scales=step.summary_scales)):
+        with pytest.raises(ValueError, match="summar"):
+            make(**over)
