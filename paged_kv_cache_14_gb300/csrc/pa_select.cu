@@ -870,12 +870,15 @@ int block_summaries(const void* k_cache, const float* kv_scales, const int32_t* 
   if ((int64_t)num_seqs * p.seq_blocks > INT32_MAX) return PA_ERR_UNSUPPORTED;
   p.items = (int64_t)num_seqs * p.seq_blocks * num_kv_heads;
   if ((p.status = device_status_ptr()) == nullptr) return PA_ERR_CUDA;
-  // Three CTAs an SM, with 64 KB of tiles each.
+  // Three CTAs an SM with 64 KB of tiles each, or one with 128 KB where a warp's
+  // two tiles take that (16-bit blocks of 32 rows of 128): as many as run at once,
+  // since they go on from tile to tile.
   const int tile = block_size * head_dim * (kv8 ? 1 : 2);
   p.stages = std::max(2, std::min(kSummaryMaxStages, 64 * 1024 / (kSummaryWarps * tile)));
   const int smem = kSummaryWarps * p.stages * tile;
+  const int resident = wide ? 8 : smem > 64 * 1024 ? 1 : 3;
   const unsigned n = (unsigned)std::min<int64_t>((p.items + kSummaryWarps - 1) / kSummaryWarps,
-                                                 (wide ? 8 : 3) * num_sms_current_device());
+                                                 resident * num_sms_current_device());
 #define PA_SUM_D(R, D, KV8)                                                                                  \
   {                                                                                                          \
     const auto kernel = summary_kernel<R, D, KV8>;                                                           \
