@@ -333,18 +333,20 @@ __device__ __forceinline__ void copy_async_wait() {  // for all groups but the l
 // within one, and from there another such step gives the rounded quotient,
 // unless the divisor's significand is all ones (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990). That
-// holds while nothing overflows or loses bits below the normal numbers, which a
-// divisor from 2^-80 to 1 sees to for the uses here (quotients of at most 2^16
-// in size, of which those below 2^-40 matter by their sign alone). Other
-// divisors go through the division itself. (Summaries of 190000 tokens: 95 us
-// with divisions, 76 us so.)
+// holds while nothing overflows and remainders are exact, which they are for
+// divisors from 2^-63 to 1 and quotients from 2^-40 to 2^16 in size: the last
+// place of their product is 2^-23 2^-63 2^-23 2^-40 = 2^-149 or above, fp32's
+// smallest step. Of smaller quotients the uses here need the sign alone, and a
+// remainder that is off by half of that step moves none past 0 (it is 2^-149 by
+// the divisor at least). Other divisors go through the division itself.
+// (Summaries of 190000 tokens: 95 us with divisions, 76 us so.)
 struct Divisor {
   float by, inv;
   bool quick;
 };
 __device__ __forceinline__ Divisor divisor(float s) {
   return Divisor{s, __fdiv_rn(1.f, s),
-                 s >= 8.27180613e-25f && s <= 1.f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu};
+                 s >= 1.08420217e-19f && s <= 1.f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu};
 }
 __device__ __forceinline__ float quotient(float x, const Divisor& d) {
   if (!d.quick) return __fdiv_rn(x, d.by);
