@@ -761,7 +761,9 @@ int pa_compact_tree_e5m2(void* const* k_caches, void* const* v_caches, float* co
 #define PA_ROPE_RAMP 4   /* by pair: with d(t) = rot_dim ln(original_len / (2 pi t)) / (2 ln base),
                           * a = max(floor(d(high)), 0), z = min(ceil(d(low)), rot_dim - 1) and
                           * w = (i - a) / max(z - a, 0.001) held to [0, 1],
-                          * (1 - w) f_i + w f_i / factor */
+                          * (1 - w) f_i + w f_i / factor; models with such
+                          * frequencies commonly turn with an amplitude of
+                          * 0.1 ln(factor) + 1, which the caller passes */
 
 /*
  * pa_rope_table - cosines and sines of positions first_position ..

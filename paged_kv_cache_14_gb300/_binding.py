@@ -882,7 +882,8 @@ def pa_rope_table(num_positions: int, rot_dim: int, base: float = 10000.0, scali
                   stream=None) -> torch.Tensor:
     """Cosines and sines of positions: float32 [num_positions, rot_dim] on the
     current device. scaling: "none", "linear", "base", "bands" (high defaults
-    to 4 turns) or "ramp" (to 32)."""
+    to 4 turns) or "ramp" (to 32; models that use it commonly want amplitude
+    0.1 * ln(factor) + 1, which is not the default)."""
     kind = ROPE_SCALINGS.get(scaling)
     if kind is None:
         raise ValueError(f"scaling {scaling!r}: one of {', '.join(ROPE_SCALINGS)}")
