@@ -49,8 +49,8 @@ __device__ __forceinline__ void turn(uint32_t p, unsigned long long step, float&
 
 // A thread keeps N pairs (4 where the halves are whole float4) and goes from
 // position to position. Bound by instruction issue, about as long as the
-// stores take: 131072 positions of 128 (67 MB) in 12.5 us, 5.3 TB/s, where a
-// fill of the same memory takes 12.3.
+// stores take: 131072 positions of 128 (67 MB) in 11.3 us of a graph's replay, 5.9
+// TB/s, where a fill of the same memory takes 10.2; a call by itself 13.7.
 template <int N>
 __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(float* __restrict__ out, uint32_t first,
                                                                    uint32_t positions, int32_t half, float amplitude,
@@ -193,8 +193,10 @@ __device__ __forceinline__ T* rope_target(const RopeParams& p, int64_t t, int64_
 // in place, because the thread that writes an element is the one that reads it.
 //
 // Bound by HBM: 13504 tokens of 64 + 8 + 8 heads (fp16, half of each head, side
-// by side) in 92 us, 6.0 TB/s read and written; 12000 tokens of 32 + 8 + 8
-// (bf16 halves) in 57, 5.9 TB/s. More rows in flight need registers that warps
+// by side) in 92 us, 6.0 TB/s read and written; of 32 + 8 + 8 (bf16 halves) in
+// 57, 6.0 TB/s; 12000 of 32 + 8 + 8 fp32 rows in 88, 6.8 TB/s. Halves that are no
+// whole vectors take an element a thread: 12000 such tokens (bf16, 90 of 128
+// dimensions) 164, 1.8 TB/s. More rows in flight need registers that warps
 // would have (halves: 2, 3, 4 rows 62, 57, 67 us; pairs: 4, 5 rows 94, 92).
 constexpr int rope_batch(int layout) { return layout == kRopePairs ? 5 : 3; }
 
@@ -498,9 +500,11 @@ __device__ __forceinline__ void rope_cache_8bit(const RopeParams& p, bool inter,
 
 // The caches' CTAs come first: they take longer than the queries'. 64 registers
 // (8 CTAs an SM) for what is a chain of loads: 256 tokens of 64 + 8 + 8 heads,
-// each in a block under way, take 7 us (10 with 96), 6100 prompt tokens 70 (88),
-// of which the rows of the 8-bit caches are two thirds: rotated and encoded
-// one by one, a block of 16 a warp, bound by instruction issue.
+// each in a block under way, take 7 us (10 with 96), 6100 prompt tokens 74 (88),
+// of which the rows of the 8-bit caches are two thirds: a block of 16 a warp, two
+// rows in flight, read, rotated and looked up once for the largest value and once
+// more to be encoded. (Half of the variants spill 36 to 80 bytes to get by with 64
+// registers.) A chunk of 32 tokens is that chain alone, 18 us.
 template <typename T, int VEC, bool E5, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_8bit_kernel(const __grid_constant__ RopeParams p) {
   if (blockIdx.x < p.cache_ctas) {
