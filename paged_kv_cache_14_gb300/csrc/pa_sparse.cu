@@ -88,12 +88,33 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   return d;
 }
 
-// The largest bf16 below a weight (0 of 0). What is left of a weight is above 0
-// then, as the weight is, so that both parts' products with an infinity are that
-// infinity (of weights below 2^-109 the rest may be rounded to 0).
-__device__ __forceinline__ float below(float e) {
-  return __int_as_float((max(__float_as_int(e), 1) - 1) & 0xffff0000);
-}
+// A pair of weights in two parts: the largest numbers of the type below them (0
+// of 0), and what is left, times kUp. Above 0 as the weight is, what is left
+// makes of an infinite value the same infinity. (But of weights below 2^-109 in
+// bf16 and 2^-14 in fp16 the rest may be rounded to 0, and a value's infinity to
+// a NaN.) In fp16 the rest of a weight below 2^8 is at most 2^-2, which leaves
+// room for 2^14: it keeps what would lie below fp16's numbers.
+__device__ __forceinline__ float next_below(float e) { return __int_as_float(max(__float_as_int(e), 1) - 1); }
+template <typename M>
+struct TwoParts;
+template <>
+struct TwoParts<__nv_bfloat16> {
+  static constexpr float kUp = 1.f;
+  __device__ __forceinline__ static void split(float x, float y, uint32_t& first, uint32_t& rest) {
+    const uint32_t a = __float_as_uint(next_below(x)), b = __float_as_uint(next_below(y));
+    first = __byte_perm(a, b, 0x7632);
+    rest = MmaOp<__nv_bfloat16>::pack(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+  }
+};
+template <>
+struct TwoParts<__half> {
+  static constexpr float kUp = 16384.f;
+  __device__ __forceinline__ static void split(float x, float y, uint32_t& first, uint32_t& rest) {
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(first) : "f"(next_below(y)), "f"(next_below(x)));
+    const float2 held = __half22float2(*reinterpret_cast<const __half2*>(&first));
+    rest = MmaOp<__half>::pack((x - held.x) * kUp, (y - held.y) * kUp);
+  }
+};
 
 // The cluster's row: its sequence, KV head and query heads, and its list.
 struct SparseRow {
@@ -219,7 +240,9 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
   constexpr int VP = KV8 ? D / 128 : D / 64;  // 16-byte pieces of a V row for a lane
   constexpr int MT = D / 16;                  // tiles of 16 output dimensions
   constexpr int KS = D / 16;                  // steps of the score product
-  constexpr bool kTwoParts = std::is_same<M, __nv_bfloat16>::value;  // of a weight
+  // Weights in two parts where one of the products' type would be no more exact
+  // than the output's: all but fp16 weights for bf16 outputs.
+  constexpr bool kTwoParts = std::is_same<M, T>::value;
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' tiles, later their outputs
   float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
   __shared__ float sm[kSparseMaxWarps][H], sl[kSparseMaxWarps][H], cta_m[H], cta_l[H];
@@ -401,8 +424,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
           }
         }
       }
-      // Weights in the products' type (their sums are taken before): rounded to
-      // fp16, 2^-11 of a weight, or, since bf16 would lose 2^-8, as two bf16.
+      // Weights in the products' type (their sums are taken before).
       uint32_t pf[NT][2], rest[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -416,9 +438,9 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if constexpr (kTwoParts) {
-            const float a = below(e[2 * i]), b = below(e[2 * i + 1]);
-            pf[n][i] = transposed(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632));
-            rest[n][i] = transposed(MmaOp<M>::pack(e[2 * i] - a, e[2 * i + 1] - b));
+            TwoParts<M>::split(e[2 * i], e[2 * i + 1], pf[n][i], rest[n][i]);
+            pf[n][i] = transposed(pf[n][i]);
+            rest[n][i] = transposed(rest[n][i]);
           } else {
             pf[n][i] = transposed(MmaOp<M>::pack(e[2 * i], e[2 * i + 1]));
           }
@@ -451,14 +473,24 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
                                __byte_perm(v[2][e1 / 2], v[3][e1 / 2], e1 & 1 ? 0x7632 : 0x5410)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          constexpr bool kScaled = kTwoParts && TwoParts<M>::kUp != 1.f;
+          float left[4] = {0.f, 0.f, 0.f, 0.f};  // the rests' product, times kUp
+          if constexpr (kScaled) MmaOp<M>::run(left, a, rest[n][0], rest[n][1]);
           if constexpr (KV8 == 0) {
             MmaOp<M>::run(o[n][t], a, pf[n][0], pf[n][1]);
-            if constexpr (kTwoParts) MmaOp<M>::run(o[n][t], a, rest[n][0], rest[n][1]);
+            if constexpr (kTwoParts && !kScaled) MmaOp<M>::run(o[n][t], a, rest[n][0], rest[n][1]);
+            if constexpr (kScaled) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[n][t][i] = fmaf(left[i], 1.f / TwoParts<M>::kUp, o[n][t][i]);
+            }
           } else {
             float part[4] = {0.f, 0.f, 0.f, 0.f};
             MmaOp<M>::run(part, a, pf[n][0], pf[n][1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][t][i] = fmaf(v_scale, part[i], o[n][t][i]);
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kScaled) part[i] = fmaf(left[i], 1.f / TwoParts<M>::kUp, part[i]);
+              o[n][t][i] = fmaf(v_scale, part[i], o[n][t][i]);
+            }
           }
         }
       }

@@ -59,3 +59,63 @@ def test_infinite_values_keep_their_sign(lib, d, value):
             b.v[b.table[0, n % 10], 0, n // 8 % 16, n] = value  # a row's own in every dimension
         out = b.call(lib).float().cpu()
         assert (out == value).all(), alike
+
+
+def whole_scores_f16(seed, lens, keep, hq, hkv, d, block, kv):
+    """The same in fp16, over fp16 pools or (K codes of -1, 0 and 1, K scales 1) 8-bit ones."""
+    b = sparse_batch(seed, "f16", lens, keep, hq, hkv, d, block, kv, ragged=False, scale=1 / 16)
+    rng = np.random.default_rng(seed + 1)
+    b.q = torch.from_numpy(rng.integers(-1, 2, b.q.shape)).half()
+    k = torch.from_numpy(rng.integers(-1, 2, b.k.shape))
+    if kv is None:
+        b.k = k.half()
+    else:
+        one = {"e4m3": 0x38, "e5m2": 0x3C}[kv]
+        b.k = torch.where(k == 0, 0, torch.where(k > 0, one, one | 0x80)).to(torch.uint8)
+        b.scales[..., 0] = 1.0
+        assert np.array_equal(b.stored()[0], k.double().numpy())
+    return b
+
+
+@pytest.mark.parametrize("kv,hq,hkv,d", [(None, 8, 1, 128), (None, 16, 1, 128), (None, 12, 4, 64), (None, 11, 1, 64),
+                                         ("e4m3", 8, 1, 128), ("e5m2", 12, 1, 128)])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("lens,keep", [([700], 40), ([3, 60, 200], 12)])
+def test_weights_of_two_fp16_parts(lib, kv, hq, hkv, d, block, lens, keep):
+    """The first part is off by less than 2^-10 of a weight, the second by 2^-11 of
+    that: 2^-21; weights below fp16's numbers by 2^-39 (times the largest value, a
+    token). Scores, exponentials and sums as above, an 8-bit block's product once
+    more by its V scale (half a step of 2^-23); the output's rounding is 2^-11, or
+    2^-25 below fp16's normal numbers."""
+    b = whole_scores_f16(42, lens, keep, hq, hkv, d, block, kv)
+    got = b.call(lib).double().cpu().numpy()
+    assert lib.pa_get_status() == 0
+    out, weighted, largest = b.oracle()
+    es = 3 * 2.0 ** -24 * 2 * largest[..., None] + 2.0 ** -22
+    top = float(np.abs(np.asarray(b.stored()[1], np.float64)).max())
+    sums = (max(lens) / 16 + 16) * 2.0 ** -22 + 2.0 ** -24
+    tol = (2.0 ** -11 * np.abs(out) + 2.0 ** -25 + (2.0 ** -21 + 2 * es + sums) * weighted +
+           max(lens) * 2.0 ** -39 * top)
+    over = np.abs(got - out) / tol
+    assert over.max() <= 1.0, f"{over.max():.2f} times the tolerance, {(over > 1).mean():.1%} of the outputs"
+
+
+@pytest.mark.parametrize("kv,d", [(None, 64), (None, 128), ("e5m2", 128)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_infinite_fp16_values_keep_their_sign(lib, kv, d, value):
+    """Weights of exactly 1, and of sizes down to 2^-13 (below 2^-14 a weight is no
+    normal fp16 number)."""
+    for alike in (True, False):
+        b = whole_scores_f16(43, [160], 10, 8, 1, d, 16, kv)
+        b.q[:] = 1.0
+        b.k[:] = 0
+        if not alike:
+            b.scale = 0.6931471805599453 / 4
+            for i in range(10):
+                for t in range(16):
+                    n = (i * 16 + t) % 53  # weights 2^-(n / 4), as so many dimensions of -1
+                    b.k[b.table[0, i], 0, t, :n] = -1.0 if kv is None else 0xBC
+        for n in range(d):
+            b.v[b.table[0, n % 10], 0, n // 8 % 16, n] = value if kv is None else 0x7C if value > 0 else 0xFC
+        out = b.call(lib).float().cpu()
+        assert (out == value).all(), alike
