@@ -914,10 +914,10 @@ int pa_select_blocks(const void* q, const int8_t* summaries, const float* summar
  * longer than its table PA_ERR_SEQLEN: the rows concerned are unspecified.
  * num_seqs at most 65535, max_list_len at most 2^26, a GQA group of at most
  * 128, any finite scale. fp16/bf16: head_dim 64 or 128; a softmax weight goes
- * into the second product rounded to fp16 (2^-11 of it) over fp16 and 8-bit
- * pools, as the sum of two bf16 (within 2^-15) over bf16 pools. fp32: head_dim
- * a multiple of 32 up to 256, exact fp32 arithmetic. Results do not depend on
- * the order in which the device runs.
+ * into the second product as the sum of two numbers of the 16-bit type (within
+ * 2^-15 of it for bf16, 2^-21 for fp16), over 8-bit pools with bf16 q rounded to
+ * fp16 (2^-11). fp32: head_dim a multiple of 32 up to 256, exact fp32 arithmetic.
+ * Results do not depend on the order in which the device runs.
  */
 int pa_decode_sparse(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                      int32_t max_blocks_per_seq, const int32_t* seq_lens, const int32_t* block_lists,

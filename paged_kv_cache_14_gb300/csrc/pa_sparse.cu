@@ -241,7 +241,9 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
   constexpr int MT = D / 16;                  // tiles of 16 output dimensions
   constexpr int KS = D / 16;                  // steps of the score product
   // Weights in two parts where one of the products' type would be no more exact
-  // than the output's: all but fp16 weights for bf16 outputs.
+  // than the output's: all but fp16 weights for bf16 outputs, which lose 2^-11 of
+  // the output's 2^-8 (two parts there: 8 sequences of 256 blocks, 64/8 heads, e4m3
+  // 17.7 -> 18.1 us, 32/2 heads 13.6 -> 15.1).
   constexpr bool kTwoParts = std::is_same<M, T>::value;
   extern __shared__ __align__(16) uint8_t smem[];  // the warps' tiles, later their outputs
   float(*so)[H][D] = reinterpret_cast<float(*)[H][D]>(smem);
