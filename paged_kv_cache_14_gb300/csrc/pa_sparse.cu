@@ -89,30 +89,32 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
 }
 
 // A pair of weights in two parts: the largest numbers of the type below them (0
-// of 0), and what is left, times kUp. Above 0 as the weight is, what is left
-// makes of an infinite value the same infinity. (But of weights below 2^-109 in
-// bf16 and 2^-14 in fp16 the rest may be rounded to 0, and a value's infinity to
-// a NaN.) In fp16 the rest of a weight below 2^8 is at most 2^-2, which leaves
-// room for 2^14: it keeps what would lie below fp16's numbers.
+// of 0), and what is left, times kUp, the type's smallest number at least. Both
+// are above 0 where the first is, so that they make of an infinite value the same
+// infinity. fp16 has room for few sizes: its weights are 2^kLift times as large (up
+// to 2^15 then, where what is left is at most 2^5), and so are their sums; the
+// smallest have a first part from 2^-31 on, and are off by 2^-41.
 __device__ __forceinline__ float next_below(float e) { return __int_as_float(max(__float_as_int(e), 1) - 1); }
 template <typename M>
 struct TwoParts;
 template <>
 struct TwoParts<__nv_bfloat16> {
-  static constexpr float kUp = 1.f;
+  static constexpr float kUp = 1.f, kLift = 0.f;
   __device__ __forceinline__ static void split(float x, float y, uint32_t& first, uint32_t& rest) {
     const uint32_t a = __float_as_uint(next_below(x)), b = __float_as_uint(next_below(y));
     first = __byte_perm(a, b, 0x7632);
     rest = MmaOp<__nv_bfloat16>::pack(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(rest) : "r"(0x00010001u));
   }
 };
 template <>
 struct TwoParts<__half> {
-  static constexpr float kUp = 16384.f;
+  static constexpr float kUp = 1024.f, kLift = 7.f;
   __device__ __forceinline__ static void split(float x, float y, uint32_t& first, uint32_t& rest) {
     asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(first) : "f"(next_below(y)), "f"(next_below(x)));
     const float2 held = __half22float2(*reinterpret_cast<const __half2*>(&first));
     rest = MmaOp<__half>::pack((x - held.x) * kUp, (y - held.y) * kUp);
+    asm("max.f16x2 %0, %0, %1;" : "+r"(rest) : "r"(0x00010001u));
   }
 };
 
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(NT == 1 ? 384 : 256) sparse_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float ref = m[n][i & 1];
-          e[i] = fast_exp2(s[n][i] - (ref == neg_inf() ? 0.f : ref));
+          e[i] = fast_exp2(s[n][i] - (ref == neg_inf() ? 0.f : ref - (kTwoParts ? TwoParts<M>::kLift : 0.f)));
           l[n][i & 1] += e[i];
         }
 #pragma unroll

@@ -119,3 +119,25 @@ def test_infinite_fp16_values_keep_their_sign(lib, kv, d, value):
             b.v[b.table[0, n % 10], 0, n // 8 % 16, n] = value if kv is None else 0x7C if value > 0 else 0xFC
         out = b.call(lib).float().cpu()
         assert (out == value).all(), alike
+
+
+@pytest.mark.parametrize("dtype,kv,least", [("bf16", None, 125), ("f16", None, 24.5), ("f16", "e5m2", 24.5)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_infinite_values_under_small_weights(lib, dtype, kv, least, value):
+    """One infinity a sequence, under a weight of 2^-least to 1: the output is that
+    infinity. (A bf16 has numbers down to 2^-126; fp16 ones end at 2^-24, half of
+    which a rounding still takes there.)"""
+    n, d = 200, 128
+    b = sparse_batch(44, dtype, [32] * n, 2, 4, 1, d, 16, kv, ragged=False, scale=0.6931471805599453 / 8)
+    b.q[:], b.k[:] = 0.0, 0
+    b.q[..., 0] = 8.0
+    where, size = np.arange(n) % 32, np.linspace(0.0, least, n)
+    for i in range(n):
+        one = b.table[i, where[i] // 16], 0, where[i] % 16
+        # The score's exponent of 2: a bf16 of up to 125 is off by 2^-2, a value that counts as it is.
+        b.k[one][0] = -float(size[i]) if kv is None else int(torch.tensor(-size[i]).to(torch.float8_e5m2).view(torch.uint8))
+        b.v[one][:] = value if kv is None else 0x7C if value > 0 else 0xFC
+    if kv:
+        b.scales[..., 0] = 1.0
+    out = b.call(lib).float().cpu()
+    assert (out == value).all(), np.unique(np.nonzero((out != value).any(-1).any(-1).numpy())[0])
