@@ -678,7 +678,8 @@ int pa_rope_table(float* cos_sin, int64_t first_position, int64_t num_positions,
   const double kTwoPi = 6.283185307179586476925;
   const Twice one{1.0, 0.0}, per_turn{0.15915494309189535, -9.839338337591243e-18};  // 1, 1 / (2 pi)
   const Twice per_factor = scaling == PA_ROPE_NONE ? one : one / Twice{factor, 0.0};
-  const Twice per_band = one / plus(high, -low), positions{(double)original_len, 0.0};
+  // (A band narrower than normal numbers is a step.)
+  const Twice per_band = one / plus(std::max(high, low + 1e-300), -low), positions{(double)original_len, 0.0};
   const int half = rot_dim / 2;
   Twice ratio = half > 1 ? inverse_root(base, half) : one;  // from a frequency to the next
   if (scaling == PA_ROPE_BASE && half > 1) {

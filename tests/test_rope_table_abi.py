@@ -32,3 +32,15 @@ def test_largest_amplitudes():
     top = float((2 - 2 ** -23) * 2.0 ** 127)
     for amplitude in (top, -top, 1e-300, 0.0):
         assert table(amplitude=amplitude) == 0
+
+
+def test_extreme_scalings():
+    """What leaves the doubles' range on the way without leaving it at the end."""
+    assert table(kind=1, factor=1.7e308) == 0 and table(kind=2, factor=1.7e308) == 0
+    assert table(kind=3, factor=1e308, orig=8192) == 0 and table(kind=4, factor=1e308, orig=8192, high=32.0) == 0
+    assert table(kind=3, factor=4.0, orig=2 ** 31 - 1, low=1e-300, high=1.7e308) == 0
+    assert table(kind=3, factor=4.0, orig=1, low=1e-310, high=2e-310) == 0  # a band of no width in normal numbers
+    assert table(kind=3, factor=1e-310, orig=2 ** 31 - 1, low=1e-310, high=2e-310) == 0  # (every pair above it)
+    assert table(kind=4, factor=4.0, orig=1, low=1e-300, high=1.7e308) == 0
+    assert table(base=1.7e308) == 0 and table(base=1.0 + 2 ** -52) == 0
+    assert table(rot=4, base=1.7e308, kind=2, factor=1e300) == 0
